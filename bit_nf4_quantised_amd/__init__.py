@@ -11,7 +11,9 @@ Operations ("QLoRA, explained", pofe.ai): blockwise absmax NF4 quantisation with
 byte, double quantisation of the scales to E4M3, two-level dequantisation to bf16, and the adapted
 linear's forward y = x W~^T + s x A^T B^T and backward (dX, dA, dB; no gradient for W), the
 adapter merged into the base for serving, and the adapter update of a training step (global
-gradient-norm clipping, then AdamW over A and B).
+gradient-norm clipping, then AdamW over A and B). Around the linears: root-mean-square norm with the
+residual's addition, attention over packed sequences or a key/value cache, both with their backward
+passes, and 8-bit activation checkpoints that the linears' backward reads.
 """
 from __future__ import annotations
 
@@ -49,6 +51,23 @@ class CAdamWConfig(ctypes.Structure):
                 ("max_grad_norm", ctypes.c_float)]
 
 
+class CAct8(ctypes.Structure):
+    """Mirror of ``qlora_act8`` in include/qlora_nf4.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p)]
+
+
+class CAttnConfig(ctypes.Structure):
+    """Mirror of ``qlora_attn_config`` in include/qlora_nf4.h."""
+    _fields_ = [("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("window", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("q_tokens", ctypes.c_int64), ("k_tokens", ctypes.c_int64)]
+
+
+class CAttnTensor(ctypes.Structure):
+    """Mirror of ``qlora_attn_tensor`` in include/qlora_nf4.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 _p, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 _W = ctypes.POINTER(CNF4Weight)
 _SIGS = {
@@ -78,6 +97,17 @@ _SIGS = {
     "qlora_workspace_bytes_group": (_sz, [_i32, _p, _i64, _i64, _i32]),
     "qlora_linear_bwd_group": (ctypes.c_int, [_i32, _p, _p, _p, _i64, _p, _p, _i32, _f32, _p, _p, _p, _p,
                                               ctypes.c_int, _p, _sz, _p]),
+    "qlora_act8_pack": (ctypes.c_int, [_p, _i64, _p, _p, _p]),
+    "qlora_act8_unpack": (ctypes.c_int, [_p, _p, _i64, _p, _p]),
+    "qlora_linear_bwd_act8": (ctypes.c_int, [_i32, _p, _p, _p, _i64, _p, _p, _i32, _f32, _p, _p, _p, _p,
+                                             ctypes.c_int, _p, _sz, _p]),
+    "qlora_workspace_bytes_act8": (_sz, [_i32, _p, _i64, _i64, _i32]),
+    "qlora_rmsnorm_fwd": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _f32, _p, _p, _p, _p, _p]),
+    "qlora_rmsnorm_bwd": (ctypes.c_int, [_p, _p, _p, _p, _p, _i64, _i64, _p, _p, ctypes.c_int, _p, _sz, _p]),
+    "qlora_rmsnorm_workspace_bytes": (_sz, [_i64, _i64]),
+    "qlora_attn_fwd": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "qlora_attn_bwd": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "qlora_attn_workspace_bytes": (_sz, [_p, _i64, _p, ctypes.c_int]),
     "nf4_storage_bytes": (_i64, [_i64]),
     "nf4_codebook": (None, [ctypes.POINTER(ctypes.c_float)]),
     "nf4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -399,6 +429,223 @@ def qlora_linear_bwd(weight: NF4Weight, x, dy, A, B, scale: float, u, dx, dA, dB
            "qlora_linear_bwd")
 
 
+# ------------------------------------------------------------------------- 8-bit activation checkpoints
+@dataclass
+class Act8:
+    """An M x K activation in 8 bits: int8 codes and the bf16 absmax of every block of 64 along K; a
+    code stands for code * absmax / 127 (format in include/qlora_nf4.h)."""
+    codes: torch.Tensor    # int8 [M, K]
+    absmax: torch.Tensor   # bf16 [M, K/64]
+    M: int
+    K: int
+
+    def c_struct(self) -> CAct8:
+        _dtype(self.codes, torch.int8); _dtype(self.absmax, *_BF16)
+        if self.codes.numel() != self.M * self.K or self.absmax.numel() * 64 != self.M * self.K:
+            raise ValueError("codes must hold M*K values and absmax M*K/64")
+        return CAct8(_ptr(self.codes), _ptr(self.absmax))
+
+
+def empty_act8(M: int, K: int, device="cuda") -> Act8:
+    return Act8(torch.empty(M, K, dtype=torch.int8, device=device),
+                torch.empty(M, K // 64, dtype=torch.bfloat16, device=device), M, K)
+
+
+def qlora_act8_pack(x, act8: Act8, stream=None) -> None:
+    """The 8-bit checkpoint of a bf16 activation."""
+    _dtype(x, *_BF16)
+    if x.numel() != act8.M * act8.K:
+        raise ValueError("x must hold M*K values")
+    c = act8.c_struct()
+    _check(lib.qlora_act8_pack(_ptr(x), x.numel(), c.codes, c.absmax, _stream(stream)), "qlora_act8_pack")
+
+
+def qlora_act8_unpack(act8: Act8, out, stream=None) -> None:
+    """The values of an 8-bit checkpoint, in bf16."""
+    _dtype(out, *_BF16)
+    if out.numel() != act8.M * act8.K:
+        raise ValueError("out must hold M*K values")
+    c = act8.c_struct()
+    _check(lib.qlora_act8_unpack(c.codes, c.absmax, out.numel(), _ptr(out), _stream(stream)), "qlora_act8_unpack")
+
+
+def qlora_workspace_bytes_act8(M: int, N: list, K: int, r: int) -> int:
+    n = (ctypes.c_int64 * max(len(N), 1))(*[int(v) for v in N])
+    return int(lib.qlora_workspace_bytes_act8(len(N), n, M, K, r))
+
+
+def workspace_act8(M: int, N: list, K: int, r: int, device="cuda") -> torch.Tensor:
+    """A device workspace large enough for qlora_linear_bwd_act8 over weights of N rows."""
+    return torch.empty(max(qlora_workspace_bytes_act8(M, N, K, r), 256), dtype=torch.uint8, device=device)
+
+
+def qlora_linear_bwd_act8(weights: list, act8: Act8, dys: list, As: list, Bs: list, scale: float, us: list, dxs,
+                          dAs: list, dBs: list, accumulate: bool = False, ws=None, stream=None) -> None:
+    """Backward of the linears that share the input kept as act8: as qlora_linear_bwd_group, with dAs[i]
+    formed from the 8-bit codes; dxs None skips the input gradients."""
+    n = len(weights)
+    if not (len(dys) == len(As) == len(Bs) == len(us) == len(dAs) == len(dBs) == n) or n == 0 or \
+            (dxs is not None and len(dxs) != n):
+        raise ValueError("one dY, A, B, u, dA and dB (and dX) per weight, one weight at least")
+    M, K = act8.M, act8.K
+    r = As[0].shape[0]
+    for i, w in enumerate(weights):
+        for t in (dys[i], As[i], Bs[i]) + ((dxs[i],) if dxs is not None else ()):
+            _dtype(t, *_BF16)
+        for t in (us[i], dAs[i], dBs[i]):
+            _dtype(t, torch.float32)
+        if w.K != K or dys[i].shape != (M, w.N) or As[i].shape != (r, K) or Bs[i].shape != (w.N, r) \
+                or us[i].numel() != M * r or dAs[i].shape != (r, K) or dBs[i].shape != (w.N, r) \
+                or (dxs is not None and dxs[i].shape != (M, K)):
+            raise ValueError("shape mismatch")
+    if ws is None:
+        ws = workspace_act8(M, [w.N for w in weights], K, r, act8.codes.device)
+    cws = [w.c_struct() for w in weights]
+    x8 = act8.c_struct()
+    P = ctypes.c_void_p
+    arr = lambda ts: (P * n)(*[_ptr(t) for t in ts])  # noqa: E731
+    _check(lib.qlora_linear_bwd_act8(n, (P * n)(*[ctypes.addressof(c) for c in cws]), ctypes.byref(x8), arr(dys), M,
+                                     arr(As), arr(Bs), r, scale, arr(us), arr(dxs) if dxs is not None else None,
+                                     arr(dAs), arr(dBs), int(bool(accumulate)), _ptr(ws),
+                                     ws.numel() * ws.element_size(), _stream(stream)), "qlora_linear_bwd_act8")
+
+
+# ------------------------------------------------------------------------- norm
+def qlora_rmsnorm_fwd(x, weight, eps: float, y, residual=None, h=None, rstd=None, act8: Act8 | None = None,
+                      stream=None) -> None:
+    """h = x + residual, y = h * rsqrt(mean(h^2) + eps) * weight over the last dimension (M x K); h, rstd
+    and the 8-bit checkpoint of y (act8) are optional outputs."""
+    for t in (x, weight, y, residual, h):
+        _dtype(t, *_BF16)
+    _dtype(rstd, torch.float32)
+    if x.dim() != 2:
+        raise ValueError("x must be M x K")
+    M, K = x.shape
+    if weight.numel() != K or y.shape != x.shape or (residual is not None and residual.shape != x.shape) \
+            or (h is not None and h.shape != x.shape) or (rstd is not None and rstd.numel() != M) \
+            or (act8 is not None and (act8.M, act8.K) != (M, K)):
+        raise ValueError("shape mismatch")
+    c8 = None if act8 is None else act8.c_struct()
+    _check(lib.qlora_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(weight), M, K, eps, _ptr(h), _ptr(y), _ptr(rstd),
+                                 None if c8 is None else ctypes.byref(c8), _stream(stream)), "qlora_rmsnorm_fwd")
+
+
+def qlora_rmsnorm_bwd(dy, h, weight, rstd, dx, dw=None, dh=None, accumulate: bool = False, ws=None,
+                      stream=None) -> None:
+    """Backward of qlora_rmsnorm_fwd from its h and rstd: dx (of x and of the residual alike; dh is what
+    flows into h itself) and, if given, dw (float32, added to with accumulate)."""
+    for t in (dy, h, weight, dx, dh):
+        _dtype(t, *_BF16)
+    for t in (rstd, dw):
+        _dtype(t, torch.float32)
+    if h.dim() != 2:
+        raise ValueError("h must be M x K")
+    M, K = h.shape
+    if dy.shape != h.shape or dx.shape != h.shape or weight.numel() != K or rstd.numel() != M \
+            or (dh is not None and dh.shape != h.shape) or (dw is not None and dw.numel() != K):
+        raise ValueError("shape mismatch")
+    if ws is None and dw is not None:
+        ws = torch.empty(max(int(lib.qlora_rmsnorm_workspace_bytes(M, K)), 256), dtype=torch.uint8, device=h.device)
+    _check(lib.qlora_rmsnorm_bwd(_ptr(dy), _ptr(dh), _ptr(h), _ptr(weight), _ptr(rstd), M, K, _ptr(dx), _ptr(dw),
+                                 int(bool(accumulate)), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                 _stream(stream)), "qlora_rmsnorm_bwd")
+
+
+# ------------------------------------------------------------------------- attention
+class AttnSeqs:
+    """The sequences of a batch for qlora_attn_fwd and qlora_attn_bwd, marshalled once (for all layers
+    of a step): entries (q0, nq, k0, nk), nq query tokens from q0 and nk key tokens from k0, with the
+    queries standing at the last nq key positions. causal hides later keys; window > 0 hides keys more
+    than window - 1 positions back."""
+
+    def __init__(self, seqs, causal: bool = True, window: int = 0):
+        flat = [int(v) for s in seqs for v in s]
+        if any(len(s) != 4 for s in seqs):
+            raise ValueError("a sequence is (q0, nq, k0, nk)")
+        self.count = len(flat) // 4
+        self.causal, self.window = bool(causal), int(window)
+        self._seqs = (ctypes.c_int64 * max(len(flat), 4))(*flat)
+
+    @staticmethod
+    def packed(lengths, causal: bool = True, window: int = 0) -> "AttnSeqs":
+        """A packed training batch: sequences of the given lengths one after another, each attending to
+        itself."""
+        seqs, at = [], 0
+        for n in lengths:
+            seqs.append((at, n, at, n))
+            at += n
+        return AttnSeqs(seqs, causal, window)
+
+    def _config(self, q, k, scale):
+        d = q.shape[2]
+        return CAttnConfig(q.shape[1], k.shape[1], d, int(self.causal), self.window,
+                           d ** -0.5 if scale is None else scale, q.shape[0], k.shape[0])
+
+    def workspace_bytes(self, q, k, backward: bool = False, scale: float | None = None) -> int:
+        cfg = self._config(q, k, scale)
+        return int(lib.qlora_attn_workspace_bytes(ctypes.byref(cfg), self.count, self._seqs, int(bool(backward))))
+
+
+def _attn_tensor(t, like=None) -> CAttnTensor:
+    """A [tokens, heads, d] tensor; tokens and heads may be strided, d contiguous."""
+    _dtype(t, *_BF16)
+    if not t.is_cuda:
+        raise ValueError("tensor must live on the GPU")
+    if t.dim() != 3 or t.stride(2) != 1 or (like is not None and t.shape != like.shape):
+        raise ValueError("shape mismatch: attention tensors are [tokens, heads, d] with d contiguous")
+    # a single token's or head's stride carries no meaning: give it a valid value
+    heads, d = t.shape[1], t.shape[2]
+    head = t.stride(1) if heads > 1 else d
+    token = t.stride(0) if t.shape[0] > 1 else max(d, head * (heads - 1) + d if head * heads < 1 << 22 else d)
+    return CAttnTensor(t.data_ptr(), token, head)
+
+
+def _lse_ok(lse, q):
+    _dtype(lse, torch.float32)
+    if lse is not None and lse.shape != (q.shape[1], q.shape[0]):
+        raise ValueError("lse must be [heads, query tokens]")
+
+
+def _attn_ws(seqs, cfg, backward, ws, device):
+    if ws is None:
+        need = int(lib.qlora_attn_workspace_bytes(ctypes.byref(cfg), seqs.count, seqs._seqs, backward))
+        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    return ws, 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def qlora_attn_fwd(seqs: AttnSeqs, q, k, v, o, lse=None, scale: float | None = None, ws=None, stream=None) -> None:
+    """Attention of seqs: q, o [query tokens, heads, d], k, v [key tokens, kv heads, d] (bf16, tokens and
+    heads may be strided); lse [heads, query tokens] float32 is needed by the backward. scale defaults
+    to d ** -0.5."""
+    tq, tk, tv, to = _attn_tensor(q), _attn_tensor(k), _attn_tensor(v, k), _attn_tensor(o, q)
+    if q.shape[2] != k.shape[2]:
+        raise ValueError("shape mismatch: q and k differ in head size")
+    _lse_ok(lse, q)
+    cfg = seqs._config(q, k, scale)
+    ws, nbytes = _attn_ws(seqs, cfg, 0, ws, q.device)
+    _check(lib.qlora_attn_fwd(ctypes.byref(cfg), seqs.count, seqs._seqs, ctypes.byref(tq), ctypes.byref(tk),
+                              ctypes.byref(tv), ctypes.byref(to), _ptr(lse), _ptr(ws), nbytes, _stream(stream)),
+           "qlora_attn_fwd")
+
+
+def qlora_attn_bwd(seqs: AttnSeqs, q, k, v, o, lse, dout, dq, dk, dv, scale: float | None = None, ws=None,
+                   stream=None) -> None:
+    """Backward of qlora_attn_fwd: dq, dk, dv from the gradient dout of o, recomputing the probabilities
+    from lse."""
+    ts = [_attn_tensor(q), _attn_tensor(k), _attn_tensor(v, k), _attn_tensor(o, q), _attn_tensor(dout, q),
+          _attn_tensor(dq, q), _attn_tensor(dk, k), _attn_tensor(dv, k)]
+    if q.shape[2] != k.shape[2]:
+        raise ValueError("shape mismatch: q and k differ in head size")
+    if lse is None:
+        raise ValueError("the backward needs lse")
+    _lse_ok(lse, q)
+    cfg = seqs._config(q, k, scale)
+    ws, nbytes = _attn_ws(seqs, cfg, 1, ws, q.device)
+    r = [ctypes.byref(t) for t in ts]
+    _check(lib.qlora_attn_bwd(ctypes.byref(cfg), seqs.count, seqs._seqs, r[0], r[1], r[2], r[3], _ptr(lse), r[4], r[5],
+                              r[6], r[7], _ptr(ws), nbytes, _stream(stream)), "qlora_attn_bwd")
+
+
 # ------------------------------------------------------------------------- format variants
 Q4_CODEBOOKS = {"nf4": 0, "fp4": 1, "int4": 2}
 
@@ -587,5 +834,8 @@ __all__ = ["lib", "LIB_PATH", "EXPORTED", "NF4Error", "NF4Weight", "CNF4Weight",
            "workspace_group",
            "qlora_linear_bwd", "qlora_merge", "AdamWConfig", "CAdamWConfig", "AdamWPlan",
            "Q4_CODEBOOKS", "q4_codebook_values", "q4_quantize", "q4_dequant",
+           "Act8", "CAct8", "empty_act8", "qlora_act8_pack", "qlora_act8_unpack", "qlora_linear_bwd_act8",
+           "qlora_workspace_bytes_act8", "workspace_act8", "qlora_rmsnorm_fwd", "qlora_rmsnorm_bwd",
+           "AttnSeqs", "CAttnConfig", "CAttnTensor", "qlora_attn_fwd", "qlora_attn_bwd",
            "qlora_workspace_bytes", "nf4_storage_bytes", "nf4_codebook", "workspace",
            "empty_weight", "quantize_weight"]

@@ -8,6 +8,7 @@
 #include <atomic>
 #include <mutex>
 #include <new>
+#include <vector>
 
 #include "common.h"
 #include "launch.h"
@@ -174,6 +175,13 @@ size_t bwd_group_ws(int count, const int64_t* N, int64_t M, int64_t K, int r) {
     if (x > part) part = x;
   }
   return (size_t)count * align_up((size_t)M * r * 4) + align_up(part * 4);
+}
+
+// as bwd_group_ws with the adapter gradients formed from an 8-bit checkpoint
+size_t bwd_act8_ws(int count, const int64_t* N, int64_t M, int64_t K, int r) {
+  const size_t rest = bwd_group_ws(count, N, M, K, r);
+  const size_t mine = (size_t)count * align_up((size_t)M * r * 4) + align_up(nf4::act8_grad_ws_floats(count, M, K, r) * 4);
+  return rest > mine ? rest : mine;
 }
 
 }  // namespace
@@ -387,10 +395,15 @@ size_t qlora_workspace_bytes_group(int32_t count, const int64_t* N, int64_t M, i
   return f > b ? f : b;
 }
 
-int qlora_linear_bwd_group(int32_t count, const nf4_weight* const* W, const uint16_t* x, const uint16_t* const* dy,
-                           int64_t M, const uint16_t* const* A, const uint16_t* const* B, int32_t r, float scale,
-                           const float* const* u, uint16_t* const* dx, float* const* dA, float* const* dB,
-                           int accumulate, void* ws, size_t ws_bytes, hipStream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// The grouped backward from the bf16 input x or, with x NULL, from its 8-bit checkpoint x8.
+int run_bwd_group(int32_t count, const nf4_weight* const* W, const uint16_t* x, const qlora_act8* x8,
+                  const uint16_t* const* dy, int64_t M, const uint16_t* const* A, const uint16_t* const* B, int32_t r,
+                  float scale, const float* const* u, uint16_t* const* dx, float* const* dA, float* const* dB,
+                  int accumulate, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (count < 1 || count > 4) return NF4_ERR_SHAPE;
   if (!W || !dy || !A || !B || !u || !dA || !dB) return NF4_ERR_NULL;
   int64_t N[4];
@@ -404,7 +417,9 @@ int qlora_linear_bwd_group(int32_t count, const nf4_weight* const* W, const uint
   }
   if ((st = check_rank(r))) return st;
   if (M == 0) return NF4_OK;
-  if (!x || !aligned16(x) || (ws && !aligned16(ws))) return !x ? NF4_ERR_NULL : NF4_ERR_ALIGN;
+  if (!x && !(x8 && x8->codes && x8->absmax)) return NF4_ERR_NULL;
+  if ((x ? !aligned16(x) : !aligned16(x8->codes) || !aligned16(x8->absmax)) || (ws && !aligned16(ws)))
+    return NF4_ERR_ALIGN;
   for (int i = 0; i < count; ++i) {
     if (!dy[i] || !A[i] || !B[i] || !u[i] || !dA[i] || !dB[i] || (dx && !dx[i])) return NF4_ERR_NULL;
     if (!aligned16(dy[i]) || !aligned16(A[i]) || !aligned16(B[i]) || !aligned16(u[i]) || !aligned16(dA[i]) ||
@@ -412,7 +427,7 @@ int qlora_linear_bwd_group(int32_t count, const nf4_weight* const* W, const uint
       return NF4_ERR_ALIGN;
   }
   const int64_t K = W[0]->K;
-  if (!ws || ws_bytes < bwd_group_ws(count, N, M, K, r)) return NF4_ERR_WORKSPACE;
+  if (!ws || ws_bytes < (x ? bwd_group_ws(count, N, M, K, r) : bwd_act8_ws(count, N, M, K, r))) return NF4_ERR_WORKSPACE;
   const size_t vslot = align_up((size_t)M * r * 4);
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + count * vslot);
   float* v[4];
@@ -447,10 +462,218 @@ int qlora_linear_bwd_group(int32_t count, const nf4_weight* const* W, const uint
           return NF4_ERR_HIP;
     }
   }
-  return nf4::launch_lora_dx_group(count, x, M, K, v, r, scale, accumulate, part, dA, stream) == hipSuccess
-             ? NF4_OK
-             : NF4_ERR_HIP;
+  if (x8)
+    return from_hip(nf4::launch_act8_grad(count, x8->codes, x8->absmax, M, K, v, r, scale, accumulate, part, dA, stream));
+  return from_hip(nf4::launch_lora_dx_group(count, x, M, K, v, r, scale, accumulate, part, dA, stream));
 }
+
+}  // namespace
+
+extern "C" {
+
+int qlora_linear_bwd_group(int32_t count, const nf4_weight* const* W, const uint16_t* x, const uint16_t* const* dy,
+                           int64_t M, const uint16_t* const* A, const uint16_t* const* B, int32_t r, float scale,
+                           const float* const* u, uint16_t* const* dx, float* const* dA, float* const* dB,
+                           int accumulate, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return run_bwd_group(count, W, x, nullptr, dy, M, A, B, r, scale, u, dx, dA, dB, accumulate, ws, ws_bytes, stream);
+}
+
+int qlora_linear_bwd_act8(int32_t count, const nf4_weight* const* W, const qlora_act8* x8, const uint16_t* const* dy,
+                          int64_t M, const uint16_t* const* A, const uint16_t* const* B, int32_t r, float scale,
+                          const float* const* u, uint16_t* const* dx, float* const* dA, float* const* dB,
+                          int accumulate, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!x8) return NF4_ERR_NULL;
+  return run_bwd_group(count, W, nullptr, x8, dy, M, A, B, r, scale, u, dx, dA, dB, accumulate, ws, ws_bytes, stream);
+}
+
+size_t qlora_workspace_bytes_act8(int32_t count, const int64_t* N, int64_t M, int64_t K, int32_t r) {
+  if (qlora_workspace_bytes_group(count, N, M, K, r) == 0) return 0;
+  return bwd_act8_ws(count, N, M, K, r);
+}
+
+int qlora_act8_pack(const uint16_t* x, int64_t numel, int8_t* codes, uint16_t* absmax, hipStream_t stream) {
+  if (numel < 0 || numel % 64 || numel > (int64_t(1) << 42)) return NF4_ERR_SHAPE;
+  if (numel == 0) return NF4_OK;
+  if (!x || !codes || !absmax) return NF4_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(absmax)) return NF4_ERR_ALIGN;
+  return from_hip(nf4::launch_act8_pack(x, numel, codes, absmax, stream));
+}
+
+int qlora_act8_unpack(const int8_t* codes, const uint16_t* absmax, int64_t numel, uint16_t* x, hipStream_t stream) {
+  if (numel < 0 || numel % 64 || numel > (int64_t(1) << 42)) return NF4_ERR_SHAPE;
+  if (numel == 0) return NF4_OK;
+  if (!x || !codes || !absmax) return NF4_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(absmax)) return NF4_ERR_ALIGN;
+  return from_hip(nf4::launch_act8_unpack(codes, absmax, numel, x, stream));
+}
+
+// sizes of the norm calls; with codes the rows are whole blocks of 64
+static int check_norm(int64_t M, int64_t K, float eps, bool codes) {
+  if (M < 0 || M >= (int64_t(1) << 31) || K < 8 || K > 16384 || K % (codes ? 64 : 8)) return NF4_ERR_SHAPE;
+  if (!(eps >= 0.f) || !isfinite(eps)) return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+int qlora_rmsnorm_fwd(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
+                      float eps, uint16_t* h, uint16_t* y, float* rstd, const qlora_act8* y8, hipStream_t stream) {
+  const int st = check_norm(M, K, eps, y8 != nullptr);
+  if (st || M == 0) return st;
+  if (!x || !weight || !y || (y8 && !(y8->codes && y8->absmax))) return NF4_ERR_NULL;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) || !aligned16(y) || !aligned16(rstd) ||
+      (y8 && !(aligned16(y8->codes) && aligned16(y8->absmax))))
+    return NF4_ERR_ALIGN;
+  const nf4::NormFwdArgs a{x, residual, weight, M, K, eps, h, y, rstd, y8 ? y8->codes : nullptr, y8 ? y8->absmax : nullptr};
+  return from_hip(nf4::launch_rmsnorm_fwd(a, stream));
+}
+
+size_t qlora_rmsnorm_workspace_bytes(int64_t M, int64_t K) {
+  if (check_norm(M, K, 0.f, false) || M == 0) return 0;
+  return align_up(nf4::norm_bwd_ws_floats(M, K) * 4);
+}
+
+int qlora_rmsnorm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
+                      const float* rstd, int64_t M, int64_t K, uint16_t* dx, float* dw, int accumulate, void* ws,
+                      size_t ws_bytes, hipStream_t stream) {
+  const int st = check_norm(M, K, 0.f, false);
+  if (st || M == 0) return st;
+  if (!dy || !h || !weight || !rstd || !dx) return NF4_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(dh) || !aligned16(h) || !aligned16(weight) || !aligned16(rstd) || !aligned16(dx) ||
+      !aligned16(dw) || !aligned16(ws))
+    return NF4_ERR_ALIGN;
+  if (dw && (!ws || ws_bytes < qlora_rmsnorm_workspace_bytes(M, K))) return NF4_ERR_WORKSPACE;
+  const nf4::NormBwdArgs a{dy, dh, h, weight, rstd, M, K, dx};
+  return from_hip(nf4::launch_rmsnorm_bwd(a, dw, accumulate, static_cast<float*>(ws), stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- attention: argument checks
+constexpr int64_t kAttnLimit = int64_t(1) << 30;   // tokens of one sequence; a window past it hides nothing
+
+int check_attn_config(const qlora_attn_config* c) {
+  if (!c) return NF4_ERR_NULL;
+  if (c->kv_heads < 1 || c->heads < c->kv_heads || c->heads > 65535 || c->heads % c->kv_heads) return NF4_ERR_SHAPE;
+  if (c->d < 8 || c->d > 128 || c->d % 8) return NF4_ERR_SHAPE;
+  if (c->window < 0 || c->q_tokens < 0 || c->k_tokens < 0) return NF4_ERR_SHAPE;
+  if (c->q_tokens > (int64_t(1) << 40) || c->k_tokens > (int64_t(1) << 40)) return NF4_ERR_SHAPE;
+  if (!(c->scale > 0.f) || !isfinite(c->scale)) return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+// Sequences inside the tensors; query ranges in order and apart (each output row has one writer), and
+// for the backward key ranges too. Launches count workgroups in 32 bits.
+int check_attn_seqs(const qlora_attn_config* c, int64_t count, const qlora_attn_seq* s, bool backward) {
+  if (count < 0 || count > (int64_t(1) << 24)) return NF4_ERR_SHAPE;
+  if (count && !s) return NF4_ERR_NULL;
+  int64_t q_end = 0, k_end = 0, workgroups = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (s[i].nq < 0 || s[i].nk < 0 || s[i].nq >= kAttnLimit || s[i].nk >= kAttnLimit) return NF4_ERR_SHAPE;
+    if (s[i].q0 < q_end || s[i].q0 > c->q_tokens - s[i].nq) return NF4_ERR_SHAPE;
+    if (s[i].k0 < (backward ? k_end : 0) || s[i].k0 > c->k_tokens - s[i].nk) return NF4_ERR_SHAPE;
+    q_end = s[i].q0 + s[i].nq;
+    k_end = s[i].k0 + s[i].nk;
+    workgroups += ((s[i].nq + 127) / 128 + (s[i].nk + 127) / 128) * c->heads;
+    if (workgroups >= (int64_t(1) << 30)) return NF4_ERR_SHAPE;
+  }
+  return NF4_OK;
+}
+
+// One tensor of `tokens` x `heads` x d: 16-byte aligned rows whose bytes fit 32-bit offsets within a tile
+// of tokens; an output's rows must not overlap.
+int check_attn_tensor(const qlora_attn_tensor* t, int64_t tokens, int heads, int d, bool output) {
+  if (!t) return NF4_ERR_NULL;
+  if (t->token_stride < d || t->token_stride >= (int64_t(1) << 22) || t->token_stride % 8) return NF4_ERR_SHAPE;
+  if (t->head_stride < 0 || t->head_stride > (int64_t(1) << 44) || t->head_stride % 8) return NF4_ERR_SHAPE;
+  if (output && heads > 1) {
+    const bool tokens_outer = t->head_stride >= d && t->token_stride >= t->head_stride * (heads - 1) + d;
+    const bool heads_outer = tokens == 0 || t->head_stride >= t->token_stride * (tokens - 1) + d;
+    if (!tokens_outer && !heads_outer) return NF4_ERR_SHAPE;
+  }
+  if (tokens == 0) return NF4_OK;
+  if (!t->data) return NF4_ERR_NULL;
+  return aligned16(t->data) ? NF4_OK : NF4_ERR_ALIGN;
+}
+
+nf4::AttnTensor attn_tensor(const qlora_attn_tensor* t) { return nf4::AttnTensor{t->data, t->token_stride, t->head_stride}; }
+
+int attn_window(const qlora_attn_config* c) { return c->window >= kAttnLimit ? 0 : (int)c->window; }
+
+// the sequences as the launchers take them; throws std::bad_alloc
+std::vector<nf4::AttnSeq> attn_seqs(int64_t count, const qlora_attn_seq* s) {
+  std::vector<nf4::AttnSeq> v((size_t)count);
+  for (int64_t i = 0; i < count; ++i) v[(size_t)i] = nf4::AttnSeq{s[i].q0, s[i].k0, (int)s[i].nq, (int)s[i].nk};
+  return v;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qlora_attn_workspace_bytes(const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs, int backward) {
+  if (check_attn_config(cfg) || check_attn_seqs(cfg, count, seqs, backward != 0) || count == 0) return 0;
+  try {
+    const std::vector<nf4::AttnSeq> v = attn_seqs(count, seqs);
+    const size_t f = backward ? nf4::attn_bwd_ws_floats(v.data(), count, cfg->heads, cfg->kv_heads, cfg->d, cfg->q_tokens)
+                              : nf4::attn_fwd_ws_floats(v.data(), count, cfg->heads, cfg->kv_heads, cfg->d, attn_window(cfg));
+    return align_up(f * 4);
+  } catch (...) {
+    return 0;
+  }
+}
+
+int qlora_attn_fwd(const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs, const qlora_attn_tensor* q,
+                   const qlora_attn_tensor* k, const qlora_attn_tensor* v, const qlora_attn_tensor* o, float* lse,
+                   void* ws, size_t ws_bytes, hipStream_t stream) {
+  int st = check_attn_config(cfg);
+  if (st || (st = check_attn_seqs(cfg, count, seqs, false))) return st;
+  if ((st = check_attn_tensor(q, cfg->q_tokens, cfg->heads, cfg->d, false)) ||
+      (st = check_attn_tensor(k, cfg->k_tokens, cfg->kv_heads, cfg->d, false)) ||
+      (st = check_attn_tensor(v, cfg->k_tokens, cfg->kv_heads, cfg->d, false)) ||
+      (st = check_attn_tensor(o, cfg->q_tokens, cfg->heads, cfg->d, true)))
+    return st;
+  if (!aligned16(lse) || !aligned16(ws)) return NF4_ERR_ALIGN;
+  try {
+    const std::vector<nf4::AttnSeq> s = attn_seqs(count, seqs);
+    const size_t need = nf4::attn_fwd_ws_floats(s.data(), count, cfg->heads, cfg->kv_heads, cfg->d, attn_window(cfg)) * 4;
+    if (need && (!ws || ws_bytes < need)) return NF4_ERR_WORKSPACE;
+    const nf4::AttnFwdArgs a{attn_tensor(q), attn_tensor(k), attn_tensor(v), attn_tensor(o), lse, cfg->q_tokens, cfg->heads,
+                             cfg->kv_heads, cfg->d, cfg->causal != 0, attn_window(cfg), cfg->scale * 1.4426950408889634f};
+    return from_hip(nf4::launch_attn_fwd(a, s.data(), count, static_cast<float*>(ws), stream));
+  } catch (...) {
+    return NF4_ERR_HIP;   // no host memory for the sequence list
+  }
+}
+
+int qlora_attn_bwd(const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs, const qlora_attn_tensor* q,
+                   const qlora_attn_tensor* k, const qlora_attn_tensor* v, const qlora_attn_tensor* o, const float* lse,
+                   const qlora_attn_tensor* dout, const qlora_attn_tensor* dq, const qlora_attn_tensor* dk,
+                   const qlora_attn_tensor* dv, void* ws, size_t ws_bytes, hipStream_t stream) {
+  int st = check_attn_config(cfg);
+  if (st || (st = check_attn_seqs(cfg, count, seqs, true))) return st;
+  const int64_t tq = cfg->q_tokens, tk = cfg->k_tokens;
+  if ((st = check_attn_tensor(q, tq, cfg->heads, cfg->d, false)) || (st = check_attn_tensor(k, tk, cfg->kv_heads, cfg->d, false)) ||
+      (st = check_attn_tensor(v, tk, cfg->kv_heads, cfg->d, false)) || (st = check_attn_tensor(o, tq, cfg->heads, cfg->d, false)) ||
+      (st = check_attn_tensor(dout, tq, cfg->heads, cfg->d, false)) || (st = check_attn_tensor(dq, tq, cfg->heads, cfg->d, true)) ||
+      (st = check_attn_tensor(dk, tk, cfg->kv_heads, cfg->d, true)) || (st = check_attn_tensor(dv, tk, cfg->kv_heads, cfg->d, true)))
+    return st;
+  if (count == 0) return NF4_OK;
+  if (!lse && tq > 0) return NF4_ERR_NULL;
+  if (!aligned16(lse) || !aligned16(ws)) return NF4_ERR_ALIGN;
+  try {
+    const std::vector<nf4::AttnSeq> s = attn_seqs(count, seqs);
+    const size_t need = nf4::attn_bwd_ws_floats(s.data(), count, cfg->heads, cfg->kv_heads, cfg->d, tq) * 4;
+    if (need && (!ws || ws_bytes < need)) return NF4_ERR_WORKSPACE;
+    const nf4::AttnBwdArgs a{attn_tensor(q), attn_tensor(k), attn_tensor(v), attn_tensor(o), attn_tensor(dout), attn_tensor(dq),
+                             attn_tensor(dk), attn_tensor(dv), lse, nullptr, tq, cfg->heads, cfg->kv_heads, cfg->d,
+                             cfg->causal != 0, attn_window(cfg), cfg->scale * 1.4426950408889634f, cfg->scale};
+    return from_hip(nf4::launch_attn_bwd(a, s.data(), count, tq, static_cast<float*>(ws), stream));
+  } catch (...) {
+    return NF4_ERR_HIP;   // no host memory for the sequence list
+  }
+}
+
 
 int qlora_linear_fwd_noalloc(const nf4_weight* W, const uint16_t* x, int64_t M, const uint16_t* A,
                              const uint16_t* B, int32_t r, float scale, uint16_t* y, float* u_out,

@@ -1,0 +1,225 @@
+// 8-bit activation checkpoints (gfx950): packing, unpacking, and the adapter gradient that reads them.
+//
+// The adapted linear's backward needs its input x only for dA = s v^T x (v = dY B). With x kept as
+// codes and block maxima (act8.h), x[m][c] = q[m][c] a[m][b] / 127 for the 64-column block b of c:
+//   dA[j][c] = s sum_m (v[m][j] a[m][b] / 127) q[m][c],
+// so the scale goes into the rank-sized operand once per row and block, and the streamed operand is
+// the codes themselves, which bf16 holds exactly. The pass reads 1.03 bytes per value where the bf16
+// input would take 2.
+#include "act8.h"
+#include "launch.h"
+
+namespace nf4 {
+
+// Packing: a lane takes 8 values, 8 lanes a block. Bound by memory: 2 bytes in and 1.03 out per value.
+__global__ __launch_bounds__(256) void act8_pack_kernel(const u32x4* __restrict__ x, int64_t vecs, u32x2* __restrict__ codes,
+                                                        uint16_t* __restrict__ absmax) {
+  constexpr int U = 4;   // loads in flight per lane
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < vecs; i0 += U * step) {
+    u32x4 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) v[k] = x[min(i0 + k * step, vecs - 1)];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t i = i0 + k * step;
+      const float a = max8(absmax8(v[k]));   // vecs is a multiple of 8: a block's lanes are in or out together
+      if (i < vecs) {
+        codes[i] = act8_codes(v[k], a);
+        if ((i & 7) == 0) absmax[i >> 3] = (uint16_t)(__float_as_uint(a) >> 16);
+      }
+    }
+  }
+}
+
+// Unpacking: a lane takes 8 values. Bound by memory: 1.03 bytes in and 2 out per value.
+__global__ __launch_bounds__(256) void act8_unpack_kernel(const u32x2* __restrict__ codes, const uint16_t* __restrict__ absmax,
+                                                          int64_t vecs, u32x4* __restrict__ x) {
+  constexpr int U = 4;
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < vecs; i0 += U * step) {
+    u32x2 q[U];
+    uint32_t a[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t i = min(i0 + k * step, vecs - 1);
+      q[k] = codes[i];
+      a[k] = absmax[i >> 3];
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t i = i0 + k * step;
+      if (i >= vecs) break;
+      const float f = __uint_as_float(a[k] << 16) * (1.f / 127.f);
+      u32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = q[k][e >> 1] >> (16 * (e & 1));
+        o[e] = pack_bf16x2((float)(int8_t)w * f, (float)(int8_t)(w >> 8) * f);
+      }
+      x[i] = o;
+    }
+  }
+}
+
+static unsigned stream_grid(int64_t vecs) {
+  const int64_t b = (vecs + 1023) / 1024;   // four vectors a thread
+  return (unsigned)(b < 1 ? 1 : b > 8192 ? 8192 : b);
+}
+
+hipError_t launch_act8_pack(const uint16_t* x, int64_t numel, int8_t* codes, uint16_t* absmax, hipStream_t stream) {
+  const int64_t vecs = numel / 8;
+  hipLaunchKernelGGL(act8_pack_kernel, dim3(stream_grid(vecs)), dim3(256), 0, stream, reinterpret_cast<const u32x4*>(x),
+                     vecs, reinterpret_cast<u32x2*>(codes), absmax);
+  return hipGetLastError();
+}
+
+hipError_t launch_act8_unpack(const int8_t* codes, const uint16_t* absmax, int64_t numel, uint16_t* x, hipStream_t stream) {
+  const int64_t vecs = numel / 8;
+  hipLaunchKernelGGL(act8_unpack_kernel, dim3(stream_grid(vecs)), dim3(256), 0, stream,
+                     reinterpret_cast<const u32x2*>(codes), absmax, vecs, reinterpret_cast<u32x4*>(x));
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------------
+// dA from the codes. A workgroup takes 128 columns (two blocks) and a range of rows, for up to RT
+// tiles of 16 adapter ranks (of one linear or of several that share x); its 4 waves take 32-row
+// chunks in turn. In v_mfma_f32_16x16x32_bf16 a lane's operand fragment is 8 rows of one column, so a
+// lane loads one dword (4 columns) from each of 8 rows and keeps all four columns: column tile t is
+// the columns 4 i + t of the block, and nothing is transposed. The rank operand is scaled in fp32 and
+// split into a bf16 pair hi + lo, as the passes over bf16 inputs split theirs (relative error 2^-17).
+struct Dx8Tile {
+  const float* v;      // [M x r], at the tile's first column
+  float* part;         // [row ranges][K][r], at the tile's first column
+};
+struct Dx8Args {
+  const int8_t* codes;
+  const uint16_t* absmax;
+  int64_t M, K;
+  int64_t rows;        // rows per range (a multiple of 32)
+  int r;               // rank
+  Dx8Tile tile[4 * 8];
+};
+
+template <int RT>
+__global__ __launch_bounds__(256) void act8_grad_kernel(const Dx8Args a, int tile0) {
+  __shared__ f32x4 red[4][4][64];
+  const int tid = threadIdx.x, lane = tid & 63, grp = lane >> 4, col = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t nb = a.K / 64, b0 = (int64_t)blockIdx.x * 2;
+  const int blocks = (int)min((int64_t)2, nb - b0);
+  const int64_t m_begin = (int64_t)blockIdx.y * a.rows, m_end = min(a.M, m_begin + a.rows);
+  f32x4 acc[RT][2][4];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[t][b][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  for (int64_t m0 = m_begin + 32 * wave; m0 < m_end; m0 += 128) {
+    uint32_t x[2][8];
+    float s[2][8], v[RT][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t m = m0 + 8 * grp + e, mr = min(m, m_end - 1);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int64_t blk = b0 + min(b, blocks - 1);
+        x[b][e] = *reinterpret_cast<const uint32_t*>(a.codes + mr * a.K + blk * 64 + 4 * col);
+        s[b][e] = __uint_as_float((uint32_t)a.absmax[mr * nb + blk] << 16) * (1.f / 127.f);
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) v[t][e] = m < m_end ? a.tile[tile0 + t].v[mr * a.r + col] : 0.f;
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      bf16x8 xf[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xf[c][e] = (__bf16)(float)(int8_t)(x[b][e] >> (8 * c));
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        bf16x8 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float p = v[t][e] * s[b][e];
+          hi[e] = (__bf16)p;
+          lo[e] = (__bf16)(p - (float)hi[e]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[t][b][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, xf[c], acc[t][b][c], 0, 0, 0);
+          acc[t][b][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, xf[c], acc[t][b][c], 0, 0, 0);
+        }
+      }
+    }
+  }
+  // the waves' sums, added in wave order: wave w finishes column tile w
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) red[wave][c][lane] = acc[t][b][c];
+      __syncthreads();
+      f32x4 v = red[0][wave][lane];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) v += red[w][wave][lane];
+      if (b < blocks) {
+        const int64_t c = (b0 + b) * 64 + 4 * col + wave;
+        *reinterpret_cast<f32x4*>(a.tile[tile0 + t].part + ((int64_t)blockIdx.y * a.K + c) * a.r + 4 * grp) = v;
+      }
+      __syncthreads();
+    }
+}
+
+// Rows per range: about 512 workgroups, 128 rows (one chunk a wave) at least.
+static int64_t dx8_rows(int64_t M, int64_t K) {
+  const int64_t groups = (K / 64 + 1) / 2;
+  int64_t ranges = (512 + groups - 1) / groups;
+  if (ranges > (M + 127) / 128) ranges = (M + 127) / 128;
+  return ((M + ranges - 1) / ranges + 31) / 32 * 32;
+}
+static int64_t dx8_ranges(int64_t M, int64_t K) {
+  const int64_t rows = dx8_rows(M, K);
+  return (M + rows - 1) / rows;
+}
+
+size_t act8_grad_ws_floats(int count, int64_t M, int64_t K, int r) {
+  return (size_t)count * (size_t)dx8_ranges(M, K) * (size_t)K * r;
+}
+
+hipError_t launch_act8_grad(int count, const int8_t* codes, const uint16_t* absmax, int64_t M, int64_t K,
+                            const float* const* v, int r, float scale, int accumulate, float* ws, float* const* dA,
+                            hipStream_t stream) {
+  if (count < 1 || count > 4) return hipErrorInvalidValue;
+  Dx8Args a{};
+  a.codes = codes;
+  a.absmax = absmax;
+  a.M = M;
+  a.K = K;
+  a.r = r;
+  a.rows = dx8_rows(M, K);
+  const int64_t ranges = dx8_ranges(M, K);
+  const float* part[4];
+  int nt = 0;
+  for (int i = 0; i < count; ++i) {
+    float* base = ws + (size_t)i * ranges * K * r;
+    part[i] = base;
+    for (int t = 0; t < r / 16; ++t) a.tile[nt++] = Dx8Tile{v[i] + 16 * t, base + 16 * t};
+  }
+  const dim3 grid((unsigned)((K / 64 + 1) / 2), (unsigned)ranges), block(256);
+  for (int t = 0; t < nt; t += 4) {
+    switch (nt - t) {
+      case 1: hipLaunchKernelGGL(act8_grad_kernel<1>, grid, block, 0, stream, a, t); break;
+      case 2: hipLaunchKernelGGL(act8_grad_kernel<2>, grid, block, 0, stream, a, t); break;
+      case 3: hipLaunchKernelGGL(act8_grad_kernel<3>, grid, block, 0, stream, a, t); break;
+      default: hipLaunchKernelGGL(act8_grad_kernel<4>, grid, block, 0, stream, a, t); break;
+    }
+  }
+  return launch_lora_sum(count, part, (int)ranges, K, r, scale, accumulate, dA, stream);
+}
+
+}  // namespace nf4

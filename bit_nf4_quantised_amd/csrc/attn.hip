@@ -1,0 +1,1003 @@
+// Attention of the layer around the quantised linears (gfx950): forward, few-row forward over a long
+// cache, and the backward pass that recomputes the probabilities.
+//
+// For query row i of a sequence with nq queries and nk keys, standing at position p_i = nk - nq + i,
+// over its visible keys j (j <= p_i when causal, j > p_i - window with a window):
+//   z_ij = scale q_i.k_j    lse_i = ln sum_j exp(z_ij)    P_ij = exp(z_ij - lse_i)    o_i = sum_j P_ij v_j
+//   delta_i = do_i.o_i      dS_ij = P_ij (do_i.v_j - delta_i)
+//   dq_i = scale sum_j dS_ij k_j    dk_j = scale sum_i dS_ij q_i    dv_j = sum_i P_ij do_i
+// (dk, dv also sum over the query heads that share the key head). Scores, softmax statistics and all
+// sums are fp32; P and dS are rounded to bf16 where they enter the second product of each pair, as
+// the matrix instructions take bf16 operands (relative error 2^-9 a term, independent over terms).
+//
+// Layout. Every product is taken with v_mfma_f32_32x32x16_bf16, whose result holds in lane l column
+// l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4 for i < 16. The scores are formed with the rows that
+// the wave streams past as result rows and the rows that it owns as result columns, so a lane holds
+// 16 consecutive-in-groups-of-4 streamed rows of one owned row: the softmax of a row is a reduction
+// inside a lane plus one exchange between lane halves, and the rounded probabilities are already the
+// second product's operand (its contraction runs over the streamed rows in the lane's own order; the
+// other operand is read in the same order from LDS with transpose loads). Nothing goes through LDS
+// between the two products.
+#include "common.h"
+#include "launch.h"
+
+#include <limits.h>
+
+#include <algorithm>
+#include <vector>
+
+namespace nf4 {
+
+typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// A row's reference maximum is raised only when a new score passes it by more than this many powers
+// of two: until then the probabilities of the row grow to at most 2^kSlack, which costs no accuracy
+// in fp32 sums and bf16 operands (both are relative), and the output is not rescaled.
+constexpr float kSlack = 8.f;
+
+// ------------------------------------------------------------------------------------------
+// LDS tiles: rows of DP bf16 in 16-byte chunks; chunk c of row m sits at slot c ^ swz(m). 16
+// consecutive rows at one chunk (operand reads along a row) and 4 aligned rows at 4 aligned chunks
+// (transpose reads) both fall on 16 different 16-byte bank groups.
+template <int DP>
+struct Tile {
+  static constexpr int kChunks = DP / 8;
+  static __device__ __forceinline__ int swz(int m) {
+    return DP == 128 ? (((m & 3) << 2) | ((m >> 2) & 3)) : ((((m >> 1) & 1) << 2) | ((m >> 2) & 3));
+  }
+  static __device__ __forceinline__ int elem(int m, int c) { return m * DP + ((c ^ swz(m)) << 3); }
+
+  // operand whose rows are tile rows m0 .. m0+31 and whose contraction runs along the tile's
+  // columns 16 ks .. 16 ks + 15
+  static __device__ __forceinline__ bf16x8 rows(const uint16_t* t, int m0, int ks, int lane) {
+    const int m = lane & 31;
+    return *reinterpret_cast<const bf16x8*>(t + m0 * DP + elem(m, 2 * ks + (lane >> 5)));
+  }
+  // operand whose rows are tile columns 32 dt .. 32 dt + 31 and whose contraction runs over tile rows
+  // m0 .. m0+15 (m0 a multiple of 16) in the order of a score accumulator: lane half h takes rows
+  // 4 h .. 4 h + 3, then 8 + 4 h .. 8 + 4 h + 3
+  static __device__ __forceinline__ bf16x8 cols(const uint16_t* t, int m0, int dt, int lane) {
+    const int j = lane & 15, h = lane >> 5;
+    const int m = 4 * h + (j >> 2), c = 4 * dt + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
+    const uint16_t* base = t + m0 * DP + 4 * (j & 1);
+    bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(base + elem(m, c)));
+    bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(base + elem(m + 8, c)));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
+// LDS-DMA of ROWS x DP into a tile by NW waves: rows past `rows` and columns past d become zeros.
+template <int DP, int ROWS, int NW>
+struct TileDma {
+  static constexpr int kLoads = ROWS * (DP / 8) / 64 / NW;   // per wave
+  static_assert(kLoads >= 1, "a wave loads 1 KiB at least");
+  uint32_t off[kLoads];
+  __device__ __forceinline__ void init(int wave, int lane, int d, uint32_t stride) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int slot = (wave * kLoads + j) * 64 + lane;
+      const int row = slot / Tile<DP>::kChunks, c = (slot % Tile<DP>::kChunks) ^ Tile<DP>::swz(row);
+      off[j] = 8 * c < d ? (uint32_t)row * stride * 2u + (uint32_t)c * 16u : kOutOfRange;
+    }
+  }
+  // base: the tile's first row; rows >= 0 valid rows
+  __device__ __forceinline__ void load(uint16_t* tile, const uint16_t* base, int rows, int d, uint32_t stride,
+                                       int wave) const {
+    const uint32_t nrec = rows > 0 ? ((uint32_t)(min(rows, ROWS) - 1) * stride + (uint32_t)d) * 2u : 0u;
+    __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)nrec, kRsrcFlags);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(tile + (wave * kLoads + j) * 512), 16, off[j], 0, 0, 0);
+  }
+};
+
+// Keys and values of one key head of a sequence, streamed in tiles of ROWS.
+template <int DP, int ROWS, int NW>
+struct KvStream {
+  typedef TileDma<DP, ROWS, NW> Dma;
+  static constexpr int kLoads = 2 * Dma::kLoads;   // per wave and tile
+  Dma kd, vd;
+  const uint16_t *k, *v;
+  uint32_t ks, vs;
+  int nk, d;
+  __device__ __forceinline__ void init(const AttnTensor& kt, const AttnTensor& vt, const AttnSeq& s, int kvh, int dd, int wave,
+                                       int lane) {
+    ks = (uint32_t)kt.token;
+    vs = (uint32_t)vt.token;
+    nk = s.nk;
+    d = dd;
+    k = kt.p + s.k0 * kt.token + (int64_t)kvh * kt.head;
+    v = vt.p + s.k0 * vt.token + (int64_t)kvh * vt.head;
+    kd.init(wave, lane, d, ks);
+    vd.init(wave, lane, d, vs);
+  }
+  __device__ __forceinline__ void load(uint16_t* kt, uint16_t* vt, int j, int wave) const {   // keys from j
+    kd.load(kt, k + (int64_t)j * ks, nk - j, d, ks, wave);
+    vd.load(vt, v + (int64_t)j * vs, nk - j, d, vs, wave);
+  }
+};
+
+// Rows in registers as the operand whose columns are those rows (contraction along d): lane column
+// lane % 32, chunk 2 ks + lane / 32 for every ks. `row` is the lane's row, or null for zeros.
+template <int DP>
+__device__ __forceinline__ void load_rows(bf16x8 (&f)[DP / 16], const uint16_t* row, int d, int lane) {
+#pragma unroll
+  for (int ks = 0; ks < DP / 16; ++ks) {
+    const int c = 8 * (2 * ks + (lane >> 5));
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
+    if (row && c < d) v = *reinterpret_cast<const u32x4*>(row + c);
+    f[ks] = __builtin_bit_cast(bf16x8, v);
+  }
+}
+
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// maximum and sum over the two lane halves (lane and lane ^ 32), in both
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// accumulator rows 8 s .. 8 s + 7 of the lane (s = 0, 1) as an operand fragment
+__device__ __forceinline__ bf16x8 pack8(const f32x16& v, int s) {
+  u32x4 p;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) p[k] = pack_bf16x2(v[8 * s + 2 * k], v[8 * s + 2 * k + 1]);
+  return __builtin_bit_cast(bf16x8, p);
+}
+
+// index of accumulator element i of this lane among the 32 result rows
+__device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+// Stores a 32-row result tile (rows: columns 32 dt .. of a token's head, columns: tokens) as bf16:
+// lane halves exchange groups of four so that every lane writes 16 contiguous bytes. dst: the lane's
+// token and head, or null.
+__device__ __forceinline__ void store_cols(uint16_t* dst, const f32x16& v, float scale, int dt, int d, int lane) {
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    u32x2 a, b;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      a[k] = pack_bf16x2(v[8 * g + 2 * k] * scale, v[8 * g + 2 * k + 1] * scale);
+      b[k] = pack_bf16x2(v[8 * g + 4 + 2 * k] * scale, v[8 * g + 4 + 2 * k + 1] * scale);
+    }
+    const auto x = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+    const int c = 32 * dt + 16 * g + 8 * (lane >> 5);
+    if (dst && c < d) *reinterpret_cast<u32x4*>(dst + c) = u32x4{x[0], y[0], x[1], y[1]};
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Work lists. A launch takes up to kAttnSeqs sequences by value; workgroup indexes count tiles of
+// the sequences in turn (first[s] .. first[s + 1] - 1 belong to sequence s).
+__device__ __forceinline__ int find_seq(const AttnSeqs& sq, int tile) {
+  const int lane = threadIdx.x & 63;
+  const int f = lane < sq.count ? sq.first[lane] : 0x7FFFFFFF;
+  return __builtin_amdgcn_readfirstlane((int)__popcll(__ballot(f <= tile)) - 1);
+}
+
+// Workgroup b of a launch over tiles x kv_heads x per (`per`: workgroups that share a tile and a key
+// head). Consecutive workgroups go to the 8 XCDs in turn; with a multiple of 8 key heads each XCD
+// takes its own heads, so their keys and values stay in its L2. Tiles vary slowest: the host orders
+// them by falling work.
+struct Unit {
+  int tile, kvh, sub;
+};
+__device__ __forceinline__ Unit unit_of(int b, int kv_heads, int per) {
+  Unit u;
+  if (kv_heads % 8 == 0) {
+    const int hx = kv_heads / 8, i = b >> 3;
+    u.sub = i % per;
+    u.kvh = (b & 7) * hx + (i / per) % hx;
+    u.tile = i / (per * hx);
+  } else {
+    u.sub = b % per;
+    u.kvh = (b / per) % kv_heads;
+    u.tile = b / (per * kv_heads);
+  }
+  return u;
+}
+
+// visible keys [lo, hi) of the query at position p
+struct Range {
+  int lo, hi;
+};
+__device__ __forceinline__ Range visible(int p, int nk, int causal, int window) {
+  Range r;
+  r.hi = causal ? min(nk, p + 1) : nk;
+  r.lo = window ? max(0, p - window + 1) : 0;
+  return r;
+}
+
+// Running softmax of a wave's 32 owned rows (one per lane column) over NT blocks of 32 streamed keys.
+template <int DT>
+struct Online {
+  float m, mc, l;     // reference maximum (raw score), m * c (0 while no key was seen), the lane's part of the sum
+  f32x16 o[DT];       // unnormalised output, rows d, columns owned rows
+  __device__ __forceinline__ void init() {
+    m = -INFINITY;
+    mc = 0.f;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i] = zero16();
+  }
+  template <int NT>
+  __device__ __forceinline__ void update(f32x16 (&s)[NT], float c, float slack) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
+    mx = half_max(mx);
+    if (__any(mx > m + slack)) {
+      const float mn = fmaxf(m, mx);
+      const float mnc = mn == -INFINITY ? 0.f : mn * c;
+      const float a = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mc - mnc);   // no key yet: l and o are zero
+      m = mn;
+      mc = mnc;
+      l *= a;
+#pragma unroll
+      for (int k = 0; k < DT; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[k][i] *= a;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[t][i] = __builtin_amdgcn_exp2f(__fmaf_rn(s[t][i], c, -mc));
+        sum += s[t][i];
+      }
+    l += sum;
+  }
+};
+
+// ------------------------------------------------------------------------------------------
+// Forward. A workgroup of 4 waves takes 128 query rows of one head, 32 per wave; keys and values
+// stream through LDS in tiles of 64, two tiles deep, by LDS-DMA.
+template <int DP>
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnFwdArgs a, const AttnSeqs sq) {
+  constexpr int BN = 64, KS = DP / 16, DT = DP / 32;
+  typedef Tile<DP> T;
+  typedef KvStream<DP, BN, 4> Stream;
+  __shared__ __attribute__((aligned(16))) uint16_t Ks[2][BN * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t Vs[2][BN * DP];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int G = a.heads / a.kv_heads;
+  const Unit u = unit_of((int)blockIdx.x, a.kv_heads, G);
+  const int si = find_seq(sq, u.tile);
+  const AttnSeq s = sq.seq[si];
+  // a sequence's tiles run from its last rows (the most keys when causal) to its first
+  const int qt = sq.first[si + 1] - 1 - u.tile;
+  const int head = u.kvh * G + u.sub;
+  const int r0 = qt * 128, shift = s.nk - s.nq;   // row i stands at position i + shift
+
+  const int row = r0 + wave * 32 + (lane & 31);
+  bf16x8 qf[KS];
+  load_rows<DP>(qf, row < s.nq ? a.q.p + (s.q0 + row) * a.q.token + (int64_t)head * a.q.head : nullptr, a.d, lane);
+
+  // keys that some row of the workgroup (of this wave) sees
+  const int r1 = min(s.nq, r0 + 128) - 1;
+  const int k_lo = visible(r0 + shift, s.nk, a.causal, a.window).lo & ~(BN - 1);
+  const int k_hi = visible(r1 + shift, s.nk, a.causal, a.window).hi;
+  const int w0 = r0 + wave * 32, w1 = min(s.nq - 1, w0 + 31);
+  const Range wa = visible(w0 + shift, s.nk, a.causal, a.window), wb = visible(w1 + shift, s.nk, a.causal, a.window);
+  const Range mine = visible(row + shift, s.nk, a.causal, a.window);
+  const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
+
+  Stream kv;
+  kv.init(a.k, a.v, s, u.kvh, a.d, wave, lane);
+
+  Online<DT> acc;
+  acc.init();
+  const float slack = kSlack / a.c;
+  if (nt > 0) kv.load(Ks[0], Vs[0], k_lo, wave);
+  for (int t = 0; t < nt; ++t) {
+    const int st = t & 1;
+    if (t + 1 < nt) {
+      kv.load(Ks[st ^ 1], Vs[st ^ 1], k_lo + (t + 1) * BN, wave);
+      wait_vmcnt<Stream::kLoads>();   // loads complete in order: tile t is in, tile t + 1 may be in flight
+    } else {
+      wait_vmcnt<0>();
+    }
+    lds_barrier();
+    const int j0 = k_lo + t * BN;
+    if (j0 < wb.hi && j0 + BN > wa.lo) {
+      f32x16 sc[BN / 32];
+#pragma unroll
+      for (int kt = 0; kt < BN / 32; ++kt) {
+        sc[kt] = zero16();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) sc[kt] = mfma(T::rows(Ks[st], 32 * kt, ks, lane), qf[ks], sc[kt]);
+      }
+      // some row of the wave does not see some key of the tile
+      if (j0 + BN > wa.hi || j0 < wb.lo) {
+#pragma unroll
+        for (int kt = 0; kt < BN / 32; ++kt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int j = j0 + 32 * kt + acc_row(i, lane);
+            if (j < mine.lo || j >= mine.hi) sc[kt][i] = -INFINITY;
+          }
+      }
+      acc.update(sc, a.c, slack);
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk) {
+        const bf16x8 p = pack8(sc[kk / 2], kk & 1);
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(T::cols(Vs[st], 16 * kk, dt, lane), p, acc.o[dt]);
+      }
+    }
+    lds_barrier();
+  }
+
+  const float l = half_sum(acc.l);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint16_t* dst = row < s.nq ? a.o.p + (s.q0 + row) * a.o.token + (int64_t)head * a.o.head : nullptr;
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) store_cols(dst, acc.o[dt], inv, dt, a.d, lane);
+  if (a.lse && lane < 32 && row < s.nq)
+    a.lse[(int64_t)head * a.lse_stride + s.q0 + row] = l > 0.f ? acc.mc * kLn2 + __logf(l) : -INFINITY;
+}
+
+// ------------------------------------------------------------------------------------------
+// Few query rows over many keys. The query heads that share a key head are packed with the tokens
+// into rows (row = token * group + head in group), 32 rows a workgroup; its keys are one range of the
+// sequence's, and its 4 waves take 32-key tiles of that range in turn, each through its own LDS ring
+// without barriers. The waves' results are joined in LDS; with several ranges they go to the
+// workspace and attn_join_kernel joins them, in order.
+template <int DP>
+__global__ __launch_bounds__(256, 1) void attn_split_kernel(const AttnFwdArgs a, const AttnSeqs sq, const AttnSplit sp) {
+  constexpr int BN = 32, KS = DP / 16, DT = DP / 32, ST = DP == 128 ? 2 : 4;
+  typedef Tile<DP> T;
+  typedef KvStream<DP, BN, 1> Stream;
+  __shared__ __attribute__((aligned(16))) uint16_t ring[2][4][ST][BN * DP];   // keys, values
+  __shared__ float Ms[4][32], Ls[4][32];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int G = a.heads / a.kv_heads;
+  const Unit u = unit_of((int)blockIdx.x, a.kv_heads, 1);
+  const int si = find_seq(sq, u.tile);
+  const AttnSeq s = sq.seq[si];
+  const int local = u.tile - sq.first[si];
+  const int ns = sp.nsplit[si], split = local % ns, rt = local / ns;
+  const int shift = s.nk - s.nq, rows = s.nq * G;
+  const int row = rt * 32 + (lane & 31);
+  const int tok = min(row, rows - 1) / G, head = u.kvh * G + min(row, rows - 1) % G;
+  bf16x8 qf[KS];
+  load_rows<DP>(qf, row < rows ? a.q.p + (s.q0 + tok) * a.q.token + (int64_t)head * a.q.head : nullptr, a.d, lane);
+
+  const int t0 = rt * 32 / G, t1 = min(rows - 1, rt * 32 + 31) / G;   // tokens of the row tile
+  const Range first = visible(t0 + shift, s.nk, a.causal, a.window), last = visible(t1 + shift, s.nk, a.causal, a.window);
+  const Range mine = visible(tok + shift, s.nk, a.causal, a.window);
+  const int k_lo = max(first.lo & ~(BN - 1), sp.lo[si] + split * sp.chunk);
+  const int k_hi = min(last.hi, sp.lo[si] + (split + 1) * sp.chunk);
+  const int tiles = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
+  const int nt = tiles > wave ? (tiles - wave + 3) / 4 : 0;   // of this wave
+
+  Stream kv;
+  kv.init(a.k, a.v, s, u.kvh, a.d, 0, lane);
+  const int j_w = k_lo + wave * BN;   // the wave's first tile; its tiles are 4 apart
+  Online<DT> acc;
+  acc.init();
+  const float slack = kSlack / a.c;
+  for (int t = 0; t < ST - 1 && t < nt; ++t) kv.load(ring[0][wave][t], ring[1][wave][t], j_w + t * 4 * BN, 0);
+  for (int t = 0; t < nt; ++t) {
+    if (t + ST - 1 < nt) {
+      const int n = t + ST - 1;
+      kv.load(ring[0][wave][n % ST], ring[1][wave][n % ST], j_w + n * 4 * BN, 0);
+      wait_vmcnt<(ST - 1) * Stream::kLoads>();
+    } else {
+      const int ahead = nt - 1 - t;
+      if (ST > 3 && ahead == 2) wait_vmcnt<(ST > 3 ? 2 : 0) * Stream::kLoads>();
+      else if (ST > 2 && ahead == 1) wait_vmcnt<(ST > 2 ? 1 : 0) * Stream::kLoads>();
+      else wait_vmcnt<0>();
+    }
+    asm volatile("" ::: "memory");   // the tile's LDS reads stay after the wait
+    const uint16_t* ks_ = ring[0][wave][t % ST];
+    const uint16_t* vs_ = ring[1][wave][t % ST];
+    const int j0 = j_w + t * 4 * BN;
+    f32x16 sc[1];
+    sc[0] = zero16();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) sc[0] = mfma(T::rows(ks_, 0, ks, lane), qf[ks], sc[0]);
+    if (j0 + BN > first.hi || j0 < last.lo) {   // some row does not see some key (ranges end on tiles)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = j0 + acc_row(i, lane);
+        if (j < mine.lo || j >= mine.hi) sc[0][i] = -INFINITY;
+      }
+    }
+    acc.update(sc, a.c, slack);
+#pragma unroll
+    for (int kk = 0; kk < BN / 16; ++kk) {
+      const bf16x8 p = pack8(sc[0], kk & 1);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(T::cols(vs_, 16 * kk, dt, lane), p, acc.o[dt]);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the ring slot is read out before it is refilled
+  }
+
+  // join the waves: the common maximum, then the scaled sums, added in wave order
+  float l = half_sum(acc.l);
+  if (lane < 32) {
+    Ms[wave][lane] = acc.m;
+    Ls[wave][lane] = l;
+  }
+  __syncthreads();
+  const int col = lane & 31;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) mx = fmaxf(mx, Ms[w][col]);
+  const float mxc = mx == -INFINITY ? 0.f : mx * a.c;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) l += Ms[w][col] == -INFINITY ? 0.f : Ls[w][col] * __builtin_amdgcn_exp2f(Ms[w][col] * a.c - mxc);
+  const float f = acc.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(acc.mc - mxc);
+  __syncthreads();
+  // the waves' outputs as [wave][d][32 rows]
+  constexpr int P = 33;
+  float* buf = reinterpret_cast<float*>(&ring[0][0][0][0]) + wave * (DP * P);
+  static_assert(4 * DP * P * 4 <= sizeof(ring), "the joined outputs fit the ring");
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) buf[(32 * dt + acc_row(i, lane)) * P + col] = acc.o[dt][i] * f;
+  __syncthreads();
+  // thread: row tid / 8, columns 8 (tid % 8) + 64 k
+  const float* all = reinterpret_cast<const float*>(&ring[0][0][0][0]);
+  const int orow = tid >> 3, grow = rt * 32 + orow;
+  const float rl = __shfl(l, orow), rm = __shfl(mxc, orow);   // the row's statistics, as lane `orow` holds them
+  if (grow >= rows) return;
+  const int otok = grow / G, ohead = u.kvh * G + grow % G;
+#pragma unroll
+  for (int k = 0; k < DP / 64; ++k) {
+    const int c0 = 8 * (tid & 7) + 64 * k;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v[e] += all[w * (DP * P) + (c0 + e) * P + orow];
+    }
+    if (c0 >= a.d) continue;
+    if (ns == 1) {
+      const float inv = rl > 0.f ? 1.f / rl : 0.f;
+      u32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+      *reinterpret_cast<u32x4*>(a.o.p + (s.q0 + otok) * a.o.token + (int64_t)ohead * a.o.head + c0) = o;
+    } else {
+      float* part = sp.part + (sp.row0[si] + ((int64_t)grow * a.kv_heads + u.kvh) * ns + split) * (int64_t)(a.d + 8);
+      *reinterpret_cast<f32x4*>(part + c0) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(part + c0 + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  }
+  if ((tid & 7) == 0) {
+    if (ns == 1) {
+      if (a.lse) a.lse[(int64_t)ohead * a.lse_stride + s.q0 + otok] = rl > 0.f ? rm * kLn2 + __logf(rl) : -INFINITY;
+    } else {
+      float* part = sp.part + (sp.row0[si] + ((int64_t)grow * a.kv_heads + u.kvh) * ns + split) * (int64_t)(a.d + 8);
+      part[a.d] = rl > 0.f ? rm : -INFINITY;
+      part[a.d + 1] = rl;
+    }
+  }
+}
+
+// Joins the ranges of attn_split_kernel: one wave per query row and head, ranges in order.
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnFwdArgs a, const AttnSeqs sq, const AttnSplit sp) {
+  const int lane = threadIdx.x & 63;
+  const int G = a.heads / a.kv_heads;
+  const int item = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);   // row of a joined sequence x key head
+  // sequences with one range have no items
+  const int f = lane < sq.count ? sp.join_first[lane] : 0x7FFFFFFF;
+  const int si = __builtin_amdgcn_readfirstlane((int)__popcll(__ballot(f <= item)) - 1);
+  if (item >= sp.join_first[sq.count]) return;
+  const AttnSeq s = sq.seq[si];
+  const int local = item - sp.join_first[si], ns = sp.nsplit[si];
+  const int grow = local / a.kv_heads, kvh = local % a.kv_heads;
+  const int tok = grow / G, head = kvh * G + grow % G;
+  const float* part = sp.part + (sp.row0[si] + (int64_t)local * ns) * (int64_t)(a.d + 8);
+  float mx = -INFINITY;
+  for (int k = 0; k < ns; ++k) mx = fmaxf(mx, part[(int64_t)k * (a.d + 8) + a.d]);
+  float l = 0.f, v0 = 0.f, v1 = 0.f;
+  const int c = 2 * lane;
+  for (int k = 0; k < ns; ++k) {
+    const float* p = part + (int64_t)k * (a.d + 8);
+    const float m = p[a.d];
+    const float w = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mx);
+    l += w * p[a.d + 1];
+    if (c < a.d) {
+      v0 += w * p[c];
+      v1 += w * p[c + 1];
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (c < a.d)
+    *reinterpret_cast<uint32_t*>(a.o.p + (s.q0 + tok) * a.o.token + (int64_t)head * a.o.head + c) =
+        pack_bf16x2(v0 * inv, v1 * inv);
+  if (a.lse && lane == 0)
+    a.lse[(int64_t)head * a.lse_stride + s.q0 + tok] = l > 0.f ? mx * kLn2 + __logf(l) : -INFINITY;
+}
+
+// ------------------------------------------------------------------------------------------
+// Backward, first launch: delta and dq. As the forward (128 query rows a workgroup, keys streamed),
+// with the probabilities recomputed from lse.
+template <int DP>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, const AttnSeqs sq) {
+  constexpr int BN = 64, KS = DP / 16, DT = DP / 32;
+  typedef Tile<DP> T;
+  typedef KvStream<DP, BN, 4> Stream;
+  __shared__ __attribute__((aligned(16))) uint16_t Ks[2][BN * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t Vs[2][BN * DP];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int G = a.heads / a.kv_heads;
+  const Unit u = unit_of((int)blockIdx.x, a.kv_heads, G);
+  const int si = find_seq(sq, u.tile);
+  const AttnSeq s = sq.seq[si];
+  const int qt = sq.first[si + 1] - 1 - u.tile;
+  const int head = u.kvh * G + u.sub;
+  const int r0 = qt * 128, shift = s.nk - s.nq;
+
+  const int row = r0 + wave * 32 + (lane & 31);
+  const bool own = row < s.nq;
+  bf16x8 qf[KS], gf[KS];
+  load_rows<DP>(qf, own ? a.q.p + (s.q0 + row) * a.q.token + (int64_t)head * a.q.head : nullptr, a.d, lane);
+  load_rows<DP>(gf, own ? a.dout.p + (s.q0 + row) * a.dout.token + (int64_t)head * a.dout.head : nullptr, a.d, lane);
+  float delta = 0.f, lse2 = 0.f;
+  {
+    bf16x8 of[KS];
+    load_rows<DP>(of, own ? a.o.p + (s.q0 + row) * a.o.token + (int64_t)head * a.o.head : nullptr, a.d, lane);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta = __fmaf_rn((float)gf[ks][e], (float)of[ks][e], delta);
+    delta = half_sum(delta);
+  }
+  const int64_t at = (int64_t)head * a.lse_stride + s.q0 + row;
+  if (own) {
+    lse2 = a.lse[at] * kLog2e;
+    if (lane < 32) a.delta[at] = delta;
+  }
+
+  const int r1 = min(s.nq, r0 + 128) - 1;
+  const int k_lo = visible(r0 + shift, s.nk, a.causal, a.window).lo & ~(BN - 1);
+  const int k_hi = visible(r1 + shift, s.nk, a.causal, a.window).hi;
+  const int w0 = r0 + wave * 32, w1 = min(s.nq - 1, w0 + 31);
+  const Range wa = visible(w0 + shift, s.nk, a.causal, a.window), wb = visible(w1 + shift, s.nk, a.causal, a.window);
+  const Range mine = visible(row + shift, s.nk, a.causal, a.window);
+  const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
+
+  Stream kv;
+  kv.init(a.k, a.v, s, u.kvh, a.d, wave, lane);
+  f32x16 dq[DT];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) dq[dt] = zero16();
+  if (nt > 0) kv.load(Ks[0], Vs[0], k_lo, wave);
+  for (int t = 0; t < nt; ++t) {
+    const int st = t & 1;
+    if (t + 1 < nt) {
+      kv.load(Ks[st ^ 1], Vs[st ^ 1], k_lo + (t + 1) * BN, wave);
+      wait_vmcnt<Stream::kLoads>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    lds_barrier();
+#pragma unroll
+    for (int kt = 0; kt < BN / 32; ++kt) {
+      const int j0 = k_lo + t * BN + 32 * kt;
+      if (j0 < wb.hi && j0 + 32 > wa.lo) {
+        f32x16 sc = zero16(), dp = zero16();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Ks[st], 32 * kt, ks, lane), qf[ks], sc);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) dp = mfma(T::rows(Vs[st], 32 * kt, ks, lane), gf[ks], dp);
+        const bool edge = j0 + 32 > wa.hi || j0 < wb.lo;
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int j = j0 + acc_row(i, lane);
+            const float p = __builtin_amdgcn_exp2f(__fmaf_rn(sc[i], a.c, -lse2));
+            dp[i] = (j >= mine.lo && j < mine.hi) ? p * (dp[i] - delta) : 0.f;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dp[i] = __builtin_amdgcn_exp2f(__fmaf_rn(sc[i], a.c, -lse2)) * (dp[i] - delta);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          const bf16x8 ds = pack8(dp, kk);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) dq[dt] = mfma(T::cols(Ks[st], 32 * kt + 16 * kk, dt, lane), ds, dq[dt]);
+        }
+      }
+    }
+    lds_barrier();
+  }
+  uint16_t* dst = own ? a.dq.p + (s.q0 + row) * a.dq.token + (int64_t)head * a.dq.head : nullptr;
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) store_cols(dst, dq[dt], a.scale, dt, a.d, lane);
+}
+
+// ------------------------------------------------------------------------------------------
+// Backward, second launch: dk and dv. A workgroup of 4 waves takes 128 keys of one key head, 32 per
+// wave, kept in registers; the rows of q and do of its query heads stream through LDS in tiles of 64,
+// two deep. The query heads of the group can be split over several workgroups (gper heads each):
+// their fp32 results go to the workspace, and attn_dkv_sum_kernel adds them in order.
+template <int DP, int ROWS, int NW>
+struct RowStream {   // rows [lo, hi) of q, do, lse and delta, head after head, in tiles of ROWS <= 64
+  typedef TileDma<DP, ROWS, NW> Dma;
+  static constexpr int kLoads = 2 * Dma::kLoads + 2;   // per wave and tile
+  Dma qd, gd;
+  const AttnBwdArgs& a;
+  int64_t q0;
+  int nq, head, i, lo, hi;
+  __device__ __forceinline__ RowStream(const AttnBwdArgs& args, const AttnSeq& s, int head0, int lo_, int hi_, int wave, int lane)
+      : a(args), q0(s.q0), nq(s.nq), head(head0), i(lo_), lo(lo_), hi(hi_) {
+    qd.init(wave, lane, a.d, (uint32_t)a.q.token);
+    gd.init(wave, lane, a.d, (uint32_t)a.dout.token);
+  }
+  // the next tile; lse and delta go to the wave's own copies. Rows past the sequence read 0: their q
+  // and do are 0 too, so they add nothing.
+  __device__ __forceinline__ void load(uint16_t* qt, uint16_t* gt, float* lt, float* dt, int wave, int lane) {
+    const int64_t tok = q0 + i, at = (int64_t)head * a.lse_stride + tok;
+    const int rows = nq - i, nrec = min(ROWS, rows) * 4;
+    qd.load(qt, a.q.p + tok * a.q.token + (int64_t)head * a.q.head, rows, a.d, (uint32_t)a.q.token, wave);
+    gd.load(gt, a.dout.p + tok * a.dout.token + (int64_t)head * a.dout.head, rows, a.d, (uint32_t)a.dout.token, wave);
+    __amdgpu_buffer_rsrc_t rl = __builtin_amdgcn_make_buffer_rsrc((void*)(a.lse + at), (short)0, nrec, kRsrcFlags);
+    __amdgpu_buffer_rsrc_t rd = __builtin_amdgcn_make_buffer_rsrc((void*)(a.delta + at), (short)0, nrec, kRsrcFlags);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rl, (lds_void*)lt, 4, (uint32_t)lane * 4u, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_void*)dt, 4, (uint32_t)lane * 4u, 0, 0, 0);
+    i += ROWS;
+    if (i >= hi) {
+      i = lo;
+      ++head;
+    }
+  }
+};
+
+template <int DP>
+__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdArgs a, const AttnSeqs sq, const AttnKvSplit sp) {
+  constexpr int BM = 64, KS = DP / 16, DT = DP / 32;
+  typedef Tile<DP> T;
+  typedef RowStream<DP, BM, 4> Stream;
+  __shared__ __attribute__((aligned(16))) uint16_t Qs[2][BM * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t Gs[2][BM * DP];
+  __shared__ __attribute__((aligned(16))) float Ls[2][4][BM], Ds[2][4][BM];   // lse and delta, a copy per wave
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int G = a.heads / a.kv_heads;
+  const Unit u = unit_of((int)blockIdx.x, a.kv_heads, sp.splits);
+  const int si = find_seq(sq, u.tile);
+  const AttnSeq s = sq.seq[si];
+  const int j0 = (u.tile - sq.first[si]) * 128;     // first key of the workgroup
+  const int shift = s.nk - s.nq;
+  const int key = j0 + wave * 32 + (lane & 31);
+  const bool own = key < s.nk;
+  bf16x8 kf[KS], vf[KS];
+  load_rows<DP>(kf, own ? a.k.p + (s.k0 + key) * a.k.token + (int64_t)u.kvh * a.k.head : nullptr, a.d, lane);
+  load_rows<DP>(vf, own ? a.v.p + (s.k0 + key) * a.v.token + (int64_t)u.kvh * a.v.head : nullptr, a.d, lane);
+
+  // query rows [i_lo, i_hi) that see some key of the workgroup
+  const int jl = min(s.nk, j0 + 128) - 1;
+  const int i_lo = (a.causal ? max(0, j0 - shift) : 0) & ~(BM - 1);
+  const int i_hi = a.window ? (int)min((int64_t)s.nq, (int64_t)jl + a.window - shift) : s.nq;
+  const int tiles = i_hi > i_lo ? (i_hi - i_lo + BM - 1) / BM : 0;
+  const int g0 = u.sub * sp.gper, g1 = min(G, g0 + sp.gper);
+  const int total = tiles * (g1 - g0);
+  // rows [c_lo, c_hi) see the lane's key
+  const int c_lo = a.causal ? key - shift : INT_MIN;
+  const int64_t c_hi64 = (int64_t)key + a.window - shift;
+  const int c_hi = a.window ? (int)min(c_hi64, (int64_t)INT_MAX) : INT_MAX;
+  // and of the wave's keys: rows in [all_lo, all_hi) see all, rows in [any_lo, any_hi) see some
+  const int kw = j0 + wave * 32;
+  const int any_lo = a.causal ? kw - shift : INT_MIN, all_lo = a.causal ? kw + 31 - shift : INT_MIN;
+  const int all_hi = a.window ? (int)min((int64_t)kw + a.window - shift, (int64_t)INT_MAX) : INT_MAX;
+  const int any_hi = a.window ? (int)min((int64_t)kw + 31 + a.window - shift, (int64_t)INT_MAX) : INT_MAX;
+
+  Stream rows(a, s, u.kvh * G + g0, i_lo, i_hi, wave, lane);
+
+  f32x16 dk[DT], dv[DT];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) {
+    dk[dt] = zero16();
+    dv[dt] = zero16();
+  }
+  if (total > 0) rows.load(Qs[0], Gs[0], Ls[0][wave], Ds[0][wave], wave, lane);
+  int ci = i_lo;   // first row of the tile in work
+  for (int t = 0; t < total; ++t) {
+    const int st = t & 1;
+    if (t + 1 < total) {
+      rows.load(Qs[st ^ 1], Gs[st ^ 1], Ls[st ^ 1][wave], Ds[st ^ 1][wave], wave, lane);
+      wait_vmcnt<Stream::kLoads>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    lds_barrier();
+#pragma unroll
+    for (int mt = 0; mt < BM / 32; ++mt) {
+      const int i0 = ci + 32 * mt;
+      if (i0 + 31 >= any_lo && i0 < any_hi) {
+        f32x16 sc = zero16(), dp = zero16();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Qs[st], 32 * mt, ks, lane), kf[ks], sc);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) dp = mfma(T::rows(Gs[st], 32 * mt, ks, lane), vf[ks], dp);
+        const bool edge = i0 < all_lo || i0 + 31 >= all_hi;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int m = 32 * mt + 8 * g + 4 * (lane >> 5);
+          const f32x4 ls = *reinterpret_cast<const f32x4*>(&Ls[st][wave][m]);
+          const f32x4 dl = *reinterpret_cast<const f32x4*>(&Ds[st][wave][m]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float p = __builtin_amdgcn_exp2f(__fmaf_rn(sc[4 * g + e], a.c, -ls[e] * kLog2e));
+            if (edge) {
+              const int i = ci + m + e;
+              p = (i >= c_lo && i < c_hi) ? p : 0.f;
+            }
+            sc[4 * g + e] = p;
+            dp[4 * g + e] = p * (dp[4 * g + e] - dl[e]);
+          }
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          const bf16x8 p = pack8(sc, kk), ds = pack8(dp, kk);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) dv[dt] = mfma(T::cols(Gs[st], 32 * mt + 16 * kk, dt, lane), p, dv[dt]);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) dk[dt] = mfma(T::cols(Qs[st], 32 * mt + 16 * kk, dt, lane), ds, dk[dt]);
+        }
+      }
+    }
+    ci += BM;
+    if (ci >= i_hi) ci = i_lo;
+    lds_barrier();
+  }
+  if (sp.splits == 1) {
+    uint16_t* pk = own ? a.dk.p + (s.k0 + key) * a.dk.token + (int64_t)u.kvh * a.dk.head : nullptr;
+    uint16_t* pv = own ? a.dv.p + (s.k0 + key) * a.dv.token + (int64_t)u.kvh * a.dv.head : nullptr;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      store_cols(pk, dk[dt], a.scale, dt, a.d, lane);
+      store_cols(pv, dv[dt], 1.f, dt, a.d, lane);
+    }
+  } else {
+    // accumulators as they lie in the lanes: [tile][key head][split][wave][dk, dv][DT][4][lane][4]
+    float* dst = sp.part + ((((int64_t)u.tile * a.kv_heads + u.kvh) * sp.splits + u.sub) * 4 + wave) * (2 * 32 * DP) + 4 * lane;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f32x4 x, y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = dk[dt][4 * g + e];
+          y[e] = dv[dt][4 * g + e];
+        }
+        *reinterpret_cast<f32x4*>(dst + (dt * 4 + g) * 256) = x;
+        *reinterpret_cast<f32x4*>(dst + 32 * DP + (dt * 4 + g) * 256) = y;
+      }
+  }
+}
+
+// Sums the split results of attn_dkv_kernel in split order: a workgroup per key tile, key head and one
+// of dk, dv; a wave per 32 keys.
+template <int DP>
+__global__ __launch_bounds__(256) void attn_dkv_sum_kernel(const AttnBwdArgs a, const AttnSeqs sq, const AttnKvSplit sp) {
+  constexpr int DT = DP / 32;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int which = (int)blockIdx.x & 1;
+  const int kvh = ((int)blockIdx.x >> 1) % a.kv_heads, tile = ((int)blockIdx.x >> 1) / a.kv_heads;
+  const int si = find_seq(sq, tile);
+  const AttnSeq s = sq.seq[si];
+  const int key = (tile - sq.first[si]) * 128 + wave * 32 + (lane & 31);
+  const float* src = sp.part + (((int64_t)tile * a.kv_heads + kvh) * sp.splits * 4 + wave) * (2 * 32 * DP) + which * 32 * DP + 4 * lane;
+  f32x16 v[DT];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) v[dt] = zero16();
+  for (int k = 0; k < sp.splits; ++k) {
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(src + (dt * 4 + g) * 256);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[dt][4 * g + e] += x[e];
+      }
+    src += 4 * (2 * 32 * DP);
+  }
+  const AttnTensor o = which ? a.dv : a.dk;
+  uint16_t* dst = key < s.nk ? o.p + (s.k0 + key) * o.token + (int64_t)kvh * o.head : nullptr;
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) store_cols(dst, v[dt], which ? 1.f : a.scale, dt, a.d, lane);
+}
+
+// ------------------------------------------------------------------------------------------
+// Host side: sequences in order of falling length, in launches of up to kAttnSeqs.
+static int64_t ceil64(int64_t x, int64_t y) { return (x + y - 1) / y; }
+
+// the heaviest sequences first, so that the last workgroups to start are short ones
+static std::vector<AttnSeq> by_work(const AttnSeq* seqs, int64_t count, bool keys) {
+  std::vector<AttnSeq> v;
+  v.reserve((size_t)count);
+  for (int64_t i = 0; i < count; ++i)
+    if (keys ? seqs[i].nk > 0 : seqs[i].nq > 0) v.push_back(seqs[i]);
+  std::stable_sort(v.begin(), v.end(), [](const AttnSeq& x, const AttnSeq& y) { return x.nk > y.nk; });
+  return v;
+}
+
+// one launch's sequences, `tiles_of(seq)` workgroup tiles each
+template <typename F>
+static AttnSeqs pack_seqs(const std::vector<AttnSeq>& v, size_t from, F tiles_of) {
+  AttnSeqs q{};
+  for (size_t i = from; i < v.size() && q.count < kAttnSeqs; ++i) {
+    q.seq[q.count] = v[i];
+    q.first[q.count + 1] = q.first[q.count] + (int)tiles_of(v[i]);
+    ++q.count;
+  }
+  return q;
+}
+
+static int q_tiles(const AttnSeq& s) { return (int)ceil64(s.nq, 128); }
+static int k_tiles(const AttnSeq& s) { return (int)ceil64(s.nk, 128); }
+
+// first key that the first row of the sequence can see
+static int64_t first_key(const AttnSeq& s, int window) {
+  return window ? std::max<int64_t>(0, (int64_t)s.nk - s.nq - window + 1) : 0;
+}
+
+// The forward's plan: attn_fwd_kernel when its workgroups fill the GPU, else attn_split_kernel, with
+// the key ranges as long as give about 512 workgroups (two a compute unit).
+struct FwdPlan {
+  bool split;
+  int64_t chunk;         // keys per range
+  int64_t part_floats;   // workspace of one launch (the largest)
+};
+static int split_count(const AttnSeq& s, int window, int64_t chunk) {
+  const int64_t lo = first_key(s, window) & ~int64_t(31);
+  return (int)std::max<int64_t>(1, ceil64(s.nk - lo, chunk));
+}
+static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, int d, int window) {
+  FwdPlan p{false, 0, 0};
+  const int G = heads / kv_heads;
+  int64_t wgs = 0, key_tiles = 0;
+  for (const AttnSeq& s : v) {
+    wgs += (int64_t)q_tiles(s) * heads;
+    key_tiles += ceil64((int64_t)s.nq * G, 32) * ceil64(s.nk - first_key(s, window), 128) * kv_heads;
+  }
+  if (wgs >= 256 && v[0].nq > 16) return p;
+  p.split = true;
+  p.chunk = 128 * std::max<int64_t>(2, ceil64(key_tiles, 512));
+  for (size_t from = 0; from < v.size(); from += kAttnSeqs) {
+    int64_t f = 0;
+    for (size_t i = from; i < v.size() && i < from + kAttnSeqs; ++i) {
+      const int ns = split_count(v[i], window, p.chunk);
+      if (ns > 1) f += (int64_t)v[i].nq * heads * ns * (d + 8);
+    }
+    p.part_floats = std::max(p.part_floats, f);
+  }
+  return p;
+}
+
+// Splits of the dk, dv launch over the query heads of a group, for about 512 workgroups.
+static int kv_splits(const std::vector<AttnSeq>& v, int heads, int kv_heads) {
+  const int G = heads / kv_heads;
+  int64_t wgs = 0;
+  for (const AttnSeq& s : v) wgs += (int64_t)k_tiles(s) * kv_heads;
+  if (wgs == 0) return 1;
+  const int64_t want = std::min<int64_t>(G, ceil64(512, wgs));
+  const int gper = (int)ceil64(G, want);
+  return (int)ceil64(G, gper);
+}
+static int64_t dkv_part_floats(const std::vector<AttnSeq>& v, int heads, int kv_heads, int dp) {
+  const int splits = kv_splits(v, heads, kv_heads);
+  if (splits == 1) return 0;
+  int64_t most = 0;
+  for (size_t from = 0; from < v.size(); from += kAttnSeqs) {
+    int64_t t = 0;
+    for (size_t i = from; i < v.size() && i < from + kAttnSeqs; ++i) t += k_tiles(v[i]);
+    most = std::max(most, t * kv_heads * splits * (128 * 2 * dp));
+  }
+  return most;
+}
+static int padded_d(int d) { return d <= 64 ? 64 : 128; }
+static int64_t round64(int64_t f) { return (f + 63) & ~int64_t(63); }
+
+size_t attn_fwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window) {
+  const std::vector<AttnSeq> v = by_work(seqs, count, false);
+  return v.empty() ? 0 : (size_t)fwd_plan(v, heads, kv_heads, d, window).part_floats;
+}
+size_t attn_bwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int64_t q_tokens) {
+  const std::vector<AttnSeq> v = by_work(seqs, count, true);
+  return (size_t)(round64(q_tokens * heads) + dkv_part_floats(v, heads, kv_heads, padded_d(d)));
+}
+
+hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream) {
+  const std::vector<AttnSeq> v = by_work(seqs, count, false);
+  if (v.empty()) return hipSuccess;
+  const int G = a.heads / a.kv_heads;
+  const FwdPlan plan = fwd_plan(v, a.heads, a.kv_heads, a.d, a.window);
+  for (size_t from = 0; from < v.size(); from += kAttnSeqs) {
+    if (!plan.split) {
+      const AttnSeqs q = pack_seqs(v, from, q_tiles);
+      const dim3 grid((unsigned)(q.first[q.count] * a.heads));
+      if (a.d <= 64) hipLaunchKernelGGL(attn_fwd_kernel<64>, grid, dim3(256), 0, stream, a, q);
+      else hipLaunchKernelGGL(attn_fwd_kernel<128>, grid, dim3(256), 0, stream, a, q);
+    } else {
+      const AttnSeqs q = pack_seqs(v, from, [&](const AttnSeq& s) {
+        return ceil64((int64_t)s.nq * G, 32) * split_count(s, a.window, plan.chunk);
+      });
+      AttnSplit sp{};
+      sp.part = ws;
+      sp.chunk = (int)plan.chunk;
+      int64_t row0 = 0;
+      for (int i = 0; i < q.count; ++i) {
+        sp.lo[i] = (int)(first_key(q.seq[i], a.window) & ~int64_t(31));
+        sp.nsplit[i] = split_count(q.seq[i], a.window, plan.chunk);
+        sp.row0[i] = row0;
+        const int64_t items = sp.nsplit[i] > 1 ? (int64_t)q.seq[i].nq * a.heads : 0;
+        row0 += items * sp.nsplit[i];
+        sp.join_first[i + 1] = sp.join_first[i] + (int)items;
+      }
+      const dim3 grid((unsigned)(q.first[q.count] * a.kv_heads));
+      if (a.d <= 64) hipLaunchKernelGGL(attn_split_kernel<64>, grid, dim3(256), 0, stream, a, q, sp);
+      else hipLaunchKernelGGL(attn_split_kernel<128>, grid, dim3(256), 0, stream, a, q, sp);
+      const int items = sp.join_first[q.count];
+      if (items) hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a, q, sp);
+    }
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_bwd(const AttnBwdArgs& args, const AttnSeq* seqs, int64_t count, int64_t q_tokens, float* ws,
+                           hipStream_t stream) {
+  AttnBwdArgs a = args;
+  a.delta = ws;
+  const std::vector<AttnSeq> vq = by_work(seqs, count, false), vk = by_work(seqs, count, true);
+  for (size_t from = 0; from < vq.size(); from += kAttnSeqs) {
+    const AttnSeqs q = pack_seqs(vq, from, q_tiles);
+    const dim3 grid((unsigned)(q.first[q.count] * a.heads));
+    if (a.d <= 64) hipLaunchKernelGGL(attn_dq_kernel<64>, grid, dim3(256), 0, stream, a, q);
+    else hipLaunchKernelGGL(attn_dq_kernel<128>, grid, dim3(256), 0, stream, a, q);
+  }
+  AttnKvSplit sp{};
+  sp.splits = kv_splits(vk, a.heads, a.kv_heads);
+  sp.gper = (int)ceil64(a.heads / a.kv_heads, sp.splits);
+  sp.part = ws + round64(q_tokens * a.heads);
+  for (size_t from = 0; from < vk.size(); from += kAttnSeqs) {
+    const AttnSeqs q = pack_seqs(vk, from, k_tiles);
+    const int units = q.first[q.count] * a.kv_heads;
+    const dim3 grid((unsigned)(units * sp.splits)), sums((unsigned)(units * 2));
+    if (a.d <= 64) {
+      hipLaunchKernelGGL(attn_dkv_kernel<64>, grid, dim3(256), 0, stream, a, q, sp);
+      if (sp.splits > 1) hipLaunchKernelGGL(attn_dkv_sum_kernel<64>, sums, dim3(256), 0, stream, a, q, sp);
+    } else {
+      hipLaunchKernelGGL(attn_dkv_kernel<128>, grid, dim3(256), 0, stream, a, q, sp);
+      if (sp.splits > 1) hipLaunchKernelGGL(attn_dkv_sum_kernel<128>, sums, dim3(256), 0, stream, a, q, sp);
+    }
+  }
+  return hipGetLastError();
+}
+
+}  // namespace nf4

@@ -124,6 +124,11 @@ size_t lora_dx_group_ws_floats(int count, int64_t M, int64_t K, int r);
 hipError_t launch_lora_dx_group(int count, const uint16_t* X, int64_t M, int64_t K, const float* const* v, int r,
                                 float scale, int accumulate, float* ws, float* const* dA, hipStream_t stream);
 
+// dA_i = scale * (sum over `parts` partial sums part_i [parts][K][r], in order) (+ dA_i), transposed to
+// [r][K], for count (<= 4) linears in one launch
+hipError_t launch_lora_sum(int count, const float* const* part, int parts, int64_t K, int r, float scale,
+                           int accumulate, float* const* dA, hipStream_t stream);
+
 // Skinny forward (M <= 16): split-K dequant-GEMV on MFMA with a deterministic reduction.
 // `part` holds skinny_workspace_floats(M, N, K, r) floats; u_out receives u = x A^T [M x r].
 bool skinny_eligible(int64_t M, int64_t N, int64_t K);
@@ -164,5 +169,84 @@ hipError_t launch_q4_quantize(const float* w, int64_t numel, int book, int block
 hipError_t launch_q4_dequant(const uint8_t* packed, const float* absmax, const uint8_t* scale_q,
                              const float* scale_c2, int64_t numel, int book, int blocksize, uint16_t* out,
                              hipStream_t stream);
+
+// ---- Attention (attn.hip). A sequence: nq query tokens from q0, nk key tokens from k0.
+struct AttnSeq {
+  int64_t q0, k0;
+  int nq, nk;
+};
+constexpr int kAttnSeqs = 64;   // sequences per launch, passed by value in the kernel arguments
+struct AttnSeqs {
+  int count;
+  int first[kAttnSeqs + 1];     // prefix sums of the sequences' workgroup tiles
+  AttnSeq seq[kAttnSeqs];
+};
+struct AttnTensor {             // element (token, head, i) at p[token * token + head * head + i]
+  uint16_t* p;
+  int64_t token, head;
+};
+struct AttnFwdArgs {
+  AttnTensor q, k, v, o;
+  float* lse;                   // [heads][lse_stride] or null
+  int64_t lse_stride;
+  int heads, kv_heads, d, causal, window;
+  float c;                      // scale * log2(e)
+};
+struct AttnBwdArgs {
+  AttnTensor q, k, v, o, dout, dq, dk, dv;
+  const float* lse;
+  float* delta;                 // [heads][lse_stride], set by launch_attn_bwd
+  int64_t lse_stride;
+  int heads, kv_heads, d, causal, window;
+  float c, scale;
+};
+struct AttnSplit {              // ranges of keys of the few-row forward
+  float* part;                  // per row, key head and range: d outputs, maximum, sum, 6 unused
+  int chunk;
+  int lo[kAttnSeqs], nsplit[kAttnSeqs];
+  int64_t row0[kAttnSeqs];      // first record of a sequence in part
+  int join_first[kAttnSeqs + 1];
+};
+struct AttnKvSplit {            // split of a group's query heads in the dk, dv launch
+  float* part;
+  int splits, gper;
+};
+// Workspace in floats; window 0: none
+size_t attn_fwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window);
+size_t attn_bwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int64_t q_tokens);
+hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream);
+hipError_t launch_attn_bwd(const AttnBwdArgs& a, const AttnSeq* seqs, int64_t count, int64_t q_tokens, float* ws,
+                           hipStream_t stream);
+
+// ---- 8-bit activation checkpoints (act8.hip; format in act8.h). numel a multiple of 64.
+hipError_t launch_act8_pack(const uint16_t* x, int64_t numel, int8_t* codes, uint16_t* absmax, hipStream_t stream);
+hipError_t launch_act8_unpack(const int8_t* codes, const uint16_t* absmax, int64_t numel, uint16_t* x, hipStream_t stream);
+// dA_i = scale * v_i^T x (+ dA_i if accumulate) for count (<= 4) linears that share x, kept in 8 bits;
+// ws holds act8_grad_ws_floats floats
+size_t act8_grad_ws_floats(int count, int64_t M, int64_t K, int r);
+hipError_t launch_act8_grad(int count, const int8_t* codes, const uint16_t* absmax, int64_t M, int64_t K,
+                            const float* const* v, int r, float scale, int accumulate, float* ws, float* const* dA,
+                            hipStream_t stream);
+
+// ---- Root-mean-square norm (norm.hip). K a multiple of 8 (of 64 with codes), at most 16384.
+struct NormFwdArgs {
+  const uint16_t *x, *res, *w;    // [M x K], [M x K] or null, [K]
+  int64_t M, K;
+  float eps;
+  uint16_t *h, *y;                // [M x K] or null, [M x K]
+  float* rstd;                    // [M] or null
+  int8_t* codes;                  // [M x K] or null
+  uint16_t* absmax;               // [M x K / 64], with codes
+};
+struct NormBwdArgs {
+  const uint16_t *dy, *dh, *h, *w;   // dh may be null
+  const float* rstd;
+  int64_t M, K;
+  uint16_t* dx;
+};
+hipError_t launch_rmsnorm_fwd(const NormFwdArgs& a, hipStream_t stream);
+// dw: [K] or null; ws holds norm_bwd_ws_floats floats where dw is asked for
+size_t norm_bwd_ws_floats(int64_t M, int64_t K);
+hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, float* dw, int accumulate, float* ws, hipStream_t stream);
 
 }  // namespace nf4

@@ -18,6 +18,8 @@
  *                     such a merged weight again.
  *   qlora_adamw_plan_*   sections "The algorithm, step by step" and "Minimal implementation":
  *                     global gradient-norm clipping, then AdamW over A and B.
+ *   qlora_act8_*, qlora_linear_bwd_act8, qlora_rmsnorm_*, qlora_attn_*   what a layer runs around its
+ *                     adapted linears: 8-bit activation checkpoints, the norm and the attention.
  *   q4_*              sections "A toy run" and "Double quantisation": FP4 and INT4 codebooks,
  *                     blocksizes 16..4096, and fp32 scales without double quantisation.
  *
@@ -335,6 +337,122 @@ int qlora_adamw_plan_step(const qlora_adamw_plan *plan, const qlora_adamw_config
 
 /* Free the plan (its device memory). No step on it may still be running. NULL is a no-op. */
 int qlora_adamw_plan_destroy(qlora_adamw_plan *plan);
+
+/* ---- 8-bit activation checkpoints. Training keeps the input of every adapted linear for dA; kept in
+ * 8 bits it takes 1.03 bytes per value instead of 2, and the backward reads that much less.
+ * Format of a row-major M x K activation, K % 64 == 0, blocks of 64 along K:
+ *   absmax  uint16[M*K/64]: bf16 bits of the block's largest |x| (exact, as x is bf16);
+ *   codes   int8[M*K]: round(127 x / absmax), the nearest integer of the exact quotient, ties to even;
+ *           a block of zeros has absmax 0 and codes 0.
+ * A code stands for code * absmax / 127: within absmax / 254 of x. */
+typedef struct {
+  int8_t *codes;      /* [M*K]    */
+  uint16_t *absmax;   /* [M*K/64] */
+} qlora_act8;
+
+/* x [numel] bf16 to its checkpoint; numel % 64 == 0. One launch.
+ * Errors: NF4_ERR_SHAPE, NF4_ERR_NULL, NF4_ERR_ALIGN, NF4_ERR_HIP. */
+int qlora_act8_pack(const uint16_t *x, int64_t numel, int8_t *codes, uint16_t *absmax, hipStream_t stream);
+
+/* The values the checkpoint stands for, rounded to bf16. One launch. Errors as qlora_act8_pack. */
+int qlora_act8_unpack(const int8_t *codes, const uint16_t *absmax, int64_t numel, uint16_t *x, hipStream_t stream);
+
+/* Backward of 1..4 adapted linears that share an input kept as an 8-bit checkpoint x8 [M x K]: as
+ * qlora_linear_bwd_group, with dA_i = s (dY_i B_i)^T x8 over the values that the codes stand for
+ * (exactly code * absmax / 127, not their bf16 rounding). dX and dB do not read the input and equal
+ * qlora_linear_bwd_group's bit for bit. The sums over rows run in a fixed order.
+ *   ws: at least qlora_workspace_bytes_act8(count, N, M, K, r) bytes.
+ * Errors: as qlora_linear_bwd_group; NF4_ERR_NULL also for x8 or one of its arrays. */
+int qlora_linear_bwd_act8(int32_t count, const nf4_weight *const *W, const qlora_act8 *x8,
+                          const uint16_t *const *dy, int64_t M, const uint16_t *const *A,
+                          const uint16_t *const *B, int32_t r, float scale, const float *const *u,
+                          uint16_t *const *dx, float *const *dA, float *const *dB, int accumulate,
+                          void *ws, size_t ws_bytes, hipStream_t stream);
+/* Workspace bytes of qlora_linear_bwd_act8; 0 for sizes it refuses. N is a HOST array. */
+size_t qlora_workspace_bytes_act8(int32_t count, const int64_t *N, int64_t M, int64_t K, int32_t r);
+
+/* ---- Root-mean-square norm with the residual's addition (bf16 in and out, fp32 inside, each output
+ * rounded once). K % 8 == 0 (K % 64 == 0 with a checkpoint), 8 <= K <= 16384, 0 <= M < 2^31; M == 0
+ * is a no-op.
+ *   h = x + residual;  rstd = (mean(h^2) + eps)^(-1/2) per row;  y = h * rstd * weight
+ * (the statistics and y from h before its rounding).
+ *   residual [M x K] or NULL (h = x);  weight [K];  eps >= 0.
+ *   h [M x K] or NULL: the sum, the next residual (may be x's or residual's own memory);
+ *   y [M x K] (may be x's own memory);  rstd [M] float or NULL (saved for qlora_rmsnorm_bwd);
+ *   y8: NULL, or receives the 8-bit checkpoint of the rounded y, bit for bit what qlora_act8_pack
+ *       makes of y.
+ * Errors: NF4_ERR_SHAPE (M, K, eps), NF4_ERR_NULL, NF4_ERR_ALIGN, NF4_ERR_HIP. */
+int qlora_rmsnorm_fwd(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, int64_t M,
+                      int64_t K, float eps, uint16_t *h, uint16_t *y, float *rstd, const qlora_act8 *y8,
+                      hipStream_t stream);
+
+/* Its backward, from the stored h and rstd: with n = h * rstd,
+ *   dx = dh + rstd * (weight * dy - n * mean(weight * dy * n))   [M x K] bf16: the gradient of x and of
+ *        residual alike; may be dy's or dh's own memory;
+ *   dw = sum over rows of dy * n   [K] float, or NULL (a frozen weight); accumulate adds into it.
+ *   dh [M x K] bf16: what flows into h itself, or NULL.
+ *   ws: with dw, at least qlora_rmsnorm_workspace_bytes(M, K) bytes.
+ * The sum over rows runs in a fixed order. Errors: as the forward, and NF4_ERR_WORKSPACE. */
+int qlora_rmsnorm_bwd(const uint16_t *dy, const uint16_t *dh, const uint16_t *h, const uint16_t *weight,
+                      const float *rstd, int64_t M, int64_t K, uint16_t *dx, float *dw, int accumulate,
+                      void *ws, size_t ws_bytes, hipStream_t stream);
+size_t qlora_rmsnorm_workspace_bytes(int64_t M, int64_t K);   /* 0 for refused sizes */
+
+/* ---- Attention over sequences of a batch, forward and backward (bf16 tensors, fp32 scores, softmax
+ * statistics and sums; the probabilities and their gradients are rounded to bf16 as operands of the
+ * second products). Query i of a sequence with nq queries and nk keys stands at position
+ * p = nk - nq + i of the sequence's keys and sees key j when
+ *   (not causal or j <= p) and (window == 0 or j > p - window).
+ *   z_ij = scale q_i.k_j;  lse_i = ln sum_j exp(z_ij);  o_i = sum_j exp(z_ij - lse_i) v_j.
+ * A query that sees no key gives o = 0, lse = -inf and no gradient. Queries and keys outside every
+ * sequence are neither read nor written. heads / kv_heads query heads share a key head in turn. */
+typedef struct {
+  int64_t q0, nq;   /* query tokens q0 .. q0 + nq - 1 of q, o, lse and their gradients; nq >= 0 */
+  int64_t k0, nk;   /* key tokens k0 .. k0 + nk - 1 of k, v and their gradients; nk >= 0 */
+} qlora_attn_seq;
+typedef struct {
+  int32_t heads, kv_heads;      /* heads a multiple of kv_heads */
+  int32_t d;                    /* head size: a multiple of 8 in 8..128 */
+  int32_t causal;
+  int64_t window;               /* 0: none */
+  float scale;                  /* > 0 */
+  int64_t q_tokens, k_tokens;   /* tokens that the tensors hold */
+} qlora_attn_config;
+/* Element (token, head, i) at data[token * token_stride + head * head_stride + i], strides in elements,
+ * multiples of 8; d <= token_stride < 2^22. Slices of a projection's output, [tokens][heads][d] and
+ * [heads][tokens][d] all fit. */
+typedef struct {
+  uint16_t *data;
+  int64_t token_stride, head_stride;
+} qlora_attn_tensor;
+
+/* Forward. seqs: HOST array of count entries, their query ranges in ascending order and apart (key
+ * ranges may be shared and in any order, as for caches); packed training batches and padded or shared
+ * caches are both lists of such sequences. Up to 64 sequences travel in one launch's arguments.
+ *   lse   [heads][q_tokens] float output, or NULL (it is needed by the backward).
+ *   ws    at least qlora_attn_workspace_bytes(cfg, count, seqs, 0) bytes (0: may be NULL).
+ * Few queries over many keys (decoding) split the keys over the GPU and join the parts in order.
+ * Errors: NF4_ERR_SHAPE (sizes, strides, overlapping or outlying sequences), NF4_ERR_NULL,
+ * NF4_ERR_ALIGN, NF4_ERR_WORKSPACE, NF4_ERR_HIP (also when host memory runs out). */
+int qlora_attn_fwd(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs,
+                   const qlora_attn_tensor *q, const qlora_attn_tensor *k, const qlora_attn_tensor *v,
+                   const qlora_attn_tensor *o, float *lse, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Backward, from the forward's o and lse and the gradient dout of o, recomputing the probabilities:
+ * with delta_i = dout_i.o_i and dS_ij = exp(z_ij - lse_i) (dout_i.v_j - delta_i),
+ *   dq_i = scale sum_j dS_ij k_j;  dk_j = scale sum_i dS_ij q_i;  dv_j = sum_i exp(z_ij - lse_i) dout_i,
+ * dk and dv summed over the query heads that share the key head. Key ranges too must be in ascending
+ * order and apart. No atomics: the sums run in a fixed order. dq, dk, dv must not overlap any input.
+ *   ws    at least qlora_attn_workspace_bytes(cfg, count, seqs, 1) bytes.
+ * Errors: as qlora_attn_fwd. */
+int qlora_attn_bwd(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs,
+                   const qlora_attn_tensor *q, const qlora_attn_tensor *k, const qlora_attn_tensor *v,
+                   const qlora_attn_tensor *o, const float *lse, const qlora_attn_tensor *dout,
+                   const qlora_attn_tensor *dq, const qlora_attn_tensor *dk, const qlora_attn_tensor *dv,
+                   void *ws, size_t ws_bytes, hipStream_t stream);
+/* Workspace bytes of qlora_attn_fwd (backward 0) or qlora_attn_bwd (1); 0 for refused arguments. */
+size_t qlora_attn_workspace_bytes(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs,
+                                  int backward);
 
 /* Workspace bytes that qlora_linear_fwd and qlora_linear_bwd need for these sizes (the larger of
  * the two). Returns 0 for invalid sizes. */

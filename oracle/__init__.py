@@ -22,6 +22,7 @@ from .nf4 import (NF4_ZERO_INDEX, codebook, quantize_blocks, pack_nibbles, unpac
 from .linear import linear_fwd, linear_bwd, linear_fwd_f64, linear_bwd_f64, linear_bwd_sampled
 from .merge import bf16_bits_from_f64, merge
 from .optim import AdamWConfig, global_grad_norm, clip_coefficient, adamw_step
+from .layer import (visible, attention_head, attention, rmsnorm, rmsnorm_bwd, act8, act8_values)
 from .toy import int4_codebook, fp4_codebook, relative_mse, residual_capture
 
 __all__ = [
@@ -30,5 +31,6 @@ __all__ = [
     "f32_from_bf16_bits", "dequant", "storage_bits", "quantize_with", "dequant_blocks", "linear_fwd", "linear_bwd", "linear_fwd_f64",
     "linear_bwd_f64", "linear_bwd_sampled", "bf16_bits_from_f64", "merge", "AdamWConfig",
     "global_grad_norm", "clip_coefficient", "adamw_step", "int4_codebook",
+    "visible", "attention_head", "attention", "rmsnorm", "rmsnorm_bwd", "act8", "act8_values",
     "fp4_codebook", "relative_mse", "residual_capture",
 ]

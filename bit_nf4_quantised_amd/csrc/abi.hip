@@ -666,7 +666,7 @@ int qlora_attn_bwd(const qlora_attn_config* cfg, int64_t count, const qlora_attn
     const size_t need = nf4::attn_bwd_ws_floats(s.data(), count, cfg->heads, cfg->kv_heads, cfg->d, tq) * 4;
     if (need && (!ws || ws_bytes < need)) return NF4_ERR_WORKSPACE;
     const nf4::AttnBwdArgs a{attn_tensor(q), attn_tensor(k), attn_tensor(v), attn_tensor(o), attn_tensor(dout), attn_tensor(dq),
-                             attn_tensor(dk), attn_tensor(dv), lse, nullptr, tq, cfg->heads, cfg->kv_heads, cfg->d,
+                             attn_tensor(dk), attn_tensor(dv), lse, nullptr, nullptr, tq, cfg->heads, cfg->kv_heads, cfg->d,
                              cfg->causal != 0, attn_window(cfg), cfg->scale * 1.4426950408889634f, cfg->scale};
     return from_hip(nf4::launch_attn_bwd(a, s.data(), count, tq, static_cast<float*>(ws), stream));
   } catch (...) {

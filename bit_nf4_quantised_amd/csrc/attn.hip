@@ -161,8 +161,25 @@ __device__ __forceinline__ bf16x8 pack8(const f32x16& v, int s) {
   return __builtin_bit_cast(bf16x8, p);
 }
 
+// Ties a value to its place in the program. Used in blocks that few iterations need, which the compiler
+// would otherwise run every time, with selects.
+__device__ __forceinline__ void pin(f32x16& v) { asm volatile("" : "+v"(v)); }
+
 // index of accumulator element i of this lane among the 32 result rows
 __device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+struct Range {
+  int lo, hi;
+};
+// result rows r0 .. r0 + 31 outside [r.lo, r.hi) become `value`
+__device__ __forceinline__ void hide(f32x16& v, Range r, int r0, int lane, float value) {
+  pin(v);
+  const int lo = r.lo - r0 - 4 * (lane >> 5);
+  const uint32_t n = (uint32_t)max(r.hi - r.lo, 0);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if ((uint32_t)(8 * (i >> 2) + (i & 3) - lo) >= n) v[i] = value;
+}
 
 // Stores a 32-row result tile (rows: columns 32 dt .. of a token's head, columns: tokens) as bf16:
 // lane halves exchange groups of four so that every lane writes 16 contiguous bytes. dst: the lane's
@@ -215,9 +232,6 @@ __device__ __forceinline__ Unit unit_of(int b, int kv_heads, int per) {
 }
 
 // visible keys [lo, hi) of the query at position p
-struct Range {
-  int lo, hi;
-};
 __device__ __forceinline__ Range visible(int p, int nk, int causal, int window) {
   Range r;
   r.hi = causal ? min(nk, p + 1) : nk;
@@ -331,12 +345,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnFwdArgs a, c
       // some row of the wave does not see some key of the tile
       if (j0 + BN > wa.hi || j0 < wb.lo) {
 #pragma unroll
-        for (int kt = 0; kt < BN / 32; ++kt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = j0 + 32 * kt + acc_row(i, lane);
-            if (j < mine.lo || j >= mine.hi) sc[kt][i] = -INFINITY;
-          }
+        for (int kt = 0; kt < BN / 32; ++kt) hide(sc[kt], mine, j0 + 32 * kt, lane, -INFINITY);
       }
       acc.update(sc, a.c, slack);
 #pragma unroll
@@ -420,11 +429,7 @@ __global__ __launch_bounds__(256, 1) void attn_split_kernel(const AttnFwdArgs a,
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) sc[0] = mfma(T::rows(ks_, 0, ks, lane), qf[ks], sc[0]);
     if (j0 + BN > first.hi || j0 < last.lo) {   // some row does not see some key (ranges end on tiles)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int j = j0 + acc_row(i, lane);
-        if (j < mine.lo || j >= mine.hi) sc[0][i] = -INFINITY;
-      }
+      hide(sc[0], mine, j0, lane, -INFINITY);
     }
     acc.update(sc, a.c, slack);
 #pragma unroll
@@ -539,7 +544,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnFwdArgs a, con
 }
 
 // ------------------------------------------------------------------------------------------
-// Backward, first launch: delta and dq. As the forward (128 query rows a workgroup, keys streamed),
+// Backward, first launch: delta (and, for the second launch, lse log2(e) and -delta) and dq. As the forward (128 query rows a workgroup, keys streamed),
 // with the probabilities recomputed from lse.
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, const AttnSeqs sq) {
@@ -576,8 +581,14 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, co
   const int64_t at = (int64_t)head * a.lse_stride + s.q0 + row;
   if (own) {
     lse2 = a.lse[at] * kLog2e;
-    if (lane < 32) a.delta[at] = delta;
+    if (lane < 32) {   // as the second launch takes them
+      a.lse2[at] = lse2;
+      a.less_delta[at] = -delta;
+    }
   }
+  f32x16 less_delta;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) less_delta[i] = -delta;
 
   const int r1 = min(s.nq, r0 + 128) - 1;
   const int k_lo = visible(r0 + shift, s.nk, a.causal, a.window).lo & ~(BN - 1);
@@ -606,23 +617,15 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, co
     for (int kt = 0; kt < BN / 32; ++kt) {
       const int j0 = k_lo + t * BN + 32 * kt;
       if (j0 < wb.hi && j0 + 32 > wa.lo) {
-        f32x16 sc = zero16(), dp = zero16();
+        f32x16 sc = zero16(), dp = less_delta;   // do.v - delta comes out of the products
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Ks[st], 32 * kt, ks, lane), qf[ks], sc);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) dp = mfma(T::rows(Vs[st], 32 * kt, ks, lane), gf[ks], dp);
-        const bool edge = j0 + 32 > wa.hi || j0 < wb.lo;
-        if (edge) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = j0 + acc_row(i, lane);
-            const float p = __builtin_amdgcn_exp2f(__fmaf_rn(sc[i], a.c, -lse2));
-            dp[i] = (j >= mine.lo && j < mine.hi) ? p * (dp[i] - delta) : 0.f;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) dp[i] = __builtin_amdgcn_exp2f(__fmaf_rn(sc[i], a.c, -lse2)) * (dp[i] - delta);
-        }
+        for (int i = 0; i < 16; ++i) dp[i] *= __builtin_amdgcn_exp2f(__fmaf_rn(sc[i], a.c, -lse2));
+        // selected away, not multiplied: a row without keys has lse -inf
+        if (j0 + 32 > wa.hi || j0 < wb.lo) hide(dp, mine, j0, lane, 0.f);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
           const bf16x8 ds = pack8(dp, kk);
@@ -644,7 +647,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, co
 // two deep. The query heads of the group can be split over several workgroups (gper heads each):
 // their fp32 results go to the workspace, and attn_dkv_sum_kernel adds them in order.
 template <int DP, int ROWS, int NW>
-struct RowStream {   // rows [lo, hi) of q, do, lse and delta, head after head, in tiles of ROWS <= 64
+struct RowStream {   // rows [lo, hi) of q, do, lse2 and less_delta, head after head, in tiles of ROWS <= 64
   typedef TileDma<DP, ROWS, NW> Dma;
   static constexpr int kLoads = 2 * Dma::kLoads + 2;   // per wave and tile
   Dma qd, gd;
@@ -656,15 +659,15 @@ struct RowStream {   // rows [lo, hi) of q, do, lse and delta, head after head, 
     qd.init(wave, lane, a.d, (uint32_t)a.q.token);
     gd.init(wave, lane, a.d, (uint32_t)a.dout.token);
   }
-  // the next tile; lse and delta go to the wave's own copies. Rows past the sequence read 0: their q
+  // the next tile; lse2 and less_delta go to the wave's own copies. Rows past the sequence read 0: their q
   // and do are 0 too, so they add nothing.
   __device__ __forceinline__ void load(uint16_t* qt, uint16_t* gt, float* lt, float* dt, int wave, int lane) {
     const int64_t tok = q0 + i, at = (int64_t)head * a.lse_stride + tok;
     const int rows = nq - i, nrec = min(ROWS, rows) * 4;
     qd.load(qt, a.q.p + tok * a.q.token + (int64_t)head * a.q.head, rows, a.d, (uint32_t)a.q.token, wave);
     gd.load(gt, a.dout.p + tok * a.dout.token + (int64_t)head * a.dout.head, rows, a.d, (uint32_t)a.dout.token, wave);
-    __amdgpu_buffer_rsrc_t rl = __builtin_amdgcn_make_buffer_rsrc((void*)(a.lse + at), (short)0, nrec, kRsrcFlags);
-    __amdgpu_buffer_rsrc_t rd = __builtin_amdgcn_make_buffer_rsrc((void*)(a.delta + at), (short)0, nrec, kRsrcFlags);
+    __amdgpu_buffer_rsrc_t rl = __builtin_amdgcn_make_buffer_rsrc((void*)(a.lse2 + at), (short)0, nrec, kRsrcFlags);
+    __amdgpu_buffer_rsrc_t rd = __builtin_amdgcn_make_buffer_rsrc((void*)(a.less_delta + at), (short)0, nrec, kRsrcFlags);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rl, (lds_void*)lt, 4, (uint32_t)lane * 4u, 0, 0, 0);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_void*)dt, 4, (uint32_t)lane * 4u, 0, 0, 0);
     i += ROWS;
@@ -682,7 +685,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdArgs a, c
   typedef RowStream<DP, BM, 4> Stream;
   __shared__ __attribute__((aligned(16))) uint16_t Qs[2][BM * DP];
   __shared__ __attribute__((aligned(16))) uint16_t Gs[2][BM * DP];
-  __shared__ __attribute__((aligned(16))) float Ls[2][4][BM], Ds[2][4][BM];   // lse and delta, a copy per wave
+  __shared__ __attribute__((aligned(16))) float Ls[2][4][BM], Ds[2][4][BM];   // lse log2(e) and -delta, a copy per wave
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = a.heads / a.kv_heads;
@@ -704,10 +707,10 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdArgs a, c
   const int tiles = i_hi > i_lo ? (i_hi - i_lo + BM - 1) / BM : 0;
   const int g0 = u.sub * sp.gper, g1 = min(G, g0 + sp.gper);
   const int total = tiles * (g1 - g0);
-  // rows [c_lo, c_hi) see the lane's key
-  const int c_lo = a.causal ? key - shift : INT_MIN;
-  const int64_t c_hi64 = (int64_t)key + a.window - shift;
-  const int c_hi = a.window ? (int)min(c_hi64, (int64_t)INT_MAX) : INT_MAX;
+  // rows that see the lane's key
+  Range seen;
+  seen.lo = a.causal ? max(0, key - shift) : 0;
+  seen.hi = a.window ? (int)min((int64_t)key + a.window - shift, (int64_t)INT_MAX) : INT_MAX;
   // and of the wave's keys: rows in [all_lo, all_hi) see all, rows in [any_lo, any_hi) see some
   const int kw = j0 + wave * 32;
   const int any_lo = a.causal ? kw - shift : INT_MIN, all_lo = a.causal ? kw + 31 - shift : INT_MIN;
@@ -737,27 +740,31 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdArgs a, c
     for (int mt = 0; mt < BM / 32; ++mt) {
       const int i0 = ci + 32 * mt;
       if (i0 + 31 >= any_lo && i0 < any_hi) {
-        f32x16 sc = zero16(), dp = zero16();
+        f32x16 sc = zero16(), dp;   // do.v - delta comes out of the products
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(&Ds[st][wave][32 * mt + 8 * g + 4 * (lane >> 5)]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dp[4 * g + e] = x[e];
+        }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Qs[st], 32 * mt, ks, lane), kf[ks], sc);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) dp = mfma(T::rows(Gs[st], 32 * mt, ks, lane), vf[ks], dp);
-        const bool edge = i0 < all_lo || i0 + 31 >= all_hi;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int m = 32 * mt + 8 * g + 4 * (lane >> 5);
-          const f32x4 ls = *reinterpret_cast<const f32x4*>(&Ls[st][wave][m]);
-          const f32x4 dl = *reinterpret_cast<const f32x4*>(&Ds[st][wave][m]);
+          const f32x4 x = *reinterpret_cast<const f32x4*>(&Ls[st][wave][32 * mt + 8 * g + 4 * (lane >> 5)]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float p = __builtin_amdgcn_exp2f(__fmaf_rn(sc[4 * g + e], a.c, -ls[e] * kLog2e));
-            if (edge) {
-              const int i = ci + m + e;
-              p = (i >= c_lo && i < c_hi) ? p : 0.f;
-            }
-            sc[4 * g + e] = p;
-            dp[4 * g + e] = p * (dp[4 * g + e] - dl[e]);
+            const int i = 4 * g + e;
+            sc[i] = __builtin_amdgcn_exp2f(__fmaf_rn(sc[i], a.c, -x[e]));
+            dp[i] *= sc[i];
           }
+        }
+        // selected away, not multiplied: a row without keys has lse -inf
+        if (i0 < all_lo || i0 + 31 >= all_hi) {
+          hide(sc, seen, i0, lane, 0.f);
+          hide(dp, seen, i0, lane, 0.f);
         }
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
@@ -930,7 +937,7 @@ size_t attn_fwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_
 }
 size_t attn_bwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int64_t q_tokens) {
   const std::vector<AttnSeq> v = by_work(seqs, count, true);
-  return (size_t)(round64(q_tokens * heads) + dkv_part_floats(v, heads, kv_heads, padded_d(d)));
+  return (size_t)(2 * round64(q_tokens * heads) + dkv_part_floats(v, heads, kv_heads, padded_d(d)));
 }
 
 hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream) {
@@ -973,7 +980,8 @@ hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t co
 hipError_t launch_attn_bwd(const AttnBwdArgs& args, const AttnSeq* seqs, int64_t count, int64_t q_tokens, float* ws,
                            hipStream_t stream) {
   AttnBwdArgs a = args;
-  a.delta = ws;
+  a.lse2 = ws;
+  a.less_delta = ws + round64(q_tokens * a.heads);
   const std::vector<AttnSeq> vq = by_work(seqs, count, false), vk = by_work(seqs, count, true);
   for (size_t from = 0; from < vq.size(); from += kAttnSeqs) {
     const AttnSeqs q = pack_seqs(vq, from, q_tiles);
@@ -984,7 +992,7 @@ hipError_t launch_attn_bwd(const AttnBwdArgs& args, const AttnSeq* seqs, int64_t
   AttnKvSplit sp{};
   sp.splits = kv_splits(vk, a.heads, a.kv_heads);
   sp.gper = (int)ceil64(a.heads / a.kv_heads, sp.splits);
-  sp.part = ws + round64(q_tokens * a.heads);
+  sp.part = ws + 2 * round64(q_tokens * a.heads);
   for (size_t from = 0; from < vk.size(); from += kAttnSeqs) {
     const AttnSeqs q = pack_seqs(vk, from, k_tiles);
     const int units = q.first[q.count] * a.kv_heads;

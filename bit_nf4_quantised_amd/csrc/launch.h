@@ -195,7 +195,7 @@ struct AttnFwdArgs {
 struct AttnBwdArgs {
   AttnTensor q, k, v, o, dout, dq, dk, dv;
   const float* lse;
-  float* delta;                 // [heads][lse_stride], set by launch_attn_bwd
+  float *lse2, *less_delta;     // [heads][lse_stride]: lse log2(e) and -delta; set by launch_attn_bwd
   int64_t lse_stride;
   int heads, kv_heads, d, causal, window;
   float c, scale;

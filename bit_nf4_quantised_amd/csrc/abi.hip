@@ -615,7 +615,8 @@ size_t qlora_attn_workspace_bytes(const qlora_attn_config* cfg, int64_t count, c
   if (check_attn_config(cfg) || check_attn_seqs(cfg, count, seqs, backward != 0) || count == 0) return 0;
   try {
     const std::vector<nf4::AttnSeq> v = attn_seqs(count, seqs);
-    const size_t f = backward ? nf4::attn_bwd_ws_floats(v.data(), count, cfg->heads, cfg->kv_heads, cfg->d, cfg->q_tokens)
+    const size_t f = backward ? nf4::attn_bwd_ws_floats(v.data(), count, cfg->heads, cfg->kv_heads, cfg->d, cfg->causal != 0, attn_window(cfg),
+                                                         cfg->q_tokens)
                               : nf4::attn_fwd_ws_floats(v.data(), count, cfg->heads, cfg->kv_heads, cfg->d, attn_window(cfg));
     return align_up(f * 4);
   } catch (...) {
@@ -663,7 +664,8 @@ int qlora_attn_bwd(const qlora_attn_config* cfg, int64_t count, const qlora_attn
   if (!aligned16(lse) || !aligned16(ws)) return NF4_ERR_ALIGN;
   try {
     const std::vector<nf4::AttnSeq> s = attn_seqs(count, seqs);
-    const size_t need = nf4::attn_bwd_ws_floats(s.data(), count, cfg->heads, cfg->kv_heads, cfg->d, tq) * 4;
+    const size_t need = nf4::attn_bwd_ws_floats(s.data(), count, cfg->heads, cfg->kv_heads, cfg->d, cfg->causal != 0,
+                                                 attn_window(cfg), tq) * 4;
     if (need && (!ws || ws_bytes < need)) return NF4_ERR_WORKSPACE;
     const nf4::AttnBwdArgs a{attn_tensor(q), attn_tensor(k), attn_tensor(v), attn_tensor(o), attn_tensor(dout), attn_tensor(dq),
                              attn_tensor(dk), attn_tensor(dv), lse, nullptr, nullptr, tq, cfg->heads, cfg->kv_heads, cfg->d,

@@ -82,33 +82,39 @@ hipError_t launch_act8_unpack(const int8_t* codes, const uint16_t* absmax, int64
 }
 
 // ------------------------------------------------------------------------------------------
-// dA from the codes. A workgroup takes 128 columns (two blocks) and a range of rows, for up to RT
-// tiles of 16 adapter ranks (of one linear or of several that share x); its 4 waves take 32-row
-// chunks in turn. In v_mfma_f32_16x16x32_bf16 a lane's operand fragment is 8 rows of one column, so a
-// lane loads one dword (4 columns) from each of 8 rows and keeps all four columns: column tile t is
-// the columns 4 i + t of the block, and nothing is transposed. The rank operand is scaled in fp32 and
-// split into a bf16 pair hi + lo, as the passes over bf16 inputs split theirs (relative error 2^-17).
+// dA from the codes. A workgroup takes 128 columns (two blocks), a range of rows and up to RT tiles of
+// 16 adapter ranks (of one linear or of several that share x); its 4 waves take 32-row chunks in turn.
+// In v_mfma_f32_16x16x32_bf16 a lane's operand fragment is 8 rows of one column, so a lane loads one
+// dword (4 columns) from each of 8 rows and keeps all four columns: column tile t is the columns
+// 4 i + t of the block, and nothing is transposed. The rank operand is scaled in fp32 and split into a
+// bf16 pair hi + lo, as the passes over bf16 inputs split theirs (relative error 2^-17).
 struct Dx8Tile {
   const float* v;      // [M x r], at the tile's first column
-  float* part;         // [row ranges][K][r], at the tile's first column
+  float* out;          // at the tile's first row: partial sums [row ranges][r][K], or dA [r][K] itself
 };
+constexpr int kDx8Tiles = 4 * 8;   // four linears of rank 128
 struct Dx8Args {
   const int8_t* codes;
   const uint16_t* absmax;
   int64_t M, K;
   int64_t rows;        // rows per range (a multiple of 32)
-  int r;               // rank
-  Dx8Tile tile[4 * 8];
+  int r, tiles;        // rank; rank tiles in all
+  int final_;          // one range: out is dA, scaled (and added to)
+  int accumulate;
+  float scale;
+  Dx8Tile tile[kDx8Tiles];
 };
 
 template <int RT>
-__global__ __launch_bounds__(256) void act8_grad_kernel(const Dx8Args a, int tile0) {
+__global__ __launch_bounds__(256) void act8_grad_kernel(const Dx8Args a) {
   __shared__ f32x4 red[4][4][64];
+  __shared__ __attribute__((aligned(16))) float out[16][68];   // 16 ranks x 64 columns
   const int tid = threadIdx.x, lane = tid & 63, grp = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t nb = a.K / 64, b0 = (int64_t)blockIdx.x * 2;
   const int blocks = (int)min((int64_t)2, nb - b0);
   const int64_t m_begin = (int64_t)blockIdx.y * a.rows, m_end = min(a.M, m_begin + a.rows);
+  const int tile0 = (int)blockIdx.z * RT;
   f32x4 acc[RT][2][4];
 #pragma unroll
   for (int t = 0; t < RT; ++t)
@@ -130,7 +136,7 @@ __global__ __launch_bounds__(256) void act8_grad_kernel(const Dx8Args a, int til
         s[b][e] = __uint_as_float((uint32_t)a.absmax[mr * nb + blk] << 16) * (1.f / 127.f);
       }
 #pragma unroll
-      for (int t = 0; t < RT; ++t) v[t][e] = m < m_end ? a.tile[tile0 + t].v[mr * a.r + col] : 0.f;
+      for (int t = 0; t < RT; ++t) v[t][e] = m < m_end ? a.tile[min(tile0 + t, a.tiles - 1)].v[mr * a.r + col] : 0.f;
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -156,23 +162,33 @@ __global__ __launch_bounds__(256) void act8_grad_kernel(const Dx8Args a, int til
       }
     }
   }
-  // the waves' sums, added in wave order: wave w finishes column tile w
+  // the waves' sums, added in wave order (wave w finishes column tile w), then rows of 64 columns
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
+  for (int t = 0; t < RT; ++t) {
+    if (tile0 + t >= a.tiles) break;
+    float* dst = a.tile[tile0 + t].out + (int64_t)blockIdx.y * a.r * a.K;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
+      if (b >= blocks) break;
 #pragma unroll
       for (int c = 0; c < 4; ++c) red[wave][c][lane] = acc[t][b][c];
       __syncthreads();
       f32x4 v = red[0][wave][lane];
 #pragma unroll
       for (int w = 1; w < 4; ++w) v += red[w][wave][lane];
-      if (b < blocks) {
-        const int64_t c = (b0 + b) * 64 + 4 * col + wave;
-        *reinterpret_cast<f32x4*>(a.tile[tile0 + t].part + ((int64_t)blockIdx.y * a.K + c) * a.r + 4 * grp) = v;
-      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[4 * grp + e][4 * col + wave] = v[e];
       __syncthreads();
+      const int j = tid >> 4;
+      float* p = dst + j * a.K + (b0 + b) * 64 + 4 * (tid & 15);
+      f32x4 o = *reinterpret_cast<const f32x4*>(&out[j][4 * (tid & 15)]);
+      if (a.final_) {
+        o *= a.scale;
+        if (a.accumulate) o += *reinterpret_cast<const f32x4*>(p);
+      }
+      *reinterpret_cast<f32x4*>(p) = o;
     }
+  }
 }
 
 // Rows per range: about 512 workgroups, 128 rows (one chunk a wave) at least.
@@ -187,39 +203,43 @@ static int64_t dx8_ranges(int64_t M, int64_t K) {
   return (M + rows - 1) / rows;
 }
 
+// partial sums only where there are several ranges
 size_t act8_grad_ws_floats(int count, int64_t M, int64_t K, int r) {
-  return (size_t)count * (size_t)dx8_ranges(M, K) * (size_t)K * r;
+  const int64_t ranges = dx8_ranges(M, K);
+  return ranges > 1 ? (size_t)count * (size_t)ranges * (size_t)K * r : 0;
 }
 
 hipError_t launch_act8_grad(int count, const int8_t* codes, const uint16_t* absmax, int64_t M, int64_t K,
                             const float* const* v, int r, float scale, int accumulate, float* ws, float* const* dA,
                             hipStream_t stream) {
   if (count < 1 || count > 4) return hipErrorInvalidValue;
+  const int64_t ranges = dx8_ranges(M, K), groups = (K / 64 + 1) / 2;
   Dx8Args a{};
   a.codes = codes;
   a.absmax = absmax;
   a.M = M;
   a.K = K;
-  a.r = r;
   a.rows = dx8_rows(M, K);
-  const int64_t ranges = dx8_ranges(M, K);
+  a.r = r;
+  a.final_ = ranges == 1;
+  a.accumulate = accumulate;
+  a.scale = scale;
   const float* part[4];
-  int nt = 0;
   for (int i = 0; i < count; ++i) {
-    float* base = ws + (size_t)i * ranges * K * r;
+    float* base = a.final_ ? dA[i] : ws + (size_t)i * ranges * K * r;
     part[i] = base;
-    for (int t = 0; t < r / 16; ++t) a.tile[nt++] = Dx8Tile{v[i] + 16 * t, base + 16 * t};
+    for (int t = 0; t < r / 16; ++t) a.tile[a.tiles++] = Dx8Tile{v[i] + 16 * t, base + (int64_t)16 * t * K};
   }
-  const dim3 grid((unsigned)((K / 64 + 1) / 2), (unsigned)ranges), block(256);
-  for (int t = 0; t < nt; t += 4) {
-    switch (nt - t) {
-      case 1: hipLaunchKernelGGL(act8_grad_kernel<1>, grid, block, 0, stream, a, t); break;
-      case 2: hipLaunchKernelGGL(act8_grad_kernel<2>, grid, block, 0, stream, a, t); break;
-      case 3: hipLaunchKernelGGL(act8_grad_kernel<3>, grid, block, 0, stream, a, t); break;
-      default: hipLaunchKernelGGL(act8_grad_kernel<4>, grid, block, 0, stream, a, t); break;
-    }
-  }
-  return launch_lora_sum(count, part, (int)ranges, K, r, scale, accumulate, dA, stream);
+  // as many rank tiles to a workgroup (they share its reads of x) as leave 256 workgroups: at 77 rows,
+  // K = 4096 and 12 tiles one tile each took 5 us where four took 24 in three launches
+  int rt = 4;
+  while (rt > 1 && groups * ranges * ((a.tiles + rt - 1) / rt) < 256) rt /= 2;
+  const dim3 grid((unsigned)groups, (unsigned)ranges, (unsigned)((a.tiles + rt - 1) / rt)), block(256);
+  if (rt == 4) hipLaunchKernelGGL(act8_grad_kernel<4>, grid, block, 0, stream, a);
+  else if (rt == 2) hipLaunchKernelGGL(act8_grad_kernel<2>, grid, block, 0, stream, a);
+  else hipLaunchKernelGGL(act8_grad_kernel<1>, grid, block, 0, stream, a);
+  if (a.final_) return hipGetLastError();
+  return launch_lora_sum(count, part, (int)ranges, K * r, scale, accumulate, dA, stream);
 }
 
 }  // namespace nf4

@@ -370,15 +370,56 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnFwdArgs a, c
 // ------------------------------------------------------------------------------------------
 // Few query rows over many keys. The query heads that share a key head are packed with the tokens
 // into rows (row = token * group + head in group), 32 rows a workgroup; its keys are one range of the
-// sequence's, and its 4 waves take 32-key tiles of that range in turn, each through its own LDS ring
-// without barriers. The waves' results are joined in LDS; with several ranges they go to the
-// workspace and attn_join_kernel joins them, in order.
+// sequence's, and its 4 waves take 32-key tiles of that range in turn, each through two LDS tiles of its
+// own without barriers: a tile is read into registers whole and its place refilled before the
+// arithmetic, so two tiles (32 KiB a wave at d = 128) are always on their way. The waves' results are
+// joined in LDS; with several ranges they go to the workspace and attn_join_kernel joins them, in order.
+// Bound by memory: the keys and values, once.
 template <int DP>
-__global__ __launch_bounds__(256, 1) void attn_split_kernel(const AttnFwdArgs a, const AttnSeqs sq, const AttnSplit sp) {
-  constexpr int BN = 32, KS = DP / 16, DT = DP / 32, ST = DP == 128 ? 2 : 4;
+struct SplitWave {
+  static constexpr int BN = 32, KS = DP / 16, DT = DP / 32;
   typedef Tile<DP> T;
   typedef KvStream<DP, BN, 1> Stream;
-  __shared__ __attribute__((aligned(16))) uint16_t ring[2][4][ST][BN * DP];   // keys, values
+  bf16x8 qf[KS];
+  Online<DT> acc;
+  Stream kv;
+  Range mine, first, last;   // keys that the lane's row, the tile's first and its last row see
+  float c, slack;
+  int lane;
+  // the tile in (kt, vt) with keys from j0; afterwards the tile from `next` (if below `end`) is on its way there
+  __device__ __forceinline__ void tile(uint16_t* kt, uint16_t* vt, int j0, int next, int end) {
+    bf16x8 kf[KS], vf[2 * DT];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) kf[ks] = T::rows(kt, 0, ks, lane);
+#pragma unroll
+    for (int i = 0; i < 2 * DT; ++i) vf[i] = T::cols(vt, 16 * (i / DT), i % DT, lane);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read out before it is refilled
+    if (next < end) kv.load(kt, vt, next, 0);
+    f32x16 sc[1];
+    sc[0] = zero16();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) sc[0] = mfma(kf[ks], qf[ks], sc[0]);
+    // some row does not see some key (ranges end on tiles)
+    if (j0 + BN > first.hi || j0 < last.lo) hide(sc[0], mine, j0, lane, -INFINITY);
+    acc.update(sc, c, slack);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const bf16x8 p = pack8(sc[0], kk);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(vf[kk * DT + dt], p, acc.o[dt]);
+    }
+  }
+};
+
+template <int DP>
+__global__ __launch_bounds__(256, DP == 128 ? 1 : 2) void attn_split_kernel(const AttnFwdArgs a, const AttnSeqs sq,
+                                                                          const AttnSplit sp) {
+  constexpr int BN = 32, DT = DP / 32;
+  typedef SplitWave<DP> Wave;
+  typedef typename Wave::Stream Stream;
+  // [keys, values][wave]; a variable per tile in flight, so that reads of one wait only for its own loads
+  __shared__ __attribute__((aligned(16))) uint16_t ring0[2][4][BN * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t ring1[2][4][BN * DP];
   __shared__ float Ms[4][32], Ls[4][32];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -391,55 +432,34 @@ __global__ __launch_bounds__(256, 1) void attn_split_kernel(const AttnFwdArgs a,
   const int shift = s.nk - s.nq, rows = s.nq * G;
   const int row = rt * 32 + (lane & 31);
   const int tok = min(row, rows - 1) / G, head = u.kvh * G + min(row, rows - 1) % G;
-  bf16x8 qf[KS];
-  load_rows<DP>(qf, row < rows ? a.q.p + (s.q0 + tok) * a.q.token + (int64_t)head * a.q.head : nullptr, a.d, lane);
-
   const int t0 = rt * 32 / G, t1 = min(rows - 1, rt * 32 + 31) / G;   // tokens of the row tile
-  const Range first = visible(t0 + shift, s.nk, a.causal, a.window), last = visible(t1 + shift, s.nk, a.causal, a.window);
-  const Range mine = visible(tok + shift, s.nk, a.causal, a.window);
-  const int k_lo = max(first.lo & ~(BN - 1), sp.lo[si] + split * sp.chunk);
-  const int k_hi = min(last.hi, sp.lo[si] + (split + 1) * sp.chunk);
-  const int tiles = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
-  const int nt = tiles > wave ? (tiles - wave + 3) / 4 : 0;   // of this wave
-
-  Stream kv;
-  kv.init(a.k, a.v, s, u.kvh, a.d, 0, lane);
+  Wave w;
+  w.first = visible(t0 + shift, s.nk, a.causal, a.window);
+  w.last = visible(t1 + shift, s.nk, a.causal, a.window);
+  w.mine = visible(tok + shift, s.nk, a.causal, a.window);
+  const int k_lo = max(w.first.lo & ~(BN - 1), sp.lo[si] + split * sp.chunk);
+  const int k_hi = min(w.last.hi, sp.lo[si] + (split + 1) * sp.chunk);
   const int j_w = k_lo + wave * BN;   // the wave's first tile; its tiles are 4 apart
-  Online<DT> acc;
-  acc.init();
-  const float slack = kSlack / a.c;
-  for (int t = 0; t < ST - 1 && t < nt; ++t) kv.load(ring[0][wave][t], ring[1][wave][t], j_w + t * 4 * BN, 0);
-  for (int t = 0; t < nt; ++t) {
-    if (t + ST - 1 < nt) {
-      const int n = t + ST - 1;
-      kv.load(ring[0][wave][n % ST], ring[1][wave][n % ST], j_w + n * 4 * BN, 0);
-      wait_vmcnt<(ST - 1) * Stream::kLoads>();
-    } else {
-      const int ahead = nt - 1 - t;
-      if (ST > 3 && ahead == 2) wait_vmcnt<(ST > 3 ? 2 : 0) * Stream::kLoads>();
-      else if (ST > 2 && ahead == 1) wait_vmcnt<(ST > 2 ? 1 : 0) * Stream::kLoads>();
-      else wait_vmcnt<0>();
-    }
+  w.kv.init(a.k, a.v, s, u.kvh, a.d, 0, lane);
+  if (j_w < k_hi) w.kv.load(ring0[0][wave], ring0[1][wave], j_w, 0);
+  if (j_w + 4 * BN < k_hi) w.kv.load(ring1[0][wave], ring1[1][wave], j_w + 4 * BN, 0);
+  load_rows<DP>(w.qf, row < rows ? a.q.p + (s.q0 + tok) * a.q.token + (int64_t)head * a.q.head : nullptr, a.d, lane);
+  w.acc.init();
+  w.c = a.c;
+  w.slack = kSlack / a.c;
+  w.lane = lane;
+  for (int j = j_w; j < k_hi; j += 8 * BN) {
+    if (j + 4 * BN < k_hi) wait_vmcnt<Stream::kLoads>();   // ring1's loads may be in flight
+    else wait_vmcnt<0>();
     asm volatile("" ::: "memory");   // the tile's LDS reads stay after the wait
-    const uint16_t* ks_ = ring[0][wave][t % ST];
-    const uint16_t* vs_ = ring[1][wave][t % ST];
-    const int j0 = j_w + t * 4 * BN;
-    f32x16 sc[1];
-    sc[0] = zero16();
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) sc[0] = mfma(T::rows(ks_, 0, ks, lane), qf[ks], sc[0]);
-    if (j0 + BN > first.hi || j0 < last.lo) {   // some row does not see some key (ranges end on tiles)
-      hide(sc[0], mine, j0, lane, -INFINITY);
-    }
-    acc.update(sc, a.c, slack);
-#pragma unroll
-    for (int kk = 0; kk < BN / 16; ++kk) {
-      const bf16x8 p = pack8(sc[0], kk & 1);
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(T::cols(vs_, 16 * kk, dt, lane), p, acc.o[dt]);
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the ring slot is read out before it is refilled
+    w.tile(ring0[0][wave], ring0[1][wave], j, j + 8 * BN, k_hi);
+    if (j + 4 * BN >= k_hi) break;
+    if (j + 8 * BN < k_hi) wait_vmcnt<Stream::kLoads>();
+    else wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+    w.tile(ring1[0][wave], ring1[1][wave], j + 4 * BN, j + 12 * BN, k_hi);
   }
+  Online<DT>& acc = w.acc;
 
   // join the waves: the common maximum, then the scaled sums, added in wave order
   float l = half_sum(acc.l);
@@ -451,24 +471,26 @@ __global__ __launch_bounds__(256, 1) void attn_split_kernel(const AttnFwdArgs a,
   const int col = lane & 31;
   float mx = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) mx = fmaxf(mx, Ms[w][col]);
+  for (int k = 0; k < 4; ++k) mx = fmaxf(mx, Ms[k][col]);
   const float mxc = mx == -INFINITY ? 0.f : mx * a.c;
   l = 0.f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) l += Ms[w][col] == -INFINITY ? 0.f : Ls[w][col] * __builtin_amdgcn_exp2f(Ms[w][col] * a.c - mxc);
+  for (int k = 0; k < 4; ++k) l += Ms[k][col] == -INFINITY ? 0.f : Ls[k][col] * __builtin_amdgcn_exp2f(Ms[k][col] * a.c - mxc);
   const float f = acc.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(acc.mc - mxc);
   __syncthreads();
   // the waves' outputs as [wave][d][32 rows]
   constexpr int P = 33;
-  float* buf = reinterpret_cast<float*>(&ring[0][0][0][0]) + wave * (DP * P);
-  static_assert(4 * DP * P * 4 <= sizeof(ring), "the joined outputs fit the ring");
+  // waves 0 and 1 in ring0, 2 and 3 in ring1
+  static_assert(2 * DP * P * 4 <= sizeof(ring0), "two waves' outputs fit a ring");
+  float* const out0 = reinterpret_cast<float*>(&ring0[0][0][0]);
+  float* const out1 = reinterpret_cast<float*>(&ring1[0][0][0]);
+  float* buf = (wave < 2 ? out0 : out1) + (wave & 1) * (DP * P);
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
     for (int i = 0; i < 16; ++i) buf[(32 * dt + acc_row(i, lane)) * P + col] = acc.o[dt][i] * f;
   __syncthreads();
   // thread: row tid / 8, columns 8 (tid % 8) + 64 k
-  const float* all = reinterpret_cast<const float*>(&ring[0][0][0][0]);
   const int orow = tid >> 3, grow = rt * 32 + orow;
   const float rl = __shfl(l, orow), rm = __shfl(mxc, orow);   // the row's statistics, as lane `orow` holds them
   if (grow >= rows) return;
@@ -481,7 +503,7 @@ __global__ __launch_bounds__(256, 1) void attn_split_kernel(const AttnFwdArgs a,
     for (int e = 0; e < 8; ++e) {
       v[e] = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) v[e] += all[w * (DP * P) + (c0 + e) * P + orow];
+      for (int k2 = 0; k2 < 4; ++k2) v[e] += (k2 < 2 ? out0 : out1)[(k2 & 1) * (DP * P) + (c0 + e) * P + orow];
     }
     if (c0 >= a.d) continue;
     if (ns == 1) {
@@ -521,18 +543,34 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnFwdArgs a, con
   const int grow = local / a.kv_heads, kvh = local % a.kv_heads;
   const int tok = grow / G, head = kvh * G + grow % G;
   const float* part = sp.part + (sp.row0[si] + (int64_t)local * ns) * (int64_t)(a.d + 8);
-  float mx = -INFINITY;
-  for (int k = 0; k < ns; ++k) mx = fmaxf(mx, part[(int64_t)k * (a.d + 8) + a.d]);
-  float l = 0.f, v0 = 0.f, v1 = 0.f;
+  const int64_t step = a.d + 8;
+  float mx = -INFINITY, l = 0.f, v0 = 0.f, v1 = 0.f;
   const int c = 2 * lane;
-  for (int k = 0; k < ns; ++k) {
-    const float* p = part + (int64_t)k * (a.d + 8);
-    const float m = p[a.d];
-    const float w = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mx);
-    l += w * p[a.d + 1];
-    if (c < a.d) {
-      v0 += w * p[c];
-      v1 += w * p[c + 1];
+  for (int k0 = 0; k0 < ns; k0 += 64) {   // 64 ranges at a time: lane i holds the statistics of range k0 + i
+    const int n = min(64, ns - k0);
+    const float* p = part + (k0 + min(lane, n - 1)) * step + a.d;
+    const float m = lane < n ? p[0] : -INFINITY, lk = lane < n ? p[1] : 0.f;
+    const float top = fmaxf(mx, wave_max(m));
+    if (top == -INFINITY) continue;
+    const float f = __builtin_amdgcn_exp2f(mx - top);   // 0 while nothing was seen
+    const float w = __builtin_amdgcn_exp2f(m - top), wl = w * lk;
+    l *= f;
+    v0 *= f;
+    v1 *= f;
+    mx = top;
+    for (int k = 0; k < n; k += 4) {   // four ranges' loads at a time; those past the end have weight 0
+      float2 x[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        x[q] = c < a.d ? *reinterpret_cast<const float2*>(part + (k0 + min(k + q, n - 1)) * step + c) : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int at = min(k + q, 63);
+        const float wk = k + q < n ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), at)) : 0.f;
+        l += k + q < n ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wl), at)) : 0.f;
+        v0 = __fmaf_rn(wk, x[q].x, v0);
+        v1 = __fmaf_rn(wk, x[q].y, v1);
+      }
     }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -874,51 +912,100 @@ static int64_t first_key(const AttnSeq& s, int window) {
   return window ? std::max<int64_t>(0, (int64_t)s.nk - s.nq - window + 1) : 0;
 }
 
-// The forward's plan: attn_fwd_kernel when its workgroups fill the GPU, else attn_split_kernel, with
-// the key ranges as long as give about 512 workgroups (two a compute unit).
+// The forward's plan. Sequences of more than kFewRows query rows go to attn_fwd_kernel when its
+// workgroups fill the GPU (256 compute units); the others, and these when they are too few, to
+// attn_split_kernel, with one length of key range for all.
+constexpr int kFewRows = 16, kUnits = 256;
 struct FwdPlan {
-  bool split;
-  int64_t chunk;         // keys per range
-  int64_t part_floats;   // workspace of one launch (the largest)
+  std::vector<AttnSeq> many, few;
+  int64_t chunk = 0;        // keys per range
+  int64_t part_floats = 0;  // workspace of one launch (the largest)
 };
 static int split_count(const AttnSeq& s, int window, int64_t chunk) {
   const int64_t lo = first_key(s, window) & ~int64_t(31);
   return (int)std::max<int64_t>(1, ceil64(s.nk - lo, chunk));
 }
-static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, int d, int window) {
-  FwdPlan p{false, 0, 0};
-  const int G = heads / kv_heads;
-  int64_t wgs = 0, key_tiles = 0;
-  for (const AttnSeq& s : v) {
-    wgs += (int64_t)q_tiles(s) * heads;
-    key_tiles += ceil64((int64_t)s.nq * G, 32) * ceil64(s.nk - first_key(s, window), 128) * kv_heads;
+static int64_t row_tiles(const AttnSeq& s, int G) { return ceil64((int64_t)s.nq * G, 32); }
+
+// A compute unit holds one workgroup of attn_split_kernel at a time, so the launch takes as many rounds
+// as there are workgroups to a unit, each as long as a range and a fixed part that costs about as much as
+// 224 keys (start, first loads, joining the waves: 5 us against 0.022 us a key), and joining ranges costs
+// another launch (4 us, 180 keys). The range length with the smallest sum wins; for sixteen sequences of 1
+// to 8191 keys it took 42 us where ranges for two workgroups a unit on average took 52.
+static int64_t split_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, int window) {
+  int64_t longest = 1, best = 0, best_cost = INT64_MAX;
+  for (const AttnSeq& s : v) longest = std::max(longest, (int64_t)s.nk - (first_key(s, window) & ~int64_t(31)));
+  for (int64_t chunk = 256;; chunk += std::max<int64_t>(128, chunk / 8 / 128 * 128)) {
+    int64_t wgs = 0;
+    for (const AttnSeq& s : v) wgs += row_tiles(s, G) * split_count(s, window, chunk) * kv_heads;
+    const int64_t cost = ceil64(wgs, kUnits) * (std::min(chunk, longest) + 224) + (chunk < longest ? 180 : 0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = chunk;
+    }
+    if (chunk >= longest) return best;
   }
-  if (wgs >= 256 && v[0].nq > 16) return p;
-  p.split = true;
-  p.chunk = 128 * std::max<int64_t>(2, ceil64(key_tiles, 512));
-  for (size_t from = 0; from < v.size(); from += kAttnSeqs) {
+}
+static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, int d, int window) {
+  FwdPlan p;
+  const int G = heads / kv_heads;
+  int64_t wgs = 0;
+  for (const AttnSeq& s : v)
+    if (s.nq > kFewRows) wgs += (int64_t)q_tiles(s) * heads;
+  for (const AttnSeq& s : v) (wgs >= kUnits && s.nq > kFewRows ? p.many : p.few).push_back(s);
+  if (p.few.empty()) return p;
+  p.chunk = split_chunk(p.few, G, kv_heads, window);
+  for (size_t from = 0; from < p.few.size(); from += kAttnSeqs) {
     int64_t f = 0;
-    for (size_t i = from; i < v.size() && i < from + kAttnSeqs; ++i) {
-      const int ns = split_count(v[i], window, p.chunk);
-      if (ns > 1) f += (int64_t)v[i].nq * heads * ns * (d + 8);
+    for (size_t i = from; i < p.few.size() && i < from + kAttnSeqs; ++i) {
+      const int ns = split_count(p.few[i], window, p.chunk);
+      if (ns > 1) f += (int64_t)p.few[i].nq * heads * ns * (d + 8);
     }
     p.part_floats = std::max(p.part_floats, f);
   }
   return p;
 }
 
-// Splits of the dk, dv launch over the query heads of a group, for about 512 workgroups.
-static int kv_splits(const std::vector<AttnSeq>& v, int heads, int kv_heads) {
-  const int G = heads / kv_heads;
-  int64_t wgs = 0;
-  for (const AttnSeq& s : v) wgs += (int64_t)k_tiles(s) * kv_heads;
-  if (wgs == 0) return 1;
-  const int64_t want = std::min<int64_t>(G, ceil64(512, wgs));
-  const int gper = (int)ceil64(G, want);
-  return (int)ceil64(G, gper);
+// 64-row tiles of queries that see some key of key tile t (as attn_dkv_kernel counts them)
+static int64_t dkv_row_tiles(const AttnSeq& s, int t, int causal, int window) {
+  const int64_t shift = (int64_t)s.nk - s.nq, j0 = 128 * (int64_t)t, jl = std::min<int64_t>(s.nk, j0 + 128) - 1;
+  const int64_t lo = (causal ? std::max<int64_t>(0, j0 - shift) : 0) & ~int64_t(63);
+  const int64_t hi = window ? std::min<int64_t>(s.nq, jl + window - shift) : s.nq;
+  return hi > lo ? ceil64(hi - lo, 64) : 0;
 }
-static int64_t dkv_part_floats(const std::vector<AttnSeq>& v, int heads, int kv_heads, int dp) {
-  const int splits = kv_splits(v, heads, kv_heads);
+
+// Splits of the dk, dv launch over the query heads of a group. The launch takes as long as its longest
+// workgroup or the mean over the compute units (one workgroup each at a time), about 2.6 us for a tile of
+// 64 rows; splitting shortens the first, and the fp32 results of the parts cost about 0.03 us for every
+// tile of 128 keys and part (written, read and added). Packed sequences of 1500, 1031, 783, 700, 64, 17
+// and 1 tokens with 8 heads to a key head: 2 parts 255 us + 17 us for the sums, 3 parts 198 + 26.
+static int kv_splits(const std::vector<AttnSeq>& v, int heads, int kv_heads, int causal, int window) {
+  const int G = heads / kv_heads;
+  int64_t tiles = 0, longest = 0, total = 0;
+  for (const AttnSeq& s : v) {
+    tiles += k_tiles(s);
+    if (tiles * kv_heads >= 16 * kUnits) return 1;   // workgroups enough
+    for (int t = 0; t < k_tiles(s); ++t) {
+      const int64_t n = dkv_row_tiles(s, t, causal, window);
+      longest = std::max(longest, n);
+      total += n;
+    }
+  }
+  int best = 1;
+  double best_cost = 0;
+  for (int want = 1; want <= G; ++want) {
+    const int gper = (int)ceil64(G, want), splits = (int)ceil64(G, gper);
+    if (splits != want) continue;
+    const double mean = (double)total * G * kv_heads / kUnits;
+    const double cost = 2.6 * std::max((double)longest * gper, mean) + (splits > 1 ? 4 + 0.03 * tiles * kv_heads * splits : 0);
+    if (want == 1 || cost < best_cost) {
+      best = splits;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+static int64_t dkv_part_floats(const std::vector<AttnSeq>& v, int splits, int kv_heads, int dp) {
   if (splits == 1) return 0;
   int64_t most = 0;
   for (size_t from = 0; from < v.size(); from += kAttnSeqs) {
@@ -935,9 +1022,11 @@ size_t attn_fwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_
   const std::vector<AttnSeq> v = by_work(seqs, count, false);
   return v.empty() ? 0 : (size_t)fwd_plan(v, heads, kv_heads, d, window).part_floats;
 }
-size_t attn_bwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int64_t q_tokens) {
+size_t attn_bwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int causal, int window,
+                          int64_t q_tokens) {
   const std::vector<AttnSeq> v = by_work(seqs, count, true);
-  return (size_t)(2 * round64(q_tokens * heads) + dkv_part_floats(v, heads, kv_heads, padded_d(d)));
+  const int splits = kv_splits(v, heads, kv_heads, causal, window);
+  return (size_t)(2 * round64(q_tokens * heads) + dkv_part_floats(v, splits, kv_heads, padded_d(d)));
 }
 
 hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream) {
@@ -945,34 +1034,33 @@ hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t co
   if (v.empty()) return hipSuccess;
   const int G = a.heads / a.kv_heads;
   const FwdPlan plan = fwd_plan(v, a.heads, a.kv_heads, a.d, a.window);
-  for (size_t from = 0; from < v.size(); from += kAttnSeqs) {
-    if (!plan.split) {
-      const AttnSeqs q = pack_seqs(v, from, q_tiles);
-      const dim3 grid((unsigned)(q.first[q.count] * a.heads));
-      if (a.d <= 64) hipLaunchKernelGGL(attn_fwd_kernel<64>, grid, dim3(256), 0, stream, a, q);
-      else hipLaunchKernelGGL(attn_fwd_kernel<128>, grid, dim3(256), 0, stream, a, q);
-    } else {
-      const AttnSeqs q = pack_seqs(v, from, [&](const AttnSeq& s) {
-        return ceil64((int64_t)s.nq * G, 32) * split_count(s, a.window, plan.chunk);
-      });
-      AttnSplit sp{};
-      sp.part = ws;
-      sp.chunk = (int)plan.chunk;
-      int64_t row0 = 0;
-      for (int i = 0; i < q.count; ++i) {
-        sp.lo[i] = (int)(first_key(q.seq[i], a.window) & ~int64_t(31));
-        sp.nsplit[i] = split_count(q.seq[i], a.window, plan.chunk);
-        sp.row0[i] = row0;
-        const int64_t items = sp.nsplit[i] > 1 ? (int64_t)q.seq[i].nq * a.heads : 0;
-        row0 += items * sp.nsplit[i];
-        sp.join_first[i + 1] = sp.join_first[i] + (int)items;
-      }
-      const dim3 grid((unsigned)(q.first[q.count] * a.kv_heads));
-      if (a.d <= 64) hipLaunchKernelGGL(attn_split_kernel<64>, grid, dim3(256), 0, stream, a, q, sp);
-      else hipLaunchKernelGGL(attn_split_kernel<128>, grid, dim3(256), 0, stream, a, q, sp);
-      const int items = sp.join_first[q.count];
-      if (items) hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a, q, sp);
+  for (size_t from = 0; from < plan.many.size(); from += kAttnSeqs) {
+    const AttnSeqs q = pack_seqs(plan.many, from, q_tiles);
+    const dim3 grid((unsigned)(q.first[q.count] * a.heads));
+    if (a.d <= 64) hipLaunchKernelGGL(attn_fwd_kernel<64>, grid, dim3(256), 0, stream, a, q);
+    else hipLaunchKernelGGL(attn_fwd_kernel<128>, grid, dim3(256), 0, stream, a, q);
+  }
+  for (size_t from = 0; from < plan.few.size(); from += kAttnSeqs) {
+    const AttnSeqs q = pack_seqs(plan.few, from, [&](const AttnSeq& s) {
+      return row_tiles(s, G) * split_count(s, a.window, plan.chunk);
+    });
+    AttnSplit sp{};
+    sp.part = ws;
+    sp.chunk = (int)plan.chunk;
+    int64_t row0 = 0;
+    for (int i = 0; i < q.count; ++i) {
+      sp.lo[i] = (int)(first_key(q.seq[i], a.window) & ~int64_t(31));
+      sp.nsplit[i] = split_count(q.seq[i], a.window, plan.chunk);
+      sp.row0[i] = row0;
+      const int64_t items = sp.nsplit[i] > 1 ? (int64_t)q.seq[i].nq * a.heads : 0;
+      row0 += items * sp.nsplit[i];
+      sp.join_first[i + 1] = sp.join_first[i] + (int)items;
     }
+    const dim3 grid((unsigned)(q.first[q.count] * a.kv_heads));
+    if (a.d <= 64) hipLaunchKernelGGL(attn_split_kernel<64>, grid, dim3(256), 0, stream, a, q, sp);
+    else hipLaunchKernelGGL(attn_split_kernel<128>, grid, dim3(256), 0, stream, a, q, sp);
+    const int items = sp.join_first[q.count];
+    if (items) hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a, q, sp);
   }
   return hipGetLastError();
 }
@@ -990,7 +1078,7 @@ hipError_t launch_attn_bwd(const AttnBwdArgs& args, const AttnSeq* seqs, int64_t
     else hipLaunchKernelGGL(attn_dq_kernel<128>, grid, dim3(256), 0, stream, a, q);
   }
   AttnKvSplit sp{};
-  sp.splits = kv_splits(vk, a.heads, a.kv_heads);
+  sp.splits = kv_splits(vk, a.heads, a.kv_heads, a.causal, a.window);
   sp.gper = (int)ceil64(a.heads / a.kv_heads, sp.splits);
   sp.part = ws + 2 * round64(q_tokens * a.heads);
   for (size_t from = 0; from < vk.size(); from += kAttnSeqs) {

@@ -124,10 +124,10 @@ size_t lora_dx_group_ws_floats(int count, int64_t M, int64_t K, int r);
 hipError_t launch_lora_dx_group(int count, const uint16_t* X, int64_t M, int64_t K, const float* const* v, int r,
                                 float scale, int accumulate, float* ws, float* const* dA, hipStream_t stream);
 
-// dA_i = scale * (sum over `parts` partial sums part_i [parts][K][r], in order) (+ dA_i), transposed to
-// [r][K], for count (<= 4) linears in one launch
-hipError_t launch_lora_sum(int count, const float* const* part, int parts, int64_t K, int r, float scale,
-                           int accumulate, float* const* dA, hipStream_t stream);
+// out_i = scale * (sum over `parts` partial sums part_i [parts][numel], in order) (+ out_i), for count
+// (<= 8) arrays in one launch
+hipError_t launch_lora_sum(int count, const float* const* part, int parts, int64_t numel, float scale,
+                           int accumulate, float* const* out, hipStream_t stream);
 
 // Skinny forward (M <= 16): split-K dequant-GEMV on MFMA with a deterministic reduction.
 // `part` holds skinny_workspace_floats(M, N, K, r) floats; u_out receives u = x A^T [M x r].
@@ -213,7 +213,8 @@ struct AttnKvSplit {            // split of a group's query heads in the dk, dv 
 };
 // Workspace in floats; window 0: none
 size_t attn_fwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window);
-size_t attn_bwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int64_t q_tokens);
+size_t attn_bwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int causal, int window,
+                          int64_t q_tokens);
 hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream);
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, const AttnSeq* seqs, int64_t count, int64_t q_tokens, float* ws,
                            hipStream_t stream);

@@ -668,11 +668,11 @@ hipError_t launch_lora_dx_group(int count, const uint16_t* X, int64_t M, int64_t
   return hipGetLastError();
 }
 
-hipError_t launch_lora_sum(int count, const float* const* part, int parts, int64_t K, int r, float scale,
-                           int accumulate, float* const* dA, hipStream_t stream) {
+hipError_t launch_lora_sum(int count, const float* const* part, int parts, int64_t numel, float scale,
+                           int accumulate, float* const* out, hipStream_t stream) {
   if (count < 1 || count > kMaxReduceJobs) return hipErrorInvalidValue;
   ReduceJob jobs[kMaxReduceJobs];
-  for (int i = 0; i < count; ++i) jobs[i] = reduce_job(part[i], parts, K * r, K, r, true, scale, accumulate, dA[i]);
+  for (int i = 0; i < count; ++i) jobs[i] = reduce_job(part[i], parts, numel, 0, 1, false, scale, accumulate, out[i]);
   launch_reduce(jobs, count, stream);
   return hipGetLastError();
 }

@@ -212,12 +212,17 @@ __device__ __forceinline__ int find_seq(const AttnSeqs& sq, int tile) {
 // Workgroup b of a launch over tiles x kv_heads x per (`per`: workgroups that share a tile and a key
 // head). Consecutive workgroups go to the 8 XCDs in turn; with a multiple of 8 key heads each XCD
 // takes its own heads, so their keys and values stay in its L2. Tiles vary slowest: the host orders
-// them by falling work.
+// them by falling work. `pairs`: the second workgroup of every compute unit (workgroups 256 to 511) comes
+// from the other end, so that a unit that began with the most work goes on with the least.
 struct Unit {
   int tile, kvh, sub;
 };
-__device__ __forceinline__ Unit unit_of(int b, int kv_heads, int per) {
+__device__ __forceinline__ Unit unit_of(int b, int kv_heads, int per, bool pairs = false) {
   Unit u;
+  if (pairs && b >= 256 && b < 512) {
+    const int x = b & 7, m = (min((int)gridDim.x, 512) - 256 - x + 7) >> 3;   // of this XCD
+    b = 256 + x + 8 * (m - 1 - ((b - 256) >> 3));
+  }
   if (kv_heads % 8 == 0) {
     const int hx = kv_heads / 8, i = b >> 3;
     u.sub = i % per;
@@ -681,9 +686,15 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, co
 
 // ------------------------------------------------------------------------------------------
 // Backward, second launch: dk and dv. A workgroup of 4 waves takes 128 keys of one key head, 32 per
-// wave, kept in registers; the rows of q and do of its query heads stream through LDS in tiles of 64,
-// two deep. The query heads of the group can be split over several workgroups (gper heads each):
-// their fp32 results go to the workspace, and attn_dkv_sum_kernel adds them in order.
+// wave; the rows of q and do of its query heads stream through LDS, two tiles deep. The query heads of
+// the group can be split over several workgroups (gper heads each): their fp32 results go to the
+// workspace, and attn_dkv_sum_kernel adds them in order.
+// WV = 1: the keys' and the values' operands stay in registers (350 of them, one wave a SIMD) and tiles
+// have 64 rows. WV = 2: the values' operands are read from LDS and tiles have 32 rows, which leaves room
+// for two waves a SIMD. A workgroup of the first kind alone on a compute unit takes 2.4 us for 64 rows of
+// 128 keys at d = 128, of the second 3.1 us; but two of the second take 4.7 us for both, so the second is
+// better where the launch has workgroups enough (kv_plan chooses): 8192 tokens, 32 heads over 8, not
+// causal: 2.6 ms with the first (830 TFLOP/s of the four products), 2.0 ms with the second (1100).
 template <int DP, int ROWS, int NW>
 struct RowStream {   // rows [lo, hi) of q, do, lse2 and less_delta, head after head, in tiles of ROWS <= 64
   typedef TileDma<DP, ROWS, NW> Dma;
@@ -696,6 +707,12 @@ struct RowStream {   // rows [lo, hi) of q, do, lse2 and less_delta, head after 
       : a(args), q0(s.q0), nq(s.nq), head(head0), i(lo_), lo(lo_), hi(hi_) {
     qd.init(wave, lane, a.d, (uint32_t)a.q.token);
     gd.init(wave, lane, a.d, (uint32_t)a.dout.token);
+  }
+  // the values of 32 keys from j, as an LDS tile
+  static __device__ __forceinline__ void values(uint16_t* t, const AttnBwdArgs& a, const AttnSeq& s, int kvh, int j, int lane) {
+    TileDma<DP, 32, 1> vd;
+    vd.init(0, lane, a.d, (uint32_t)a.v.token);
+    vd.load(t, a.v.p + (s.k0 + j) * a.v.token + (int64_t)kvh * a.v.head, s.nk - j, a.d, (uint32_t)a.v.token, 0);
   }
   // the next tile; lse2 and less_delta go to the wave's own copies. Rows past the sequence read 0: their q
   // and do are 0 too, so they add nothing.
@@ -716,27 +733,32 @@ struct RowStream {   // rows [lo, hi) of q, do, lse2 and less_delta, head after 
   }
 };
 
-template <int DP>
-__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdArgs a, const AttnSeqs sq, const AttnKvSplit sp) {
-  constexpr int BM = 64, KS = DP / 16, DT = DP / 32;
+template <int DP, int WV>
+__global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, const AttnSeqs sq, const AttnKvSplit sp) {
+  constexpr int BM = WV == 1 ? 64 : 32, KS = DP / 16, DT = DP / 32;
   typedef Tile<DP> T;
   typedef RowStream<DP, BM, 4> Stream;
   __shared__ __attribute__((aligned(16))) uint16_t Qs[2][BM * DP];
   __shared__ __attribute__((aligned(16))) uint16_t Gs[2][BM * DP];
-  __shared__ __attribute__((aligned(16))) float Ls[2][4][BM], Ds[2][4][BM];   // lse log2(e) and -delta, a copy per wave
+  __shared__ __attribute__((aligned(16))) float Ls[2][4][64], Ds[2][4][64];   // lse log2(e) and -delta, a copy per wave
+  __shared__ __attribute__((aligned(16))) uint16_t Vs[WV == 1 ? 8 : 128 * DP];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = a.heads / a.kv_heads;
-  const Unit u = unit_of((int)blockIdx.x, a.kv_heads, sp.splits);
+  const Unit u = unit_of((int)blockIdx.x, a.kv_heads, sp.splits, WV == 2);
   const int si = find_seq(sq, u.tile);
   const AttnSeq s = sq.seq[si];
   const int j0 = (u.tile - sq.first[si]) * 128;     // first key of the workgroup
   const int shift = s.nk - s.nq;
   const int key = j0 + wave * 32 + (lane & 31);
   const bool own = key < s.nk;
-  bf16x8 kf[KS], vf[KS];
+  bf16x8 kf[KS], vf[WV == 1 ? KS : 1];
   load_rows<DP>(kf, own ? a.k.p + (s.k0 + key) * a.k.token + (int64_t)u.kvh * a.k.head : nullptr, a.d, lane);
-  load_rows<DP>(vf, own ? a.v.p + (s.k0 + key) * a.v.token + (int64_t)u.kvh * a.v.head : nullptr, a.d, lane);
+  uint16_t* const vt = Vs + (WV == 1 ? 0 : wave * 32 * DP);
+  if constexpr (WV == 1)
+    load_rows<DP>(vf, own ? a.v.p + (s.k0 + key) * a.v.token + (int64_t)u.kvh * a.v.head : nullptr, a.d, lane);
+  else
+    Stream::values(vt, a, s, u.kvh, j0 + wave * 32, lane);
 
   // query rows [i_lo, i_hi) that see some key of the workgroup
   const int jl = min(s.nk, j0 + 128) - 1;
@@ -788,7 +810,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdArgs a, c
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Qs[st], 32 * mt, ks, lane), kf[ks], sc);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) dp = mfma(T::rows(Gs[st], 32 * mt, ks, lane), vf[ks], dp);
+        for (int ks = 0; ks < KS; ++ks)
+          dp = mfma(T::rows(Gs[st], 32 * mt, ks, lane), WV == 1 ? vf[WV == 1 ? ks : 0] : T::rows(vt, 0, ks, lane), dp);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const f32x4 x = *reinterpret_cast<const f32x4*>(&Ls[st][wave][32 * mt + 8 * g + 4 * (lane >> 5)]);
@@ -974,33 +997,43 @@ static int64_t dkv_row_tiles(const AttnSeq& s, int t, int causal, int window) {
   return hi > lo ? ceil64(hi - lo, 64) : 0;
 }
 
-// Splits of the dk, dv launch over the query heads of a group. The launch takes as long as its longest
-// workgroup or the mean over the compute units (one workgroup each at a time), about 2.6 us for a tile of
-// 64 rows; splitting shortens the first, and the fp32 results of the parts cost about 0.03 us for every
-// tile of 128 keys and part (written, read and added). Packed sequences of 1500, 1031, 783, 700, 64, 17
-// and 1 tokens with 8 heads to a key head: 2 parts 255 us + 17 us for the sums, 3 parts 198 + 26.
-static int kv_splits(const std::vector<AttnSeq>& v, int heads, int kv_heads, int causal, int window) {
+// Plan of the dk, dv launch: parts that the query heads of a group are split into, and waves per SIMD
+// (see attn_dkv_kernel). The launch takes as long as its longest workgroup alone or as the mean over the
+// compute units, counted in tiles of 64 rows of 128 keys; the parts' fp32 results (written, read and
+// added) cost 0.03 us for every tile of 128 keys and part. The coefficients (us) are fitted to d = 128.
+// Estimate and measurement, sums included: 64 heads over 8, packed sequences of 1500, 1031, 783, 700, 64,
+// 17 and 1 tokens: one wave, 2 parts 254 and 263, 4 parts 271 and 270; two waves, 2 parts 320 and 322, 4
+// parts 233 and 238, 8 parts 269 and 262. 32 heads over 8, one sequence of 2048, 4 parts: one wave 114 and
+// 112, two waves 118 and 124.
+struct KvPlan {
+  int splits, gper, waves;
+};
+static KvPlan kv_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, int d, int causal, int window) {
   const int G = heads / kv_heads;
   int64_t tiles = 0, longest = 0, total = 0;
   for (const AttnSeq& s : v) {
     tiles += k_tiles(s);
-    if (tiles * kv_heads >= 16 * kUnits) return 1;   // workgroups enough
+    if (tiles * kv_heads >= 16 * kUnits) return KvPlan{1, G, 2};   // workgroups enough
     for (int t = 0; t < k_tiles(s); ++t) {
       const int64_t n = dkv_row_tiles(s, t, causal, window);
       longest = std::max(longest, n);
       total += n;
     }
   }
-  int best = 1;
-  double best_cost = 0;
+  KvPlan best{1, G, 2};
+  double best_cost = -1;
   for (int want = 1; want <= G; ++want) {
-    const int gper = (int)ceil64(G, want), splits = (int)ceil64(G, gper);
-    if (splits != want) continue;
-    const double mean = (double)total * G * kv_heads / kUnits;
-    const double cost = 2.6 * std::max((double)longest * gper, mean) + (splits > 1 ? 4 + 0.03 * tiles * kv_heads * splits : 0);
-    if (want == 1 || cost < best_cost) {
-      best = splits;
-      best_cost = cost;
+    const int gper = (int)ceil64(G, want);
+    if (ceil64(G, gper) != want) continue;
+    const double mean = (double)total * G * kv_heads / kUnits, most = (double)longest * gper;
+    const double sums = want > 1 ? 4 + 0.03 * tiles * kv_heads * want : 0;
+    const double one = std::max(2.4 * most, 2.8 * mean) + sums, two = std::max(3.1 * most, 2.35 * mean) + sums;
+    for (int waves = d <= 64 ? 2 : 1; waves <= 2; ++waves) {   // the small tiles of d <= 64 leave room for two waves anyway
+      const double cost = waves == 1 ? one : two;
+      if (best_cost < 0 || cost < best_cost) {
+        best = KvPlan{want, gper, waves};
+        best_cost = cost;
+      }
     }
   }
   return best;
@@ -1025,8 +1058,8 @@ size_t attn_fwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_
 size_t attn_bwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int causal, int window,
                           int64_t q_tokens) {
   const std::vector<AttnSeq> v = by_work(seqs, count, true);
-  const int splits = kv_splits(v, heads, kv_heads, causal, window);
-  return (size_t)(2 * round64(q_tokens * heads) + dkv_part_floats(v, splits, kv_heads, padded_d(d)));
+  const KvPlan plan = kv_plan(v, heads, kv_heads, d, causal, window);
+  return (size_t)(2 * round64(q_tokens * heads) + dkv_part_floats(v, plan.splits, kv_heads, padded_d(d)));
 }
 
 hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream) {
@@ -1077,19 +1110,18 @@ hipError_t launch_attn_bwd(const AttnBwdArgs& args, const AttnSeq* seqs, int64_t
     if (a.d <= 64) hipLaunchKernelGGL(attn_dq_kernel<64>, grid, dim3(256), 0, stream, a, q);
     else hipLaunchKernelGGL(attn_dq_kernel<128>, grid, dim3(256), 0, stream, a, q);
   }
-  AttnKvSplit sp{};
-  sp.splits = kv_splits(vk, a.heads, a.kv_heads, a.causal, a.window);
-  sp.gper = (int)ceil64(a.heads / a.kv_heads, sp.splits);
-  sp.part = ws + 2 * round64(q_tokens * a.heads);
+  const KvPlan plan = kv_plan(vk, a.heads, a.kv_heads, a.d, a.causal, a.window);
+  const AttnKvSplit sp{ws + 2 * round64(q_tokens * a.heads), plan.splits, plan.gper};
   for (size_t from = 0; from < vk.size(); from += kAttnSeqs) {
     const AttnSeqs q = pack_seqs(vk, from, k_tiles);
     const int units = q.first[q.count] * a.kv_heads;
     const dim3 grid((unsigned)(units * sp.splits)), sums((unsigned)(units * 2));
     if (a.d <= 64) {
-      hipLaunchKernelGGL(attn_dkv_kernel<64>, grid, dim3(256), 0, stream, a, q, sp);
+      hipLaunchKernelGGL((attn_dkv_kernel<64, 2>), grid, dim3(256), 0, stream, a, q, sp);
       if (sp.splits > 1) hipLaunchKernelGGL(attn_dkv_sum_kernel<64>, sums, dim3(256), 0, stream, a, q, sp);
     } else {
-      hipLaunchKernelGGL(attn_dkv_kernel<128>, grid, dim3(256), 0, stream, a, q, sp);
+      if (plan.waves == 1) hipLaunchKernelGGL((attn_dkv_kernel<128, 1>), grid, dim3(256), 0, stream, a, q, sp);
+      else hipLaunchKernelGGL((attn_dkv_kernel<128, 2>), grid, dim3(256), 0, stream, a, q, sp);
       if (sp.splits > 1) hipLaunchKernelGGL(attn_dkv_sum_kernel<128>, sums, dim3(256), 0, stream, a, q, sp);
     }
   }

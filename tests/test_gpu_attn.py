@@ -110,6 +110,14 @@ def test_enough_rows_to_fill_the_gpu(d, heads, kv, causal, window):
     _run("many workgroups, strided", _packed(257, 200), 128, 8, d, causal=causal, window=window, layout="heads")
 
 
+@pytest.mark.parametrize("d", [80, 128])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 40)])
+def test_many_equal_sequences(d, causal, window):
+    # enough equal work for the backward's form of two waves a SIMD
+    _run("equal sequences", _packed(*([100, 64, 129, 33] * 4)), 64, 64, d, causal=causal, window=window)
+    _run("equal sequences, shared heads", _packed(*([130] * 20)), 16, 4, d, causal=causal, window=window)
+
+
 def test_not_causal():
     _run("not causal", _packed(129, 64, 1), 4, 4, 64, causal=False)
     _run("cross", [(0, 70, 0, 33), (70, 3, 33, 200)], 4, 2, 128, causal=False)

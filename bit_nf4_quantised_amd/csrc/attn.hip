@@ -313,9 +313,10 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnFwdArgs a, c
   bf16x8 qf[KS];
   load_rows<DP>(qf, row < s.nq ? a.q.p + (s.q0 + row) * a.q.token + (int64_t)head * a.q.head : nullptr, a.d, lane);
 
-  // keys that some row of the workgroup (of this wave) sees
+  // keys that some row of the workgroup (of this wave) sees; none before the first is read: with a window a
+  // cache may hold anything there, and 0 times NaN is no zero
   const int r1 = min(s.nq, r0 + 128) - 1;
-  const int k_lo = visible(r0 + shift, s.nk, a.causal, a.window).lo & ~(BN - 1);
+  const int k_lo = visible(r0 + shift, s.nk, a.causal, a.window).lo;
   const int k_hi = visible(r1 + shift, s.nk, a.causal, a.window).hi;
   const int w0 = r0 + wave * 32, w1 = min(s.nq - 1, w0 + 31);
   const Range wa = visible(w0 + shift, s.nk, a.causal, a.window), wb = visible(w1 + shift, s.nk, a.causal, a.window);
@@ -442,8 +443,10 @@ __global__ __launch_bounds__(256, DP == 128 ? 1 : 2) void attn_split_kernel(cons
   w.first = visible(t0 + shift, s.nk, a.causal, a.window);
   w.last = visible(t1 + shift, s.nk, a.causal, a.window);
   w.mine = visible(tok + shift, s.nk, a.causal, a.window);
-  const int k_lo = max(w.first.lo & ~(BN - 1), sp.lo[si] + split * sp.chunk);
-  const int k_hi = min(w.last.hi, sp.lo[si] + (split + 1) * sp.chunk);
+  // tiles are counted from the first key that the sequence's first row sees (none before it is read)
+  const int lo = sp.lo[si];
+  const int k_lo = lo + max((w.first.lo - lo) & ~(BN - 1), split * sp.chunk);
+  const int k_hi = min(w.last.hi, lo + (split + 1) * sp.chunk);
   const int j_w = k_lo + wave * BN;   // the wave's first tile; its tiles are 4 apart
   w.kv.init(a.k, a.v, s, u.kvh, a.d, 0, lane);
   if (j_w < k_hi) w.kv.load(ring0[0][wave], ring0[1][wave], j_w, 0);
@@ -634,7 +637,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, co
   for (int i = 0; i < 16; ++i) less_delta[i] = -delta;
 
   const int r1 = min(s.nq, r0 + 128) - 1;
-  const int k_lo = visible(r0 + shift, s.nk, a.causal, a.window).lo & ~(BN - 1);
+  const int k_lo = visible(r0 + shift, s.nk, a.causal, a.window).lo;
   const int k_hi = visible(r1 + shift, s.nk, a.causal, a.window).hi;
   const int w0 = r0 + wave * 32, w1 = min(s.nq - 1, w0 + 31);
   const Range wa = visible(w0 + shift, s.nk, a.causal, a.window), wb = visible(w1 + shift, s.nk, a.causal, a.window);
@@ -945,8 +948,7 @@ struct FwdPlan {
   int64_t part_floats = 0;  // workspace of one launch (the largest)
 };
 static int split_count(const AttnSeq& s, int window, int64_t chunk) {
-  const int64_t lo = first_key(s, window) & ~int64_t(31);
-  return (int)std::max<int64_t>(1, ceil64(s.nk - lo, chunk));
+  return (int)std::max<int64_t>(1, ceil64(s.nk - first_key(s, window), chunk));
 }
 static int64_t row_tiles(const AttnSeq& s, int G) { return ceil64((int64_t)s.nq * G, 32); }
 
@@ -957,7 +959,7 @@ static int64_t row_tiles(const AttnSeq& s, int G) { return ceil64((int64_t)s.nq 
 // to 8191 keys it took 42 us where ranges for two workgroups a unit on average took 52.
 static int64_t split_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, int window) {
   int64_t longest = 1, best = 0, best_cost = INT64_MAX;
-  for (const AttnSeq& s : v) longest = std::max(longest, (int64_t)s.nk - (first_key(s, window) & ~int64_t(31)));
+  for (const AttnSeq& s : v) longest = std::max(longest, s.nk - first_key(s, window));
   for (int64_t chunk = 256;; chunk += std::max<int64_t>(128, chunk / 8 / 128 * 128)) {
     int64_t wgs = 0;
     for (const AttnSeq& s : v) wgs += row_tiles(s, G) * split_count(s, window, chunk) * kv_heads;
@@ -1082,7 +1084,7 @@ hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t co
     sp.chunk = (int)plan.chunk;
     int64_t row0 = 0;
     for (int i = 0; i < q.count; ++i) {
-      sp.lo[i] = (int)(first_key(q.seq[i], a.window) & ~int64_t(31));
+      sp.lo[i] = (int)first_key(q.seq[i], a.window);
       sp.nsplit[i] = split_count(q.seq[i], a.window, plan.chunk);
       sp.row0[i] = row0;
       const int64_t items = sp.nsplit[i] > 1 ? (int64_t)q.seq[i].nq * a.heads : 0;

@@ -289,17 +289,25 @@ struct Online {
 };
 
 // ------------------------------------------------------------------------------------------
-// Forward. A workgroup of 4 waves takes 128 query rows of one head, 32 per wave; keys and values
-// stream through LDS in tiles of 64, two tiles deep, by LDS-DMA.
-template <int DP>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnFwdArgs a, const AttnSeqs sq) {
+// Forward. 4 waves take 128 query rows of one head, 32 per wave; keys and values stream through LDS in
+// tiles of 64, two tiles deep, by LDS-DMA. Bound by the matrix unit and, in launches that fill the GPU,
+// by its power: 8192 tokens, 32 heads over 8, d 128, not causal, 1051 us = 1046 TFLOP/s, where a plain
+// product of 16384^3 reaches 1355. A tile costs a workgroup that shares its compute unit with another
+// 0.93 us, but 1.15 to 1.4 us alone, with one wave a SIMD that waits for its own reads and exponentials.
+// So a launch of at most one workgroup a compute unit takes GR = 2: two groups of 4 waves take the tiles of
+// the same rows in turn and are joined at the end (256 workgroups of up to 4096 keys: 94 us with one
+// group, 78 with two). With more workgroups the other kind of pair is better, as its two members start and
+// end at different times: 2368 workgroups of packed sequences 109 us against 137.
+template <int DP, int GR>
+__global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs a, const AttnSeqs sq) {
   constexpr int BN = 64, KS = DP / 16, DT = DP / 32;
   typedef Tile<DP> T;
   typedef KvStream<DP, BN, 4> Stream;
-  __shared__ __attribute__((aligned(16))) uint16_t Ks[2][BN * DP];
-  __shared__ __attribute__((aligned(16))) uint16_t Vs[2][BN * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t Ks[GR][2][BN * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t Vs[GR][2][BN * DP];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
+  const int grp = GR == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 8);
   const int G = a.heads / a.kv_heads;
   const Unit u = unit_of((int)blockIdx.x, a.kv_heads, G);
   const int si = find_seq(sq, u.tile);
@@ -321,7 +329,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnFwdArgs a, c
   const int w0 = r0 + wave * 32, w1 = min(s.nq - 1, w0 + 31);
   const Range wa = visible(w0 + shift, s.nk, a.causal, a.window), wb = visible(w1 + shift, s.nk, a.causal, a.window);
   const Range mine = visible(row + shift, s.nk, a.causal, a.window);
-  const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
+  const int nt = k_hi > k_lo ? (k_hi - k_lo + GR * BN - 1) / (GR * BN) : 0;   // of each group
 
   Stream kv;
   kv.init(a.k, a.v, s, u.kvh, a.d, wave, lane);
@@ -329,24 +337,25 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnFwdArgs a, c
   Online<DT> acc;
   acc.init();
   const float slack = kSlack / a.c;
-  if (nt > 0) kv.load(Ks[0], Vs[0], k_lo, wave);
+  const int j_g = k_lo + grp * BN;   // the group's first tile; its tiles are GR apart
+  if (nt > 0) kv.load(Ks[grp][0], Vs[grp][0], j_g, wave);
   for (int t = 0; t < nt; ++t) {
     const int st = t & 1;
     if (t + 1 < nt) {
-      kv.load(Ks[st ^ 1], Vs[st ^ 1], k_lo + (t + 1) * BN, wave);
+      kv.load(Ks[grp][st ^ 1], Vs[grp][st ^ 1], j_g + (t + 1) * GR * BN, wave);
       wait_vmcnt<Stream::kLoads>();   // loads complete in order: tile t is in, tile t + 1 may be in flight
     } else {
       wait_vmcnt<0>();
     }
     lds_barrier();
-    const int j0 = k_lo + t * BN;
+    const int j0 = j_g + t * GR * BN;
     if (j0 < wb.hi && j0 + BN > wa.lo) {
       f32x16 sc[BN / 32];
 #pragma unroll
       for (int kt = 0; kt < BN / 32; ++kt) {
         sc[kt] = zero16();
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) sc[kt] = mfma(T::rows(Ks[st], 32 * kt, ks, lane), qf[ks], sc[kt]);
+        for (int ks = 0; ks < KS; ++ks) sc[kt] = mfma(T::rows(Ks[grp][st], 32 * kt, ks, lane), qf[ks], sc[kt]);
       }
       // some row of the wave does not see some key of the tile
       if (j0 + BN > wa.hi || j0 < wb.lo) {
@@ -358,18 +367,60 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnFwdArgs a, c
       for (int kk = 0; kk < BN / 16; ++kk) {
         const bf16x8 p = pack8(sc[kk / 2], kk & 1);
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(T::cols(Vs[st], 16 * kk, dt, lane), p, acc.o[dt]);
+        for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(T::cols(Vs[grp][st], 16 * kk, dt, lane), p, acc.o[dt]);
       }
     }
     lds_barrier();
   }
 
-  const float l = half_sum(acc.l);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  float l = half_sum(acc.l);
   uint16_t* dst = row < s.nq ? a.o.p + (s.q0 + row) * a.o.token + (int64_t)head * a.o.head : nullptr;
+  if constexpr (GR == 1) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int dt = 0; dt < DT; ++dt) store_cols(dst, acc.o[dt], inv, dt, a.d, lane);
-  if (a.lse && lane < 32 && row < s.nq)
+    for (int dt = 0; dt < DT; ++dt) store_cols(dst, acc.o[dt], inv, dt, a.d, lane);
+  } else {
+    // join the groups: each keeps half of the columns and gets the other group's sums of them (the tiles'
+    // place in LDS is free: every wave is past the loop's last barrier)
+    __shared__ float Ms[GR][128], Ls[GR][128];
+    const int rl = wave * 32 + (lane & 31);
+    if (lane < 32) {
+      Ms[grp][rl] = acc.m;
+      Ls[grp][rl] = l;
+    }
+    constexpr int H = DT / 2;
+    f32x4* const half = reinterpret_cast<f32x4*>(&Ks[0][0][0]) + wave * (H * 4 * 64) + lane;
+    static_assert(2 * 4 * H * 4 * 64 * 16 <= sizeof(Ks), "both halves fit");
+#pragma unroll
+    for (int dt = 0; dt < H; ++dt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f32x4 x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = grp ? acc.o[dt][4 * g + k] : acc.o[dt + H][4 * g + k];
+        half[(grp ^ 1) * (4 * H * 4 * 64) + (dt * 4 + g) * 64] = x;
+      }
+    lds_barrier();
+    const float mo = Ms[grp ^ 1][rl], lo = Ls[grp ^ 1][rl], m = fmaxf(acc.m, mo);
+    const float mc = m == -INFINITY ? 0.f : m * a.c;
+    const float fm = acc.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(acc.mc - mc);
+    const float fo = mo == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mo * a.c - mc);
+    l = l * fm + lo * fo;
+    acc.mc = mc;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int dt = 0; dt < H; ++dt) {
+      f32x16 v;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 x = half[grp * (4 * H * 4 * 64) + (dt * 4 + g) * 64];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[4 * g + k] = (grp ? acc.o[dt + H][4 * g + k] : acc.o[dt][4 * g + k]) * fm + x[k] * fo;
+      }
+      store_cols(dst, v, inv, grp * H + dt, a.d, lane);
+    }
+  }
+  if (a.lse && grp == 0 && lane < 32 && row < s.nq)
     a.lse[(int64_t)head * a.lse_stride + s.q0 + row] = l > 0.f ? acc.mc * kLn2 + __logf(l) : -INFINITY;
 }
 
@@ -938,9 +989,12 @@ static int64_t first_key(const AttnSeq& s, int window) {
   return window ? std::max<int64_t>(0, (int64_t)s.nk - s.nq - window + 1) : 0;
 }
 
-// The forward's plan. Sequences of more than kFewRows query rows go to attn_fwd_kernel when its
-// workgroups fill the GPU (256 compute units); the others, and these when they are too few, to
-// attn_split_kernel, with one length of key range for all.
+// The forward's plan. Sequences of up to kFewRows query rows go to attn_split_kernel. The others go to
+// attn_fwd_kernel when its workgroups outnumber the compute units (256), or when its estimate, the longest
+// workgroup at 0.94 us for 64 keys and 7 us around it, is below that of attn_split_kernel (split_chunk);
+// all sequences of a launch of attn_split_kernel have one length of key range. Measured, forward and
+// split: 512 tokens of 600 keys, 32 heads over 8, 17 and 20 us; four sequences of 300, 8 heads over 2, 11
+// and 15; 128 tokens of 4096 keys, 32 heads over 8, 64 and 29.
 constexpr int kFewRows = 16, kUnits = 256;
 struct FwdPlan {
   std::vector<AttnSeq> many, few;
@@ -957,7 +1011,7 @@ static int64_t row_tiles(const AttnSeq& s, int G) { return ceil64((int64_t)s.nq 
 // 224 keys (start, first loads, joining the waves: 5 us against 0.022 us a key), and joining ranges costs
 // another launch (4 us, 180 keys). The range length with the smallest sum wins; for sixteen sequences of 1
 // to 8191 keys it took 42 us where ranges for two workgroups a unit on average took 52.
-static int64_t split_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, int window) {
+static int64_t split_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, int window, int64_t* cost_of) {
   int64_t longest = 1, best = 0, best_cost = INT64_MAX;
   for (const AttnSeq& s : v) longest = std::max(longest, s.nk - first_key(s, window));
   for (int64_t chunk = 256;; chunk += std::max<int64_t>(128, chunk / 8 / 128 * 128)) {
@@ -968,18 +1022,30 @@ static int64_t split_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, i
       best_cost = cost;
       best = chunk;
     }
-    if (chunk >= longest) return best;
+    if (chunk >= longest) break;
   }
+  *cost_of = best_cost;
+  return best;
 }
 static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, int d, int window) {
   FwdPlan p;
   const int G = heads / kv_heads;
-  int64_t wgs = 0;
-  for (const AttnSeq& s : v)
-    if (s.nq > kFewRows) wgs += (int64_t)q_tiles(s) * heads;
-  for (const AttnSeq& s : v) (wgs >= kUnits && s.nq > kFewRows ? p.many : p.few).push_back(s);
+  int64_t wgs = 0, keys = 0, cost;
+  for (const AttnSeq& s : v) {
+    (s.nq > kFewRows ? p.many : p.few).push_back(s);
+    if (s.nq <= kFewRows) continue;
+    wgs += (int64_t)q_tiles(s) * heads;
+    keys = std::max(keys, s.nk - std::max<int64_t>(0, window ? s.nk - 128 - window : 0));
+  }
+  if (!p.many.empty() && wgs <= kUnits) {
+    split_chunk(p.many, G, kv_heads, window, &cost);
+    if (7 + 0.94 / 64 * (double)keys > 0.022 * (double)cost) {
+      p.many.clear();
+      p.few = v;
+    }
+  }
   if (p.few.empty()) return p;
-  p.chunk = split_chunk(p.few, G, kv_heads, window);
+  p.chunk = split_chunk(p.few, G, kv_heads, window, &cost);
   for (size_t from = 0; from < p.few.size(); from += kAttnSeqs) {
     int64_t f = 0;
     for (size_t i = from; i < p.few.size() && i < from + kAttnSeqs; ++i) {
@@ -1072,8 +1138,13 @@ hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t co
   for (size_t from = 0; from < plan.many.size(); from += kAttnSeqs) {
     const AttnSeqs q = pack_seqs(plan.many, from, q_tiles);
     const dim3 grid((unsigned)(q.first[q.count] * a.heads));
-    if (a.d <= 64) hipLaunchKernelGGL(attn_fwd_kernel<64>, grid, dim3(256), 0, stream, a, q);
-    else hipLaunchKernelGGL(attn_fwd_kernel<128>, grid, dim3(256), 0, stream, a, q);
+    if (grid.x <= kUnits) {   // see attn_fwd_kernel
+      if (a.d <= 64) hipLaunchKernelGGL((attn_fwd_kernel<64, 2>), grid, dim3(512), 0, stream, a, q);
+      else hipLaunchKernelGGL((attn_fwd_kernel<128, 2>), grid, dim3(512), 0, stream, a, q);
+    } else {
+      if (a.d <= 64) hipLaunchKernelGGL((attn_fwd_kernel<64, 1>), grid, dim3(256), 0, stream, a, q);
+      else hipLaunchKernelGGL((attn_fwd_kernel<128, 1>), grid, dim3(256), 0, stream, a, q);
+    }
   }
   for (size_t from = 0; from < plan.few.size(); from += kAttnSeqs) {
     const AttnSeqs q = pack_seqs(plan.few, from, [&](const AttnSeq& s) {

@@ -431,7 +431,9 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
 // own without barriers: a tile is read into registers whole and its place refilled before the
 // arithmetic, so two tiles (32 KiB a wave at d = 128) are always on their way. The waves' results are
 // joined in LDS; with several ranges they go to the workspace and attn_join_kernel joins them, in order.
-// Bound by memory: the keys and values, once.
+// Bound by memory: the keys and values, once. One token each for sixteen sequences of 1 to 8191 keys, 64
+// heads over 8, d 128: 42 us for 224 MB (5.3 TB/s) and 4 us for the join; with one tile in flight a wave and
+// ranges for two workgroups a compute unit it took 58.
 template <int DP>
 struct SplitWave {
   static constexpr int BN = 32, KS = DP / 16, DT = DP / 32;
@@ -641,8 +643,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnFwdArgs a, con
 }
 
 // ------------------------------------------------------------------------------------------
-// Backward, first launch: delta (and, for the second launch, lse log2(e) and -delta) and dq. As the forward (128 query rows a workgroup, keys streamed),
-// with the probabilities recomputed from lse.
+// Backward, first launch: delta (and, for the second launch, lse log2(e) and -delta) and dq. As the
+// forward (128 query rows a workgroup, keys streamed), with the probabilities recomputed from lse: three
+// products a tile instead of two, 8192 tokens, 32 heads over 8, d 128, not causal 1520 us = 1085 TFLOP/s.
+// delta is formed from the forward's rounded o, as the call gets it: an error of up to 2^-9 |do||o| in every
+// dS of a row, which with the rounding of dS itself puts dq and dk at 2.5e-3 of their norm from the exact
+// ones (their own rounding to bf16 alone is 1.7e-3), and at 4e-3 where rows see few keys. -delta enters the
+// products as their starting value, which saves a subtraction per score.
+// One pass over the pairs could give dq, dk and dv together with five products instead of seven, but its
+// sums of dq over key tiles would need atomics, in no fixed order, or a partial dq per key tile.
 template <int DP>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, const AttnSeqs sq) {
   constexpr int BN = 64, KS = DP / 16, DT = DP / 32;
@@ -989,12 +998,15 @@ static int64_t first_key(const AttnSeq& s, int window) {
   return window ? std::max<int64_t>(0, (int64_t)s.nk - s.nq - window + 1) : 0;
 }
 
-// The forward's plan. Sequences of up to kFewRows query rows go to attn_split_kernel. The others go to
-// attn_fwd_kernel when its workgroups outnumber the compute units (256), or when its estimate, the longest
-// workgroup at 0.94 us for 64 keys and 7 us around it, is below that of attn_split_kernel (split_chunk);
-// all sequences of a launch of attn_split_kernel have one length of key range. Measured, forward and
-// split: 512 tokens of 600 keys, 32 heads over 8, 17 and 20 us; four sequences of 300, 8 heads over 2, 11
-// and 15; 128 tokens of 4096 keys, 32 heads over 8, 64 and 29.
+// The forward's plan. Sequences of up to kFewRows query rows are work for attn_split_kernel; the others go
+// to attn_fwd_kernel when its workgroups outnumber the compute units (256), or when its estimate, the
+// longest workgroup at 0.94 us for 64 keys and 7 us around it, is below that of attn_split_kernel
+// (split_chunk); all sequences of a launch of attn_split_kernel have one length of key range. Measured,
+// forward and split: 512 tokens of 600 keys, 32 heads over 8, 17 and 20 us; four sequences of 300, 8 heads
+// over 2, 11 and 15; 128 tokens of 4096 keys, 32 heads over 8, 64 and 29.
+// Beside attn_fwd_kernel a launch of attn_split_kernel costs 4 us even for one token, so the short sequences
+// stay with the others if that adds less work than 4 us and none is longer than the longest of these (a
+// sequence of one token packed with 4095 others, 64 heads over 8: 106 us against 110).
 constexpr int kFewRows = 16, kUnits = 256;
 struct FwdPlan {
   std::vector<AttnSeq> many, few;
@@ -1030,19 +1042,29 @@ static int64_t split_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, i
 static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, int d, int window) {
   FwdPlan p;
   const int G = heads / kv_heads;
-  int64_t wgs = 0, keys = 0, cost;
+  // keys that a workgroup of 128 rows sees at most
+  auto seen = [&](const AttnSeq& s) { return window ? std::min<int64_t>(s.nk, (int64_t)window + 128) : (int64_t)s.nk; };
+  int64_t wgs = 0, keys = 0, few_keys = 0, few_tiles = 0, cost;
   for (const AttnSeq& s : v) {
-    (s.nq > kFewRows ? p.many : p.few).push_back(s);
-    if (s.nq <= kFewRows) continue;
-    wgs += (int64_t)q_tiles(s) * heads;
-    keys = std::max(keys, s.nk - std::max<int64_t>(0, window ? s.nk - 128 - window : 0));
+    if (s.nq > kFewRows) {
+      p.many.push_back(s);
+      wgs += (int64_t)q_tiles(s) * heads;
+      keys = std::max(keys, seen(s));
+    } else {
+      p.few.push_back(s);
+      few_keys = std::max(few_keys, seen(s));
+      few_tiles += ceil64(seen(s), 64) * heads;
+    }
   }
   if (!p.many.empty() && wgs <= kUnits) {
     split_chunk(p.many, G, kv_heads, window, &cost);
-    if (7 + 0.94 / 64 * (double)keys > 0.022 * (double)cost) {
-      p.many.clear();
-      p.few = v;
-    }
+    if (7 + 0.94 / 64 * (double)keys > 0.022 * (double)cost) p.many.clear();
+  }
+  if (p.many.empty()) {
+    p.few = v;
+  } else if (few_keys <= keys && 0.94 * (double)few_tiles < 4.0 * kUnits) {
+    p.many = v;
+    p.few.clear();
   }
   if (p.few.empty()) return p;
   p.chunk = split_chunk(p.few, G, kv_heads, window, &cost);

@@ -11,7 +11,8 @@
 
 namespace nf4 {
 
-// Packing: a lane takes 8 values, 8 lanes a block. Bound by memory: 2 bytes in and 1.03 out per value.
+// Packing: a lane takes 8 values, 8 lanes a block. Bound by memory: 2 bytes in and 1.03 out per value
+// (2048 x 14336: 16 us, 5.5 TB/s).
 __global__ __launch_bounds__(256) void act8_pack_kernel(const u32x4* __restrict__ x, int64_t vecs, u32x2* __restrict__ codes,
                                                         uint16_t* __restrict__ absmax) {
   constexpr int U = 4;   // loads in flight per lane
@@ -32,7 +33,8 @@ __global__ __launch_bounds__(256) void act8_pack_kernel(const u32x4* __restrict_
   }
 }
 
-// Unpacking: a lane takes 8 values. Bound by memory: 1.03 bytes in and 2 out per value.
+// Unpacking: a lane takes 8 values. Bound by memory: 1.03 bytes in and 2 out per value (2048 x 14336: 15 us,
+// 6 TB/s).
 __global__ __launch_bounds__(256) void act8_unpack_kernel(const u32x2* __restrict__ codes, const uint16_t* __restrict__ absmax,
                                                           int64_t vecs, u32x4* __restrict__ x) {
   constexpr int U = 4;
@@ -87,7 +89,9 @@ hipError_t launch_act8_unpack(const int8_t* codes, const uint16_t* absmax, int64
 // In v_mfma_f32_16x16x32_bf16 a lane's operand fragment is 8 rows of one column, so a lane loads one
 // dword (4 columns) from each of 8 rows and keeps all four columns: column tile t is the columns
 // 4 i + t of the block, and nothing is transposed. The rank operand is scaled in fp32 and split into a
-// bf16 pair hi + lo, as the passes over bf16 inputs split theirs (relative error 2^-17).
+// bf16 pair hi + lo, as the passes over bf16 inputs split theirs (relative error 2^-17). Bound by its reads:
+// 2048 rows, K = 4096, two linears of rank 16 (8.7 MB of checkpoint) 11 us and 5 for the sums, most of it
+// the latency of a workgroup's four or so chunks in turn; dX beside it takes 480.
 struct Dx8Tile {
   const float* v;      // [M x r], at the tile's first column
   float* out;          // at the tile's first row: partial sums [row ranges][r][K], or dA [r][K] itself

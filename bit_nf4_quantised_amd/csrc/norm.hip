@@ -9,6 +9,9 @@
 // Both are bound by memory: 8 bytes per value forward (two bf16 in, two out; 9.03 with the codes) and
 // 8 backward (dy, h, dh in, dx out). A row is read once and kept in registers, V 16-byte vectors a
 // thread: by one wave up to 2048 columns (four rows a workgroup, no barrier), by a workgroup above.
+// Measured: 4096 x 8192 forward 51 us (5.3 TB/s), backward with dw 45 + 5 us (6 TB/s for the first; its
+// inputs are partly in the memory-side cache); 2048 x 4096 with the checkpoint 14 us (5.4 TB/s). A copy of
+// 4 GiB reaches 4.7 TB/s.
 #include "act8.h"
 #include "launch.h"
 

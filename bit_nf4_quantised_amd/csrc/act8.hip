@@ -91,7 +91,7 @@ hipError_t launch_act8_unpack(const int8_t* codes, const uint16_t* absmax, int64
 // 4 i + t of the block, and nothing is transposed. The rank operand is scaled in fp32 and split into a
 // bf16 pair hi + lo, as the passes over bf16 inputs split theirs (relative error 2^-17). Bound by its reads:
 // 2048 rows, K = 4096, two linears of rank 16 (8.7 MB of checkpoint) 11 us and 5 for the sums, most of it
-// the latency of a workgroup's four or so chunks in turn; dX beside it takes 480.
+// latency (512 workgroups whose waves take one chunk each); dX beside it takes 480.
 struct Dx8Tile {
   const float* v;      // [M x r], at the tile's first column
   float* out;          // at the tile's first row: partial sums [row ranges][r][K], or dA [r][K] itself

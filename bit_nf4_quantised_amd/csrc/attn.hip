@@ -1010,6 +1010,7 @@ static AttnSeqs pack_seqs(const std::vector<AttnSeq>& v, size_t from, F tiles_of
   return q;
 }
 
+static int padded_d(int d) { return d <= 64 ? 64 : 128; }
 static int q_tiles(const AttnSeq& s) { return (int)ceil64(s.nq, 128); }
 static int k_tiles(const AttnSeq& s) { return (int)ceil64(s.nk, 128); }
 
@@ -1039,32 +1040,42 @@ static int split_count(const AttnSeq& s, int window, int64_t chunk) {
 static int64_t row_tiles(const AttnSeq& s, int G) { return ceil64((int64_t)s.nq * G, 32); }
 
 // A compute unit holds one workgroup of attn_split_kernel at a time, so the launch takes as many rounds
-// as there are workgroups to a unit, each as long as a range and a fixed part that costs about as much as
-// 224 keys (start, first loads, joining the waves: 5 us against 0.022 us a key), and joining ranges costs
-// another launch (4 us, 180 keys). The range length with the smallest sum wins; for sixteen sequences of 1
-// to 8191 keys it took 42 us where ranges for two workgroups a unit on average took 52.
-static int64_t split_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, int window, int64_t* cost_of) {
-  int64_t longest = 1, best = 0, best_cost = INT64_MAX;
+// as there are workgroups to a unit, each as long as a range and a fixed part of 5 us (start, first loads,
+// joining the waves), and joining ranges costs another launch, 4 us. A key takes a workgroup 0.0064 us by
+// the latency of its own loads, 0.0096 where all units read keys that others read too, and 0.022 where all
+// read their own (d = 128; less in proportion for smaller tiles). The range length with the smallest sum
+// wins. Sixteen sequences of 1 to 8191 keys, 64 heads over 8: 42 us, where ranges for two workgroups a unit on
+// average took 52; one sequence of 601 keys, 32 heads over 8: one range 10.8 us, three and the join 13.8; of
+// 2000 keys one range 19 and four 15; 128 tokens over 4096 keys: two ranges, 29 us measured and estimated.
+static int64_t split_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, int d, int window, double* cost_us) {
+  const double size = padded_d(d) / 128.0;
+  int64_t longest = 1, best = 0;
+  *cost_us = -1;
   for (const AttnSeq& s : v) longest = std::max(longest, s.nk - first_key(s, window));
   for (int64_t chunk = 256;; chunk += std::max<int64_t>(128, chunk / 8 / 128 * 128)) {
-    int64_t wgs = 0;
-    for (const AttnSeq& s : v) wgs += row_tiles(s, G) * split_count(s, window, chunk) * kv_heads;
-    const int64_t cost = ceil64(wgs, kUnits) * (std::min(chunk, longest) + 224) + (chunk < longest ? 180 : 0);
-    if (cost < best_cost) {
-      best_cost = cost;
+    int64_t wgs = 0, ranges = 0;
+    for (const AttnSeq& s : v) {
+      const int64_t n = (int64_t)split_count(s, window, chunk) * kv_heads;
+      ranges += n;
+      wgs += row_tiles(s, G) * n;
+    }
+    const double key = size * std::max({0.0064, 0.0096 * std::min<int64_t>(wgs, kUnits) / kUnits,
+                                        0.022 * std::min<int64_t>(ranges, kUnits) / kUnits});
+    const double cost = ceil64(wgs, kUnits) * (5 + key * std::min(chunk, longest)) + (chunk < longest ? 4 : 0);
+    if (*cost_us < 0 || cost < *cost_us) {
+      *cost_us = cost;
       best = chunk;
     }
-    if (chunk >= longest) break;
+    if (chunk >= longest) return best;
   }
-  *cost_of = best_cost;
-  return best;
 }
 static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, int d, int window) {
   FwdPlan p;
   const int G = heads / kv_heads;
   // keys that a workgroup of 128 rows sees at most
   auto seen = [&](const AttnSeq& s) { return window ? std::min<int64_t>(s.nk, (int64_t)window + 128) : (int64_t)s.nk; };
-  int64_t wgs = 0, keys = 0, few_keys = 0, few_tiles = 0, cost;
+  int64_t wgs = 0, keys = 0, few_keys = 0, few_tiles = 0;
+  double cost;
   for (const AttnSeq& s : v) {
     if (s.nq > kFewRows) {
       p.many.push_back(s);
@@ -1077,8 +1088,8 @@ static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, 
     }
   }
   if (!p.many.empty() && wgs <= kUnits) {
-    split_chunk(p.many, G, kv_heads, window, &cost);
-    if (7 + 0.94 / 64 * (double)keys > 0.022 * (double)cost) p.many.clear();
+    split_chunk(p.many, G, kv_heads, d, window, &cost);
+    if (7 + 0.94 / 64 * (double)keys > cost) p.many.clear();
   }
   if (p.many.empty()) {
     p.few = v;
@@ -1087,7 +1098,7 @@ static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, 
     p.few.clear();
   }
   if (p.few.empty()) return p;
-  p.chunk = split_chunk(p.few, G, kv_heads, window, &cost);
+  p.chunk = split_chunk(p.few, G, kv_heads, d, window, &cost);
   for (size_t from = 0; from < p.few.size(); from += kAttnSeqs) {
     int64_t f = 0;
     for (size_t i = from; i < p.few.size() && i < from + kAttnSeqs; ++i) {
@@ -1158,7 +1169,6 @@ static int64_t dkv_part_floats(const std::vector<AttnSeq>& v, int splits, int kv
   }
   return most;
 }
-static int padded_d(int d) { return d <= 64 ? 64 : 128; }
 static int64_t round64(int64_t f) { return (f + 63) & ~int64_t(63); }
 
 size_t attn_fwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window) {

@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
 
 import torch
@@ -174,11 +175,17 @@ def _dptr(t, dtypes):
     return _ptr(t)
 
 
-def _mptr(t, dtypes, rows, cols):
-    """_dptr of a rows x cols matrix."""
-    if t.shape != (rows, cols):
-        raise ValueError("shape mismatch")
-    return _dptr(t, dtypes)
+def _mptrs(kind, tensors, dtypes, shapes):
+    """_dptr of every tensor, which must have the shape at its place, as an array of the ctypes type."""
+    out = kind()
+    for i, t in enumerate(tensors):
+        if t.shape != shapes[i]:
+            raise ValueError("shape mismatch")
+        if t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous():
+            _dtype(t, *dtypes)
+            _ptr(t)
+        out[i] = t.data_ptr()
+    return out
 
 
 @dataclass
@@ -516,13 +523,12 @@ def qlora_linear_bwd_act8(weights: list, act8: Act8, dys: list, As: list, Bs: li
     P = ctypes.c_void_p * n
     if any(w.K != K for w in weights) or any(u.numel() != M * r for u in us):
         raise ValueError("shape mismatch")
-    pdy = P(*[_mptr(t, _BF16, M, w.N) for t, w in zip(dys, weights)])
-    pa = P(*[_mptr(t, _BF16, r, K) for t in As])
-    pb = P(*[_mptr(t, _BF16, w.N, r) for t, w in zip(Bs, weights)])
+    rows_r, r_cols = [(w.N, r) for w in weights], [(r, K)] * n
+    pdy = _mptrs(P, dys, _BF16, [(M, w.N) for w in weights])
+    pa, pb = _mptrs(P, As, _BF16, r_cols), _mptrs(P, Bs, _BF16, rows_r)
     pu = P(*[_dptr(t, _F32) for t in us])
-    pdx = None if dxs is None else P(*[_mptr(t, _BF16, M, K) for t in dxs])
-    pda = P(*[_mptr(t, _F32, r, K) for t in dAs])
-    pdb = P(*[_mptr(t, _F32, w.N, r) for t, w in zip(dBs, weights)])
+    pdx = None if dxs is None else _mptrs(P, dxs, _BF16, [(M, K)] * n)
+    pda, pdb = _mptrs(P, dAs, _F32, r_cols), _mptrs(P, dBs, _F32, rows_r)
     if ws is None:
         ws = workspace_act8(M, [w.N for w in weights], K, r, act8.codes.device)
     cws = [w.c_struct() for w in weights]
@@ -615,25 +621,27 @@ class AttnSeqs:
 
 
 def _attn_tensors(*pairs):
-    """The qlora_attn_tensor structures of (tensor, shape it must have) pairs, as pointers into one array;
-    the tensors are [tokens, heads, d], tokens and heads may be strided, d is contiguous."""
-    v = []
+    """The qlora_attn_tensor structures of (tensor, shape it must have) pairs: the array that holds them, to be
+    kept until the library has read them, then the address of each. The tensors are [tokens, heads, d], tokens
+    and heads may be strided, d is contiguous."""
+    v = array("q")
     for t, shape in pairs:
-        _dtype(t, *_BF16)
+        if t.dtype not in _BF16:
+            _dtype(t, *_BF16)
         if not t.is_cuda:
             raise ValueError("tensor must live on the GPU")
-        token, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
-        if one != 1 or t.shape != shape:
+        if t.shape != shape or len(shape) != 3 or t.stride(2) != 1:
             raise ValueError("shape mismatch: attention tensors are [tokens, heads, d] with d contiguous")
+        token, head, _ = t.stride()
         tokens, heads, d = shape
         # the stride of a single head or token carries no meaning: give it a valid value
         if heads <= 1:
             head = d
         if tokens <= 1:
             token = max(d, head * (heads - 1) + d) if head * heads < 1 << 22 else d
-        v += (t.data_ptr(), token, head)
-    a = (ctypes.c_int64 * len(v))(*v)
-    return [ctypes.byref(a, 24 * i) for i in range(len(pairs))]
+        v.extend((t.data_ptr(), token, head))
+    at = v.buffer_info()[0]
+    return [v, *range(at, at + 24 * len(pairs), 24)]
 
 
 def _lse_ptr(lse, q):
@@ -655,7 +663,7 @@ def qlora_attn_fwd(seqs: AttnSeqs, q, k, v, o, lse=None, scale: float | None = N
     """Attention of seqs: q, o [query tokens, heads, d], k, v [key tokens, kv heads, d] (bf16, tokens and
     heads may be strided); lse [heads, query tokens] float32 is needed by the backward. scale defaults
     to d ** -0.5."""
-    tq, tk, tv, to = _attn_tensors((q, q.shape), (k, k.shape), (v, k.shape), (o, q.shape))
+    keep, tq, tk, tv, to = _attn_tensors((q, q.shape), (k, k.shape), (v, k.shape), (o, q.shape))
     cfg = seqs._config(q, k, scale)
     plse = _lse_ptr(lse, q)
     ws, pws, nbytes = _attn_ws(seqs, cfg, 0, ws, q.device)
@@ -670,7 +678,7 @@ def qlora_attn_bwd(seqs: AttnSeqs, q, k, v, o, lse, dout, dq, dk, dv, scale: flo
     if lse is None:
         raise ValueError("the backward needs lse")
     sq, sk = q.shape, k.shape
-    ts = _attn_tensors((q, sq), (k, sk), (v, sk), (o, sq), (dout, sq), (dq, sq), (dk, sk), (dv, sk))
+    keep, *ts = _attn_tensors((q, sq), (k, sk), (v, sk), (o, sq), (dout, sq), (dq, sq), (dk, sk), (dv, sk))
     cfg = seqs._config(q, k, scale)
     plse = _lse_ptr(lse, q)
     ws, pws, nbytes = _attn_ws(seqs, cfg, 1, ws, q.device)

@@ -316,7 +316,7 @@ struct Online {
 // 0.93 us, but 1.15 to 1.4 us alone, with one wave a SIMD that waits for its own reads and exponentials.
 // So a launch of at most one workgroup a compute unit takes GR = 2: two groups of 4 waves take the tiles of
 // the same rows in turn and are joined at the end (256 workgroups of up to 4096 keys: 94 us with one
-// group, 78 with two). With more workgroups the other kind of pair is better, as its two members start and
+// group, 77 with two). With more workgroups the other kind of pair is better, as its two members start and
 // end at different times: 2368 workgroups of packed sequences 109 us against 137.
 template <int DP, int GR>
 __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs a, const AttnSeqs sq) {
@@ -361,13 +361,11 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
   if (nt > 0) kv.load(Ks[grp][0], Vs[grp][0], j_g, wave);
   for (int t = 0; t < nt; ++t) {
     const int st = t & 1;
-    if (t + 1 < nt) {
-      kv.load(Ks[grp][st ^ 1], Vs[grp][st ^ 1], j_g + (t + 1) * GR * BN, wave);
-      wait_vmcnt<Stream::kLoads>();   // loads complete in order: tile t is in, tile t + 1 may be in flight
-    } else {
-      wait_vmcnt<0>();
-    }
+    wait_vmcnt<0>();
+    // the only barrier of a tile (a second one after its products cost 1 % of a full launch and 4 % of a
+    // launch with one workgroup a compute unit): tile t is in, and every wave is done with tile t - 1
     lds_barrier();
+    if (t + 1 < nt) kv.load(Ks[grp][st ^ 1], Vs[grp][st ^ 1], j_g + (t + 1) * GR * BN, wave);
     const int j0 = j_g + t * GR * BN;
     if (j0 < wb.hi && j0 + BN > wa.lo) {
       f32x16 sc[BN / 32];
@@ -390,7 +388,6 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
         for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(T::cols(Vs[grp][st], 16 * kk, dt, lane), p, acc.o[dt]);
       }
     }
-    lds_barrier();
   }
 
   float l = half_sum(acc.l);
@@ -400,8 +397,9 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) store_cols(dst, acc.o[dt], inv, dt, a.d, lane);
   } else {
-    // join the groups: each keeps half of the columns and gets the other group's sums of them (the tiles'
-    // place in LDS is free: every wave is past the loop's last barrier)
+    // join the groups: each keeps half of the columns and gets the other group's sums of them, through the
+    // tiles' place in LDS
+    lds_barrier();
     __shared__ float Ms[GR][128], Ls[GR][128];
     const int rl = wave * 32 + (lane & 31);
     if (lane < 32) {
@@ -732,13 +730,9 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, co
   if (nt > 0) kv.load(Ks[0], Vs[0], k_lo, wave);
   for (int t = 0; t < nt; ++t) {
     const int st = t & 1;
-    if (t + 1 < nt) {
-      kv.load(Ks[st ^ 1], Vs[st ^ 1], k_lo + (t + 1) * BN, wave);
-      wait_vmcnt<Stream::kLoads>();
-    } else {
-      wait_vmcnt<0>();
-    }
+    wait_vmcnt<0>();
     lds_barrier();
+    if (t + 1 < nt) kv.load(Ks[st ^ 1], Vs[st ^ 1], k_lo + (t + 1) * BN, wave);
 #pragma unroll
     for (int kt = 0; kt < BN / 32; ++kt) {
       const int j0 = k_lo + t * BN + 32 * kt;
@@ -760,7 +754,6 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, co
         }
       }
     }
-    lds_barrier();
   }
   uint16_t* dst = own ? a.dq.p + (s.q0 + row) * a.dq.token + (int64_t)head * a.dq.head : nullptr;
 #pragma unroll
@@ -872,13 +865,9 @@ __global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, 
   int ci = i_lo;   // first row of the tile in work
   for (int t = 0; t < total; ++t) {
     const int st = t & 1;
-    if (t + 1 < total) {
-      rows.load(Qs[st ^ 1], Gs[st ^ 1], Ls[st ^ 1][wave], Ds[st ^ 1][wave], wave, lane);
-      wait_vmcnt<Stream::kLoads>();
-    } else {
-      wait_vmcnt<0>();
-    }
+    wait_vmcnt<0>();
     lds_barrier();
+    if (t + 1 < total) rows.load(Qs[st ^ 1], Gs[st ^ 1], Ls[st ^ 1][wave], Ds[st ^ 1][wave], wave, lane);
 #pragma unroll
     for (int mt = 0; mt < BM / 32; ++mt) {
       const int i0 = ci + 32 * mt;
@@ -922,7 +911,6 @@ __global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, 
     }
     ci += BM;
     if (ci >= i_hi) ci = i_lo;
-    lds_barrier();
   }
   if (sp.splits == 1) {
     uint16_t* pk = own ? a.dk.p + (s.k0 + key) * a.dk.token + (int64_t)u.kvh * a.dk.head : nullptr;

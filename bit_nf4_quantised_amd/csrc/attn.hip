@@ -36,6 +36,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // of two: until then the probabilities of the row grow to at most 2^kSlack, which costs no accuracy
 // in fp32 sums and bf16 operands (both are relative), and the output is not rescaled.
 constexpr float kSlack = 8.f;
+// the same as raw scores (finite for every scale: the first score always passes -inf plus this)
+__device__ __forceinline__ float slack_of(float c) { return fminf(kSlack / c, 1e30f); }
 
 // ------------------------------------------------------------------------------------------
 // LDS tiles: rows of DP bf16 in 16-byte chunks; chunk c of row m sits at slot c ^ swz(m). 16
@@ -356,7 +358,7 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
 
   Online<DT> acc;
   acc.init();
-  const float slack = kSlack / a.c;
+  const float slack = slack_of(a.c);
   const int j_g = k_lo + grp * BN;   // the group's first tile; its tiles are GR apart
   if (nt > 0) kv.load(Ks[grp][0], Vs[grp][0], j_g, wave);
   for (int t = 0; t < nt; ++t) {
@@ -525,7 +527,7 @@ __global__ __launch_bounds__(256, DP == 128 ? 1 : 2) void attn_split_kernel(cons
   load_rows<DP>(w.qf, row < rows ? a.q.p + (s.q0 + tok) * a.q.token + (int64_t)head * a.q.head : nullptr, a.d, lane);
   w.acc.init();
   w.c = a.c;
-  w.slack = kSlack / a.c;
+  w.slack = slack_of(a.c);
   w.lane = lane;
   for (int j = j_w; j < k_hi; j += 8 * BN) {
     if (j + 4 * BN < k_hi) wait_vmcnt<Stream::kLoads>();   // ring1's loads may be in flight

@@ -219,3 +219,20 @@ def test_gradient_against_differences_of_the_forward():
         want = (host(grads[at]) * direction).sum()
         third = {"dq": 0.05, "dk": 0.05, "dv": 0.0}[name] * abs(want)
         assert abs(diff - want) <= noise + third + 2 * U * abs(want), (name, diff, want, noise)
+
+
+@pytest.mark.parametrize("d,window,causal", [(128, 0, True), (80, 0, True), (64, 0, True), (128, 40, True), (128, 0, False),
+                                             (64, 150, False)])
+def test_rows_shared_by_two_groups_of_waves(d, window, causal):
+    # a few hundred rows a sequence: too few workgroups to fill the GPU, too many rows for the key split
+    _run("two groups", _packed(300, 257, 311, 290), 8, 2, d, causal=causal, window=window)
+    _run("two groups, caches and short sequences", [(0, 500, 0, 700), (500, 130, 700, 131), (630, 1, 831, 90), (631, 7, 921, 7),
+                                                    (638, 33, 928, 20)], 16, 8, d, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("seqs", [[(0, 40, 0, 40)], [(0, 1, 0, 700)], [(0, 300, 0, 300), (300, 300, 300, 300), (600, 300, 600, 300)]])
+def test_vanishing_scale(seqs):
+    # every score rounds to zero: o is the mean of the values that a row sees. Forward only: dq and dk carry the
+    # factor 1e-39, below bf16's normal numbers (2^-126), where its rounding is not relative and the bounds above
+    # do not hold
+    _run("vanishing scale", seqs, 8, 2, 128, scale=1e-39, backward=False)

@@ -310,16 +310,49 @@ struct Online {
   }
 };
 
+// Two groups of 4 waves that hold sums of the same 32-row tiles exchange halves: group 0 keeps columns dt < H
+// and group 1 the rest, and each gives the other's away. buf: [taking group][wave][H][4][lane][4] floats.
+template <int H>
+constexpr size_t kHalves = 2 * 4 * H * 4 * 64 * 16;
+template <int H>
+__device__ __forceinline__ void give_half(void* buf, const f32x16 (&v)[2 * H], int grp, int wave, int lane) {
+  f32x4* p = reinterpret_cast<f32x4*>(buf) + ((grp ^ 1) * 4 + wave) * (H * 4 * 64) + lane;
+#pragma unroll
+  for (int dt = 0; dt < H; ++dt)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      f32x4 x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = grp ? v[dt][4 * g + k] : v[dt + H][4 * g + k];
+      p[(dt * 4 + g) * 64] = x;
+    }
+}
+template <int H>
+__device__ __forceinline__ f32x16 taken_half(const void* buf, int dt, int grp, int wave, int lane) {
+  const f32x4* p = reinterpret_cast<const f32x4*>(buf) + (grp * 4 + wave) * (H * 4 * 64) + lane;
+  f32x16 v;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const f32x4 x = p[(dt * 4 + g) * 64];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[4 * g + k] = x[k];
+  }
+  return v;
+}
+
 // ------------------------------------------------------------------------------------------
 // Forward. 4 waves take 128 query rows of one head, 32 per wave; keys and values stream through LDS in
 // tiles of 64, two tiles deep, by LDS-DMA. Bound by the matrix unit and, in launches that fill the GPU,
 // by its power: 8192 tokens, 32 heads over 8, d 128, not causal, 1051 us = 1046 TFLOP/s, where a plain
 // product of 16384^3 reaches 1355. A tile costs a workgroup that shares its compute unit with another
 // 0.93 us, but 1.15 to 1.4 us alone, with one wave a SIMD that waits for its own reads and exponentials.
-// So a launch of at most one workgroup a compute unit takes GR = 2: two groups of 4 waves take the tiles of
-// the same rows in turn and are joined at the end (256 workgroups of up to 4096 keys: 94 us with one
-// group, 77 with two). With more workgroups the other kind of pair is better, as its two members start and
-// end at different times: 2368 workgroups of packed sequences 109 us against 137.
+// So where the longest workgroups decide, a workgroup has GR = 2 groups of 4 waves, which take the tiles of
+// the same rows in turn and are joined at the end; two_groups() says where. Measured, one group and two, us:
+// 256 workgroups of up to 4096 keys 94 and 77; one causal sequence, 32 heads over 8, of 1536 tokens 36 and
+// 30, of 2048 57 and 56; 3000 tokens, 16 heads over 4, 70 and 53. Where the work spreads evenly the
+// other form is better, as two workgroups on a unit start and end at different times: four causal sequences
+// of 512, 32 heads over 8, 22 and 25, 2048 tokens without a mask 75 and 79, 2368 workgroups of packed
+// sequences 109 and 137.
 template <int DP, int GR>
 __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs a, const AttnSeqs sq) {
   constexpr int BN = 64, KS = DP / 16, DT = DP / 32;
@@ -409,17 +442,8 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
       Ls[grp][rl] = l;
     }
     constexpr int H = DT / 2;
-    f32x4* const half = reinterpret_cast<f32x4*>(&Ks[0][0][0]) + wave * (H * 4 * 64) + lane;
-    static_assert(2 * 4 * H * 4 * 64 * 16 <= sizeof(Ks), "both halves fit");
-#pragma unroll
-    for (int dt = 0; dt < H; ++dt)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        f32x4 x;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = grp ? acc.o[dt][4 * g + k] : acc.o[dt + H][4 * g + k];
-        half[(grp ^ 1) * (4 * H * 4 * 64) + (dt * 4 + g) * 64] = x;
-      }
+    give_half<H>(&Ks[0][0][0], acc.o, grp, wave, lane);
+    static_assert(kHalves<H> <= sizeof(Ks), "both halves fit");
     lds_barrier();
     const float mo = Ms[grp ^ 1][rl], lo = Ls[grp ^ 1][rl], m = fmaxf(acc.m, mo);
     const float mc = m == -INFINITY ? 0.f : m * a.c;
@@ -430,13 +454,9 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
     const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int dt = 0; dt < H; ++dt) {
-      f32x16 v;
+      f32x16 v = taken_half<H>(&Ks[0][0][0], dt, grp, wave, lane);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 x = half[grp * (4 * H * 4 * 64) + (dt * 4 + g) * 64];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[4 * g + k] = (grp ? acc.o[dt + H][4 * g + k] : acc.o[dt][4 * g + k]) * fm + x[k] * fo;
-      }
+      for (int k = 0; k < 16; ++k) v[k] = (grp ? acc.o[dt + H][k] : acc.o[dt][k]) * fm + v[k] * fo;
       store_cols(dst, v, inv, grp * H + dt, a.d, lane);
     }
   }
@@ -670,17 +690,20 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnFwdArgs a, con
 // dS of a row, which with the rounding of dS itself puts dq and dk at 2.5e-3 of their norm from the exact
 // ones (their own rounding to bf16 alone is 1.7e-3), and at 4e-3 where rows see few keys. -delta enters the
 // products as their starting value, which saves a subtraction per score.
+// GR as in the forward: one causal sequence, 32 heads over 8, of 2048 tokens 193 and 187 us for the whole
+// backward, 3000 tokens, 16 heads over 4, 221 and 200; four causal sequences of 512 84 and 91.
 // One pass over the pairs could give dq, dk and dv together with five products instead of seven, but its
 // sums of dq over key tiles would need atomics, in no fixed order, or a partial dq per key tile.
-template <int DP>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, const AttnSeqs sq) {
+template <int DP, int GR>
+__global__ __launch_bounds__(256 * GR, 2) void attn_dq_kernel(const AttnBwdArgs a, const AttnSeqs sq) {
   constexpr int BN = 64, KS = DP / 16, DT = DP / 32;
   typedef Tile<DP> T;
   typedef KvStream<DP, BN, 4> Stream;
-  __shared__ __attribute__((aligned(16))) uint16_t Ks[2][BN * DP];
-  __shared__ __attribute__((aligned(16))) uint16_t Vs[2][BN * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t Ks[GR][2][BN * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t Vs[GR][2][BN * DP];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
+  const int grp = GR == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 8);
   const int G = a.heads / a.kv_heads;
   const Unit u = unit_of((int)blockIdx.x, a.kv_heads, G);
   const Found at_seq = find_seq(sq, u.tile);
@@ -707,7 +730,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, co
   const int64_t at = (int64_t)head * a.lse_stride + s.q0 + row;
   if (own) {
     lse2 = a.lse[at] * kLog2e;
-    if (lane < 32) {   // as the second launch takes them
+    if (grp == 0 && lane < 32) {   // as the second launch takes them
       a.lse2[at] = lse2;
       a.less_delta[at] = -delta;
     }
@@ -722,28 +745,29 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, co
   const int w0 = r0 + wave * 32, w1 = min(s.nq - 1, w0 + 31);
   const Range wa = visible(w0 + shift, s.nk, a.causal, a.window), wb = visible(w1 + shift, s.nk, a.causal, a.window);
   const Range mine = visible(row + shift, s.nk, a.causal, a.window);
-  const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
+  const int nt = k_hi > k_lo ? (k_hi - k_lo + GR * BN - 1) / (GR * BN) : 0;   // of each group
 
   Stream kv;
   kv.init(a.k, a.v, s, u.kvh, a.d, wave, lane);
   f32x16 dq[DT];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) dq[dt] = zero16();
-  if (nt > 0) kv.load(Ks[0], Vs[0], k_lo, wave);
+  const int j_g = k_lo + grp * BN;   // the group's first tile; its tiles are GR apart
+  if (nt > 0) kv.load(Ks[grp][0], Vs[grp][0], j_g, wave);
   for (int t = 0; t < nt; ++t) {
     const int st = t & 1;
     wait_vmcnt<0>();
     lds_barrier();
-    if (t + 1 < nt) kv.load(Ks[st ^ 1], Vs[st ^ 1], k_lo + (t + 1) * BN, wave);
+    if (t + 1 < nt) kv.load(Ks[grp][st ^ 1], Vs[grp][st ^ 1], j_g + (t + 1) * GR * BN, wave);
 #pragma unroll
     for (int kt = 0; kt < BN / 32; ++kt) {
-      const int j0 = k_lo + t * BN + 32 * kt;
+      const int j0 = j_g + t * GR * BN + 32 * kt;
       if (j0 < wb.hi && j0 + 32 > wa.lo) {
         f32x16 sc = zero16(), dp = less_delta;   // do.v - delta comes out of the products
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Ks[st], 32 * kt, ks, lane), qf[ks], sc);
+        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Ks[grp][st], 32 * kt, ks, lane), qf[ks], sc);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) dp = mfma(T::rows(Vs[st], 32 * kt, ks, lane), gf[ks], dp);
+        for (int ks = 0; ks < KS; ++ks) dp = mfma(T::rows(Vs[grp][st], 32 * kt, ks, lane), gf[ks], dp);
 #pragma unroll
         for (int i = 0; i < 16; ++i) dp[i] *= __builtin_amdgcn_exp2f(__fmaf_rn(sc[i], a.c, -lse2));
         // selected away, not multiplied: a row without keys has lse -inf
@@ -752,14 +776,30 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdArgs a, co
         for (int kk = 0; kk < 2; ++kk) {
           const bf16x8 ds = pack8(dp, kk);
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) dq[dt] = mfma(T::cols(Ks[st], 32 * kt + 16 * kk, dt, lane), ds, dq[dt]);
+          for (int dt = 0; dt < DT; ++dt) dq[dt] = mfma(T::cols(Ks[grp][st], 32 * kt + 16 * kk, dt, lane), ds, dq[dt]);
         }
       }
     }
   }
   uint16_t* dst = own ? a.dq.p + (s.q0 + row) * a.dq.token + (int64_t)head * a.dq.head : nullptr;
+  if constexpr (GR == 1) {
 #pragma unroll
-  for (int dt = 0; dt < DT; ++dt) store_cols(dst, dq[dt], a.scale, dt, a.d, lane);
+    for (int dt = 0; dt < DT; ++dt) store_cols(dst, dq[dt], a.scale, dt, a.d, lane);
+  } else {
+    // each group keeps half of the columns and adds the other group's sums of them
+    constexpr int H = DT / 2;
+    lds_barrier();
+    give_half<H>(&Ks[0][0][0], dq, grp, wave, lane);
+    static_assert(kHalves<H> <= sizeof(Ks), "both halves fit");
+    lds_barrier();
+#pragma unroll
+    for (int dt = 0; dt < H; ++dt) {
+      f32x16 v = taken_half<H>(&Ks[0][0][0], dt, grp, wave, lane);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] += grp ? dq[dt + H][k] : dq[dt][k];
+      store_cols(dst, v, a.scale, grp * H + dt, a.d, lane);
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -1100,6 +1140,25 @@ static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, 
   return p;
 }
 
+// Whether a launch over tiles of 128 query rows takes the form with two groups of waves (see
+// attn_fwd_kernel): when its work, spread over the compute units, is at most 1.2 times that of its longest
+// workgroup, in tiles of 64 keys (1.13 gains 15 % in the forward, 1.25 loses 14 %).
+static bool two_groups(const AttnSeqs& q, int heads, int causal, int window) {
+  int64_t longest = 0, total = 0;
+  for (int i = 0; i < q.count; ++i) {
+    const AttnSeq& s = q.seq[i];
+    for (int64_t r = 0; r < s.nq; r += 128) {
+      const int64_t p0 = (int64_t)s.nk - s.nq + r, p1 = (int64_t)s.nk - s.nq + std::min<int64_t>(s.nq, r + 128);
+      const int64_t hi = causal ? std::max<int64_t>(0, p1) : s.nk;
+      const int64_t lo = window ? std::max<int64_t>(0, p0 - window + 1) : 0;
+      const int64_t n = hi > lo ? ceil64(hi - lo, 64) : 0;
+      longest = std::max(longest, n);
+      total += n;
+    }
+  }
+  return (double)total * heads <= 1.2 * kUnits * (double)longest;
+}
+
 // 64-row tiles of queries that see some key of key tile t (as attn_dkv_kernel counts them)
 static int64_t dkv_row_tiles(const AttnSeq& s, int t, int causal, int window) {
   const int64_t shift = (int64_t)s.nk - s.nq, j0 = 128 * (int64_t)t, jl = std::min<int64_t>(s.nk, j0 + 128) - 1;
@@ -1180,7 +1239,7 @@ hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t co
   for (size_t from = 0; from < plan.many.size(); from += kAttnSeqs) {
     const AttnSeqs q = pack_seqs(plan.many, from, q_tiles);
     const dim3 grid((unsigned)(q.first[q.count] * a.heads));
-    if (grid.x <= kUnits) {   // see attn_fwd_kernel
+    if (two_groups(q, a.heads, a.causal, a.window)) {
       if (a.d <= 64) hipLaunchKernelGGL((attn_fwd_kernel<64, 2>), grid, dim3(512), 0, stream, a, q);
       else hipLaunchKernelGGL((attn_fwd_kernel<128, 2>), grid, dim3(512), 0, stream, a, q);
     } else {
@@ -1222,8 +1281,13 @@ hipError_t launch_attn_bwd(const AttnBwdArgs& args, const AttnSeq* seqs, int64_t
   for (size_t from = 0; from < vq.size(); from += kAttnSeqs) {
     const AttnSeqs q = pack_seqs(vq, from, q_tiles);
     const dim3 grid((unsigned)(q.first[q.count] * a.heads));
-    if (a.d <= 64) hipLaunchKernelGGL(attn_dq_kernel<64>, grid, dim3(256), 0, stream, a, q);
-    else hipLaunchKernelGGL(attn_dq_kernel<128>, grid, dim3(256), 0, stream, a, q);
+    if (two_groups(q, a.heads, a.causal, a.window)) {
+      if (a.d <= 64) hipLaunchKernelGGL((attn_dq_kernel<64, 2>), grid, dim3(512), 0, stream, a, q);
+      else hipLaunchKernelGGL((attn_dq_kernel<128, 2>), grid, dim3(512), 0, stream, a, q);
+    } else {
+      if (a.d <= 64) hipLaunchKernelGGL((attn_dq_kernel<64, 1>), grid, dim3(256), 0, stream, a, q);
+      else hipLaunchKernelGGL((attn_dq_kernel<128, 1>), grid, dim3(256), 0, stream, a, q);
+    }
   }
   const KvPlan plan = kv_plan(vk, a.heads, a.kv_heads, a.d, a.causal, a.window);
   const AttnKvSplit sp{ws + 2 * round64(q_tokens * a.heads), plan.splits, plan.gper};

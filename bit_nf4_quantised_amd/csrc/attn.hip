@@ -311,12 +311,12 @@ struct Online {
 };
 
 // Two groups of 4 waves that hold sums of the same 32-row tiles exchange halves: group 0 keeps columns dt < H
-// and group 1 the rest, and each gives the other's away. buf: [taking group][wave][H][4][lane][4] floats.
+// and group 1 the rest, and each gives the other's away, into a buffer of [wave][H][4][lane][4] floats.
 template <int H>
-constexpr size_t kHalves = 2 * 4 * H * 4 * 64 * 16;
+constexpr size_t kHalf = 4 * H * 4 * 64 * 16;
 template <int H>
-__device__ __forceinline__ void give_half(void* buf, const f32x16 (&v)[2 * H], int grp, int wave, int lane) {
-  f32x4* p = reinterpret_cast<f32x4*>(buf) + ((grp ^ 1) * 4 + wave) * (H * 4 * 64) + lane;
+__device__ __forceinline__ void give_half(void* to0, void* to1, const f32x16 (&v)[2 * H], int grp, int wave, int lane) {
+  f32x4* p = reinterpret_cast<f32x4*>(grp ? to0 : to1) + wave * (H * 4 * 64) + lane;
 #pragma unroll
   for (int dt = 0; dt < H; ++dt)
 #pragma unroll
@@ -328,8 +328,8 @@ __device__ __forceinline__ void give_half(void* buf, const f32x16 (&v)[2 * H], i
     }
 }
 template <int H>
-__device__ __forceinline__ f32x16 taken_half(const void* buf, int dt, int grp, int wave, int lane) {
-  const f32x4* p = reinterpret_cast<const f32x4*>(buf) + (grp * 4 + wave) * (H * 4 * 64) + lane;
+__device__ __forceinline__ f32x16 taken_half(const void* to0, const void* to1, int dt, int grp, int wave, int lane) {
+  const f32x4* p = reinterpret_cast<const f32x4*>(grp ? to1 : to0) + wave * (H * 4 * 64) + lane;
   f32x16 v;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
@@ -358,8 +358,10 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
   constexpr int BN = 64, KS = DP / 16, DT = DP / 32;
   typedef Tile<DP> T;
   typedef KvStream<DP, BN, 4> Stream;
-  __shared__ __attribute__((aligned(16))) uint16_t Ks[GR][2][BN * DP];
-  __shared__ __attribute__((aligned(16))) uint16_t Vs[GR][2][BN * DP];
+  // a variable per stage and code of its own for each (tile() twice in the loop): from one array, or through
+  // a stage index, the compiler lets a tile's reads wait for the next tile's loads, which are on their way
+  // (prefill chunk 68 -> 65 us)
+  __shared__ __attribute__((aligned(16))) uint16_t Ks0[GR][BN * DP], Ks1[GR][BN * DP], Vs0[GR][BN * DP], Vs1[GR][BN * DP];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
   const int grp = GR == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 8);
@@ -393,14 +395,13 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
   acc.init();
   const float slack = slack_of(a.c);
   const int j_g = k_lo + grp * BN;   // the group's first tile; its tiles are GR apart
-  if (nt > 0) kv.load(Ks[grp][0], Vs[grp][0], j_g, wave);
-  for (int t = 0; t < nt; ++t) {
-    const int st = t & 1;
+  if (nt > 0) kv.load(Ks0[grp], Vs0[grp], j_g, wave);
+  auto tile = [&](int t, const uint16_t* Kt, const uint16_t* Vt, uint16_t* kn, uint16_t* vn) __attribute__((always_inline)) {
     wait_vmcnt<0>();
     // the only barrier of a tile (a second one after its products cost 1 % of a full launch and 4 % of a
     // launch with one workgroup a compute unit): tile t is in, and every wave is done with tile t - 1
     lds_barrier();
-    if (t + 1 < nt) kv.load(Ks[grp][st ^ 1], Vs[grp][st ^ 1], j_g + (t + 1) * GR * BN, wave);
+    if (t + 1 < nt) kv.load(kn, vn, j_g + (t + 1) * GR * BN, wave);
     const int j0 = j_g + t * GR * BN;
     if (j0 < wb.hi && j0 + BN > wa.lo) {
       f32x16 sc[BN / 32];
@@ -408,7 +409,7 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
       for (int kt = 0; kt < BN / 32; ++kt) {
         sc[kt] = zero16();
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) sc[kt] = mfma(T::rows(Ks[grp][st], 32 * kt, ks, lane), qf[ks], sc[kt]);
+        for (int ks = 0; ks < KS; ++ks) sc[kt] = mfma(T::rows(Kt, 32 * kt, ks, lane), qf[ks], sc[kt]);
       }
       // some row of the wave does not see some key of the tile
       if (j0 + BN > wa.hi || j0 < wb.lo) {
@@ -420,9 +421,13 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
       for (int kk = 0; kk < BN / 16; ++kk) {
         const bf16x8 p = pack8(sc[kk / 2], kk & 1);
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(T::cols(Vs[grp][st], 16 * kk, dt, lane), p, acc.o[dt]);
+        for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(T::cols(Vt, 16 * kk, dt, lane), p, acc.o[dt]);
       }
     }
+  };
+  for (int t = 0; t < nt; t += 2) {
+    tile(t, Ks0[grp], Vs0[grp], Ks1[grp], Vs1[grp]);
+    if (t + 1 < nt) tile(t + 1, Ks1[grp], Vs1[grp], Ks0[grp], Vs0[grp]);
   }
 
   float l = half_sum(acc.l);
@@ -442,8 +447,8 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
       Ls[grp][rl] = l;
     }
     constexpr int H = DT / 2;
-    give_half<H>(&Ks[0][0][0], acc.o, grp, wave, lane);
-    static_assert(kHalves<H> <= sizeof(Ks), "both halves fit");
+    give_half<H>(Ks0, Ks1, acc.o, grp, wave, lane);
+    static_assert(kHalf<H> <= sizeof(Ks0), "a half fits");
     lds_barrier();
     const float mo = Ms[grp ^ 1][rl], lo = Ls[grp ^ 1][rl], m = fmaxf(acc.m, mo);
     const float mc = m == -INFINITY ? 0.f : m * a.c;
@@ -454,7 +459,7 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
     const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int dt = 0; dt < H; ++dt) {
-      f32x16 v = taken_half<H>(&Ks[0][0][0], dt, grp, wave, lane);
+      f32x16 v = taken_half<H>(Ks0, Ks1, dt, grp, wave, lane);
 #pragma unroll
       for (int k = 0; k < 16; ++k) v[k] = (grp ? acc.o[dt + H][k] : acc.o[dt][k]) * fm + v[k] * fo;
       store_cols(dst, v, inv, grp * H + dt, a.d, lane);
@@ -699,8 +704,7 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_dq_kernel(const AttnBwdArgs 
   constexpr int BN = 64, KS = DP / 16, DT = DP / 32;
   typedef Tile<DP> T;
   typedef KvStream<DP, BN, 4> Stream;
-  __shared__ __attribute__((aligned(16))) uint16_t Ks[GR][2][BN * DP];
-  __shared__ __attribute__((aligned(16))) uint16_t Vs[GR][2][BN * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t Ks0[GR][BN * DP], Ks1[GR][BN * DP], Vs0[GR][BN * DP], Vs1[GR][BN * DP];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
   const int grp = GR == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 8);
@@ -753,21 +757,20 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_dq_kernel(const AttnBwdArgs 
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) dq[dt] = zero16();
   const int j_g = k_lo + grp * BN;   // the group's first tile; its tiles are GR apart
-  if (nt > 0) kv.load(Ks[grp][0], Vs[grp][0], j_g, wave);
-  for (int t = 0; t < nt; ++t) {
-    const int st = t & 1;
+  if (nt > 0) kv.load(Ks0[grp], Vs0[grp], j_g, wave);
+  auto tile = [&](int t, const uint16_t* Kt, const uint16_t* Vt, uint16_t* kn, uint16_t* vn) __attribute__((always_inline)) {
     wait_vmcnt<0>();
     lds_barrier();
-    if (t + 1 < nt) kv.load(Ks[grp][st ^ 1], Vs[grp][st ^ 1], j_g + (t + 1) * GR * BN, wave);
+    if (t + 1 < nt) kv.load(kn, vn, j_g + (t + 1) * GR * BN, wave);
 #pragma unroll
     for (int kt = 0; kt < BN / 32; ++kt) {
       const int j0 = j_g + t * GR * BN + 32 * kt;
       if (j0 < wb.hi && j0 + 32 > wa.lo) {
         f32x16 sc = zero16(), dp = less_delta;   // do.v - delta comes out of the products
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Ks[grp][st], 32 * kt, ks, lane), qf[ks], sc);
+        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Kt, 32 * kt, ks, lane), qf[ks], sc);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) dp = mfma(T::rows(Vs[grp][st], 32 * kt, ks, lane), gf[ks], dp);
+        for (int ks = 0; ks < KS; ++ks) dp = mfma(T::rows(Vt, 32 * kt, ks, lane), gf[ks], dp);
 #pragma unroll
         for (int i = 0; i < 16; ++i) dp[i] *= __builtin_amdgcn_exp2f(__fmaf_rn(sc[i], a.c, -lse2));
         // selected away, not multiplied: a row without keys has lse -inf
@@ -776,10 +779,14 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_dq_kernel(const AttnBwdArgs 
         for (int kk = 0; kk < 2; ++kk) {
           const bf16x8 ds = pack8(dp, kk);
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) dq[dt] = mfma(T::cols(Ks[grp][st], 32 * kt + 16 * kk, dt, lane), ds, dq[dt]);
+          for (int dt = 0; dt < DT; ++dt) dq[dt] = mfma(T::cols(Kt, 32 * kt + 16 * kk, dt, lane), ds, dq[dt]);
         }
       }
     }
+  };
+  for (int t = 0; t < nt; t += 2) {
+    tile(t, Ks0[grp], Vs0[grp], Ks1[grp], Vs1[grp]);
+    if (t + 1 < nt) tile(t + 1, Ks1[grp], Vs1[grp], Ks0[grp], Vs0[grp]);
   }
   uint16_t* dst = own ? a.dq.p + (s.q0 + row) * a.dq.token + (int64_t)head * a.dq.head : nullptr;
   if constexpr (GR == 1) {
@@ -789,12 +796,12 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_dq_kernel(const AttnBwdArgs 
     // each group keeps half of the columns and adds the other group's sums of them
     constexpr int H = DT / 2;
     lds_barrier();
-    give_half<H>(&Ks[0][0][0], dq, grp, wave, lane);
-    static_assert(kHalves<H> <= sizeof(Ks), "both halves fit");
+    give_half<H>(Ks0, Ks1, dq, grp, wave, lane);
+    static_assert(kHalf<H> <= sizeof(Ks0), "a half fits");
     lds_barrier();
 #pragma unroll
     for (int dt = 0; dt < H; ++dt) {
-      f32x16 v = taken_half<H>(&Ks[0][0][0], dt, grp, wave, lane);
+      f32x16 v = taken_half<H>(Ks0, Ks1, dt, grp, wave, lane);
 #pragma unroll
       for (int k = 0; k < 16; ++k) v[k] += grp ? dq[dt + H][k] : dq[dt][k];
       store_cols(dst, v, a.scale, grp * H + dt, a.d, lane);
@@ -856,9 +863,10 @@ __global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, 
   constexpr int BM = WV == 1 ? 64 : 32, KS = DP / 16, DT = DP / 32;
   typedef Tile<DP> T;
   typedef RowStream<DP, BM, 4> Stream;
-  __shared__ __attribute__((aligned(16))) uint16_t Qs[2][BM * DP];
-  __shared__ __attribute__((aligned(16))) uint16_t Gs[2][BM * DP];
-  __shared__ __attribute__((aligned(16))) float Ls[2][4][64], Ds[2][4][64];   // lse log2(e) and -delta, a copy per wave
+  // a variable per stage, as in the forward (dq and this kernel together: packed 70B batch 390 -> 362 us)
+  __shared__ __attribute__((aligned(16))) uint16_t Qs0[BM * DP], Qs1[BM * DP], Gs0[BM * DP], Gs1[BM * DP];
+  // lse log2(e) and -delta, a copy per wave
+  __shared__ __attribute__((aligned(16))) float Ls0[4][64], Ls1[4][64], Ds0[4][64], Ds1[4][64];
   __shared__ __attribute__((aligned(16))) uint16_t Vs[WV == 1 ? 8 : 128 * DP];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -903,13 +911,13 @@ __global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, 
     dk[dt] = zero16();
     dv[dt] = zero16();
   }
-  if (total > 0) rows.load(Qs[0], Gs[0], Ls[0][wave], Ds[0][wave], wave, lane);
+  if (total > 0) rows.load(Qs0, Gs0, Ls0[wave], Ds0[wave], wave, lane);
   int ci = i_lo;   // first row of the tile in work
-  for (int t = 0; t < total; ++t) {
-    const int st = t & 1;
+  auto tile = [&](int t, const uint16_t* Qt, const uint16_t* Gt, const float* Lt, const float* Dt, uint16_t* qn, uint16_t* gn, float* ln,
+                  float* dn) __attribute__((always_inline)) {
     wait_vmcnt<0>();
     lds_barrier();
-    if (t + 1 < total) rows.load(Qs[st ^ 1], Gs[st ^ 1], Ls[st ^ 1][wave], Ds[st ^ 1][wave], wave, lane);
+    if (t + 1 < total) rows.load(qn, gn, ln, dn, wave, lane);
 #pragma unroll
     for (int mt = 0; mt < BM / 32; ++mt) {
       const int i0 = ci + 32 * mt;
@@ -917,18 +925,18 @@ __global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, 
         f32x16 sc = zero16(), dp;   // do.v - delta comes out of the products
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 x = *reinterpret_cast<const f32x4*>(&Ds[st][wave][32 * mt + 8 * g + 4 * (lane >> 5)]);
+          const f32x4 x = *reinterpret_cast<const f32x4*>(&Dt[32 * mt + 8 * g + 4 * (lane >> 5)]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) dp[4 * g + e] = x[e];
         }
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Qs[st], 32 * mt, ks, lane), kf[ks], sc);
+        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Qt, 32 * mt, ks, lane), kf[ks], sc);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-          dp = mfma(T::rows(Gs[st], 32 * mt, ks, lane), WV == 1 ? vf[WV == 1 ? ks : 0] : T::rows(vt, 0, ks, lane), dp);
+          dp = mfma(T::rows(Gt, 32 * mt, ks, lane), WV == 1 ? vf[WV == 1 ? ks : 0] : T::rows(vt, 0, ks, lane), dp);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 x = *reinterpret_cast<const f32x4*>(&Ls[st][wave][32 * mt + 8 * g + 4 * (lane >> 5)]);
+          const f32x4 x = *reinterpret_cast<const f32x4*>(&Lt[32 * mt + 8 * g + 4 * (lane >> 5)]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = 4 * g + e;
@@ -945,14 +953,26 @@ __global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, 
         for (int kk = 0; kk < 2; ++kk) {
           const bf16x8 p = pack8(sc, kk), ds = pack8(dp, kk);
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) dv[dt] = mfma(T::cols(Gs[st], 32 * mt + 16 * kk, dt, lane), p, dv[dt]);
+          for (int dt = 0; dt < DT; ++dt) dv[dt] = mfma(T::cols(Gt, 32 * mt + 16 * kk, dt, lane), p, dv[dt]);
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) dk[dt] = mfma(T::cols(Qs[st], 32 * mt + 16 * kk, dt, lane), ds, dk[dt]);
+          for (int dt = 0; dt < DT; ++dt) dk[dt] = mfma(T::cols(Qt, 32 * mt + 16 * kk, dt, lane), ds, dk[dt]);
         }
       }
     }
     ci += BM;
     if (ci >= i_hi) ci = i_lo;
+  };
+  if constexpr (WV == 1) {
+    for (int t = 0; t < total; t += 2) {
+      tile(t, Qs0, Gs0, Ls0[wave], Ds0[wave], Qs1, Gs1, Ls1[wave], Ds1[wave]);
+      if (t + 1 < total) tile(t + 1, Qs1, Gs1, Ls1[wave], Ds1[wave], Qs0, Gs0, Ls0[wave], Ds0[wave]);
+    }
+  } else {   // code for each stage does not leave registers enough for two waves
+    for (int t = 0; t < total; ++t) {
+      const bool o = t & 1;
+      tile(t, o ? Qs1 : Qs0, o ? Gs1 : Gs0, o ? Ls1[wave] : Ls0[wave], o ? Ds1[wave] : Ds0[wave], o ? Qs0 : Qs1, o ? Gs0 : Gs1,
+           o ? Ls0[wave] : Ls1[wave], o ? Ds0[wave] : Ds1[wave]);
+    }
   }
   if (sp.splits == 1) {
     uint16_t* pk = own ? a.dk.p + (s.k0 + key) * a.dk.token + (int64_t)u.kvh * a.dk.head : nullptr;

@@ -134,6 +134,9 @@ __device__ __forceinline__ void load_rows(bf16x8 (&f)[DP / 16], const uint16_t* 
   }
 }
 
+// the instructions before stay before, those after stay after
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
 __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -814,12 +817,12 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_dq_kernel(const AttnBwdArgs 
 // wave; the rows of q and do of its query heads stream through LDS, two tiles deep. The query heads of
 // the group can be split over several workgroups (gper heads each): their fp32 results go to the
 // workspace, and attn_dkv_sum_kernel adds them in order.
-// WV = 1: the keys' and the values' operands stay in registers (350 of them, one wave a SIMD) and tiles
-// have 64 rows. WV = 2: the values' operands are read from LDS and tiles have 32 rows, which leaves room
-// for two waves a SIMD. A workgroup of the first kind alone on a compute unit takes 2.4 us for 64 rows of
-// 128 keys at d = 128, of the second 3.1 us; but two of the second take 4.7 us for both, so the second is
-// better where the launch has workgroups enough (kv_plan chooses): 8192 tokens, 32 heads over 8, not
-// causal: 2.6 ms with the first (830 TFLOP/s of the four products), 2.0 ms with the second (1100).
+// WV = 1: the keys' and the values' operands stay in registers (of 512, one wave a SIMD) and tiles have 64
+// rows, two blocks that overlap. WV = 2: the values' operands are read from LDS and tiles have 32 rows, which
+// leaves room for two waves a SIMD. A workgroup of the first kind alone on a compute unit takes 1.9 us for 64
+// rows of 128 keys at d = 128, of the second 2.25 us, and two of the second 3.9 us for both (kv_plan chooses):
+// 32 heads over 8, one causal sequence of 2048 tokens 92 us and 96, four of 512 43 and 35, 8192 tokens, not
+// causal, 2.21 ms and 2.02 (1090 TFLOP/s of the four products).
 template <int DP, int ROWS, int NW>
 struct RowStream {   // rows [lo, hi) of q, do, lse2 and less_delta, head after head, in tiles of ROWS <= 64
   typedef TileDma<DP, ROWS, NW> Dma;
@@ -918,25 +921,122 @@ __global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, 
     wait_vmcnt<0>();
     lds_barrier();
     if (t + 1 < total) rows.load(qn, gn, ln, dn, wave, lane);
+    if constexpr (WV == 1) {
+      if (ci + BM - 1 >= any_lo && ci < any_hi) {
+        // The wave is alone on its SIMD, so its two blocks of 32 rows overlap by program order: the second's
+        // scores are formed between the first's exponentials, the first's sums between the second's. Each
+        // operand register takes its next contents from LDS as soon as its product is issued.
+        const bool masked = ci < all_lo || ci + BM - 1 >= all_hi;
+        bf16x8 fa[KS], fb[KS];   // operands on their way
+        f32x16 sc[2], dp[2], ls;
+        bf16x8 p[2], ds[2];
+        auto start = [&](int mt) __attribute__((always_inline)) {
+          sc[mt] = zero16();
 #pragma unroll
-    for (int mt = 0; mt < BM / 32; ++mt) {
-      const int i0 = ci + 32 * mt;
+          for (int g = 0; g < 4; ++g) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&Dt[32 * mt + 8 * g + 4 * (lane >> 5)]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dp[mt][4 * g + e] = x[e];
+          }
+        };
+        auto take_lse = [&](int mt) __attribute__((always_inline)) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&Lt[32 * mt + 8 * g + 4 * (lane >> 5)]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ls[4 * g + e] = x[e];
+          }
+        };
+        auto finish = [&](int mt) __attribute__((always_inline)) {
+          if (masked) {
+            hide(sc[mt], seen, ci + 32 * mt, lane, 0.f);
+            hide(dp[mt], seen, ci + 32 * mt, lane, 0.f);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {
+            p[kk] = pack8(sc[mt], kk);
+            ds[kk] = pack8(dp[mt], kk);
+          }
+        };
+#pragma unroll
+        for (int k = 0; k < KS; ++k) fa[k] = T::rows(Qt, 0, k, lane);
+        start(0);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) fb[k] = T::rows(Gt, 0, k, lane);
+        keep_order();
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          sc[0] = mfma(fa[k], kf[k], sc[0]);
+          fa[k] = T::rows(Qt, 32, k, lane);
+          keep_order();
+        }
+        take_lse(0);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          dp[0] = mfma(fb[k], vf[k], dp[0]);
+          fb[k] = T::rows(Gt, 32, k, lane);
+          keep_order();
+        }
+        start(1);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          sc[1] = mfma(fa[k], kf[k], sc[1]);
+#pragma unroll
+          for (int e = 16 / KS * k; e < 16 / KS * (k + 1); ++e) sc[0][e] = __builtin_amdgcn_exp2f(__fmaf_rn(sc[0][e], a.c, -ls[e]));
+          fa[k] = T::cols(Gt, 16 * (k / DT), k % DT, lane);
+          keep_order();
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          dp[1] = mfma(fb[k], vf[k], dp[1]);
+#pragma unroll
+          for (int e = 16 / KS * k; e < 16 / KS * (k + 1); ++e) dp[0][e] *= sc[0][e];
+          fb[k] = T::cols(Qt, 16 * (k / DT), k % DT, lane);
+          keep_order();
+        }
+        take_lse(1);
+        finish(0);
+        keep_order();
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          dv[k % DT] = mfma(fa[k], p[k / DT], dv[k % DT]);
+#pragma unroll
+          for (int e = 16 / KS * k; e < 16 / KS * (k + 1); ++e) sc[1][e] = __builtin_amdgcn_exp2f(__fmaf_rn(sc[1][e], a.c, -ls[e]));
+          fa[k] = T::cols(Gt, 32 + 16 * (k / DT), k % DT, lane);
+          keep_order();
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          dk[k % DT] = mfma(fb[k], ds[k / DT], dk[k % DT]);
+#pragma unroll
+          for (int e = 16 / KS * k; e < 16 / KS * (k + 1); ++e) dp[1][e] *= sc[1][e];
+          fb[k] = T::cols(Qt, 32 + 16 * (k / DT), k % DT, lane);
+          keep_order();
+        }
+        finish(1);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) dv[k % DT] = mfma(fa[k], p[k / DT], dv[k % DT]);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) dk[k % DT] = mfma(fb[k], ds[k / DT], dk[k % DT]);
+      }
+    } else {
+      const int i0 = ci;
       if (i0 + 31 >= any_lo && i0 < any_hi) {
         f32x16 sc = zero16(), dp;   // do.v - delta comes out of the products
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 x = *reinterpret_cast<const f32x4*>(&Dt[32 * mt + 8 * g + 4 * (lane >> 5)]);
+          const f32x4 x = *reinterpret_cast<const f32x4*>(&Dt[8 * g + 4 * (lane >> 5)]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) dp[4 * g + e] = x[e];
         }
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Qt, 32 * mt, ks, lane), kf[ks], sc);
+        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Qt, 0, ks, lane), kf[ks], sc);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-          dp = mfma(T::rows(Gt, 32 * mt, ks, lane), WV == 1 ? vf[WV == 1 ? ks : 0] : T::rows(vt, 0, ks, lane), dp);
+          dp = mfma(T::rows(Gt, 0, ks, lane), T::rows(vt, 0, ks, lane), dp);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 x = *reinterpret_cast<const f32x4*>(&Lt[32 * mt + 8 * g + 4 * (lane >> 5)]);
+          const f32x4 x = *reinterpret_cast<const f32x4*>(&Lt[8 * g + 4 * (lane >> 5)]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = 4 * g + e;
@@ -953,9 +1053,9 @@ __global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, 
         for (int kk = 0; kk < 2; ++kk) {
           const bf16x8 p = pack8(sc, kk), ds = pack8(dp, kk);
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) dv[dt] = mfma(T::cols(Gt, 32 * mt + 16 * kk, dt, lane), p, dv[dt]);
+          for (int dt = 0; dt < DT; ++dt) dv[dt] = mfma(T::cols(Gt, 16 * kk, dt, lane), p, dv[dt]);
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) dk[dt] = mfma(T::cols(Qt, 32 * mt + 16 * kk, dt, lane), ds, dk[dt]);
+          for (int dt = 0; dt < DT; ++dt) dk[dt] = mfma(T::cols(Qt, 16 * kk, dt, lane), ds, dk[dt]);
         }
       }
     }
@@ -1188,13 +1288,14 @@ static int64_t dkv_row_tiles(const AttnSeq& s, int t, int causal, int window) {
 }
 
 // Plan of the dk, dv launch: parts that the query heads of a group are split into, and waves per SIMD
-// (see attn_dkv_kernel). The launch takes as long as its longest workgroup alone or as the mean over the
-// compute units, counted in tiles of 64 rows of 128 keys; the parts' fp32 results (written, read and
-// added) cost 0.03 us for every tile of 128 keys and part. The coefficients (us) are fitted to d = 128.
-// Estimate and measurement, sums included: 64 heads over 8, packed sequences of 1500, 1031, 783, 700, 64,
-// 17 and 1 tokens: one wave, 2 parts 254 and 263, 4 parts 271 and 270; two waves, 2 parts 320 and 322, 4
-// parts 233 and 238, 8 parts 269 and 262. 32 heads over 8, one sequence of 2048, 4 parts: one wave 114 and
-// 112, two waves 118 and 124.
+// (see attn_dkv_kernel). Work is counted in tiles of 64 rows of 128 keys for one query head. The launch takes
+// as long as its longest workgroup alone, or as the mean over the compute units with the starts and ends of
+// the workgroups and, with a mask, the tiles on its edge of every key tile and head; the parts' fp32 results
+// (written, read and added) cost 0.03 us for every tile of 128 keys and part. The coefficients (us) are
+// fitted to d = 128. Estimated and measured, sums included: 32 heads over 8, one causal sequence of 2048, 4
+// parts, one wave 109 and 106, two waves 112 and 110; four of 512, 4 parts, one wave 60 and 57, two 49 and 49;
+// 64 heads over 8, packed sequences of 1500, 1031, 783, 700, 64, 17 and 1 tokens, one wave, 2 parts 232 and
+// 260, two waves, 4 parts 230 and 239; 8 heads, one sequence of 4096, one wave 135 and 125, two 176 and 151.
 struct KvPlan {
   int splits, gper, waves;
 };
@@ -1213,11 +1314,14 @@ static KvPlan kv_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, in
   KvPlan best{1, G, 2};
   double best_cost = -1;
   for (int want = 1; want <= G; ++want) {
-    const int gper = (int)ceil64(G, want);
-    if (ceil64(G, gper) != want) continue;
+    if (G % want) continue;   // equal parts (packed batch as above: 3 parts 10 us slower than 4)
+    const int gper = G / want;
     const double mean = (double)total * G * kv_heads / kUnits, most = (double)longest * gper;
+    const double wgs = (double)tiles * kv_heads * want / kUnits;
+    const double edges = causal || window ? (double)tiles * kv_heads * G / kUnits : 0;
     const double sums = want > 1 ? 4 + 0.03 * tiles * kv_heads * want : 0;
-    const double one = std::max(2.4 * most, 2.8 * mean) + sums, two = std::max(3.1 * most, 2.35 * mean) + sums;
+    const double one = std::max(1.95 * most + 10, 2.05 * mean + 7 * wgs + 3 * edges) + sums;
+    const double two = std::max(2.6 * most + 10, 1.97 * mean + 3.5 * wgs + 1.5 * edges) + sums;
     for (int waves = d <= 64 ? 2 : 1; waves <= 2; ++waves) {   // the small tiles of d <= 64 leave room for two waves anyway
       const double cost = waves == 1 ? one : two;
       if (best_cost < 0 || cost < best_cost) {

@@ -346,7 +346,7 @@ __device__ __forceinline__ f32x16 taken_half(const void* to0, const void* to1, i
 // ------------------------------------------------------------------------------------------
 // Forward. 4 waves take 128 query rows of one head, 32 per wave; keys and values stream through LDS in
 // tiles of 64, two tiles deep, by LDS-DMA. Bound by the matrix unit and, in launches that fill the GPU,
-// by its power: 8192 tokens, 32 heads over 8, d 128, not causal, 1051 us = 1046 TFLOP/s, where a plain
+// by its power: 8192 tokens, 32 heads over 8, d 128, not causal, 990 us = 1110 TFLOP/s, where a plain
 // product of 16384^3 reaches 1355. A tile costs a workgroup that shares its compute unit with another
 // 0.93 us, but 1.15 to 1.4 us alone, with one wave a SIMD that waits for its own reads and exponentials.
 // So where the longest workgroups decide, a workgroup has GR = 2 groups of 4 waves, which take the tiles of
@@ -408,11 +408,26 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
     const int j0 = j_g + t * GR * BN;
     if (j0 < wb.hi && j0 + BN > wa.lo) {
       f32x16 sc[BN / 32];
+      // KS operands are on their way from LDS at any time: each register takes its next contents as soon as its
+      // product is issued, the first half of the values' operands before the exponentials (8192 tokens, not
+      // causal, 1016 -> 987 us, 8 heads of 4096 tokens 60 -> 55; the compiler's own order keeps two)
+      bf16x8 f[KS];
 #pragma unroll
-      for (int kt = 0; kt < BN / 32; ++kt) {
-        sc[kt] = zero16();
+      for (int ks = 0; ks < KS; ++ks) f[ks] = T::rows(Kt, 0, ks, lane);
+      sc[0] = zero16();
+      sc[1] = zero16();
+      keep_order();
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) sc[kt] = mfma(T::rows(Kt, 32 * kt, ks, lane), qf[ks], sc[kt]);
+      for (int ks = 0; ks < KS; ++ks) {
+        sc[0] = mfma(f[ks], qf[ks], sc[0]);
+        f[ks] = T::rows(Kt, 32, ks, lane);
+        keep_order();
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        sc[1] = mfma(f[ks], qf[ks], sc[1]);
+        f[ks] = T::cols(Vt, 16 * (ks / DT), ks % DT, lane);
+        keep_order();
       }
       // some row of the wave does not see some key of the tile
       if (j0 + BN > wa.hi || j0 < wb.lo) {
@@ -421,11 +436,12 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
       }
       acc.update(sc, a.c, slack);
 #pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk) {
-        const bf16x8 p = pack8(sc[kk / 2], kk & 1);
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(T::cols(Vt, 16 * kk, dt, lane), p, acc.o[dt]);
+      for (int i = 0; i < KS; ++i) {
+        acc.o[i % DT] = mfma(f[i], pack8(sc[0], i / DT), acc.o[i % DT]);
+        f[i] = T::cols(Vt, 32 + 16 * (i / DT), i % DT, lane);
       }
+#pragma unroll
+      for (int i = 0; i < KS; ++i) acc.o[i % DT] = mfma(f[i], pack8(sc[1], i / DT), acc.o[i % DT]);
     }
   };
   for (int t = 0; t < nt; t += 2) {
@@ -693,7 +709,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnFwdArgs a, con
 // ------------------------------------------------------------------------------------------
 // Backward, first launch: delta (and, for the second launch, lse log2(e) and -delta) and dq. As the
 // forward (128 query rows a workgroup, keys streamed), with the probabilities recomputed from lse: three
-// products a tile instead of two, 8192 tokens, 32 heads over 8, d 128, not causal 1520 us = 1085 TFLOP/s.
+// products a tile instead of two, 8192 tokens, 32 heads over 8, d 128, not causal 1380 us = 1195 TFLOP/s.
 // delta is formed from the forward's rounded o, as the call gets it: an error of up to 2^-9 |do||o| in every
 // dS of a row, which with the rounding of dS itself puts dq and dk at 2.5e-3 of their norm from the exact
 // ones (their own rounding to bf16 alone is 1.7e-3), and at 4e-3 where rows see few keys. -delta enters the
@@ -770,10 +786,23 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_dq_kernel(const AttnBwdArgs 
       const int j0 = j_g + t * GR * BN + 32 * kt;
       if (j0 < wb.hi && j0 + 32 > wa.lo) {
         f32x16 sc = zero16(), dp = less_delta;   // do.v - delta comes out of the products
+        constexpr int R = 2;   // operands on their way, as in the forward; more of them spill
+        bf16x8 f[R];
+        auto operand = [&](int n) __attribute__((always_inline)) {
+          if (n < KS) return T::rows(Kt, 32 * kt, n, lane);
+          if (n < 2 * KS) return T::rows(Vt, 32 * kt, n - KS, lane);
+          return T::cols(Kt, 32 * kt + 16 * ((n - 2 * KS) / DT), n % DT, lane);
+        };
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) sc = mfma(T::rows(Kt, 32 * kt, ks, lane), qf[ks], sc);
+        for (int n = 0; n < R; ++n) f[n] = operand(n);
+        keep_order();
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) dp = mfma(T::rows(Vt, 32 * kt, ks, lane), gf[ks], dp);
+        for (int n = 0; n < 2 * KS; ++n) {
+          if (n < KS) sc = mfma(f[n % R], qf[n % KS], sc);
+          else dp = mfma(f[n % R], gf[n % KS], dp);
+          f[n % R] = operand(n + R);
+          keep_order();
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) dp[i] *= __builtin_amdgcn_exp2f(__fmaf_rn(sc[i], a.c, -lse2));
         // selected away, not multiplied: a row without keys has lse -inf
@@ -782,7 +811,11 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_dq_kernel(const AttnBwdArgs 
         for (int kk = 0; kk < 2; ++kk) {
           const bf16x8 ds = pack8(dp, kk);
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) dq[dt] = mfma(T::cols(Kt, 32 * kt + 16 * kk, dt, lane), ds, dq[dt]);
+          for (int dt = 0; dt < DT; ++dt) {
+            const int n = 2 * KS + kk * DT + dt;
+            dq[dt] = mfma(f[n % R], ds, dq[dt]);
+            if (n + R < 3 * KS) f[n % R] = operand(n + R);
+          }
         }
       }
     }

@@ -346,7 +346,7 @@ __device__ __forceinline__ f32x16 taken_half(const void* to0, const void* to1, i
 // ------------------------------------------------------------------------------------------
 // Forward. 4 waves take 128 query rows of one head, 32 per wave; keys and values stream through LDS in
 // tiles of 64, two tiles deep, by LDS-DMA. Bound by the matrix unit and, in launches that fill the GPU,
-// by its power: 8192 tokens, 32 heads over 8, d 128, not causal, 990 us = 1110 TFLOP/s, where a plain
+// by its power: 8192 tokens, 32 heads over 8, d 128, not causal, 980 us = 1120 TFLOP/s, where a plain
 // product of 16384^3 reaches 1355. A tile costs a workgroup that shares its compute unit with another
 // 0.93 us, but 1.15 to 1.4 us alone, with one wave a SIMD that waits for its own reads and exponentials.
 // So where the longest workgroups decide, a workgroup has GR = 2 groups of 4 waves, which take the tiles of

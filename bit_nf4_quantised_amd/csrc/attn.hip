@@ -1095,12 +1095,12 @@ __global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, 
     ci += BM;
     if (ci >= i_hi) ci = i_lo;
   };
-  if constexpr (WV == 1) {
+  if constexpr (WV == 1 || DP == 64) {
     for (int t = 0; t < total; t += 2) {
       tile(t, Qs0, Gs0, Ls0[wave], Ds0[wave], Qs1, Gs1, Ls1[wave], Ds1[wave]);
       if (t + 1 < total) tile(t + 1, Qs1, Gs1, Ls1[wave], Ds1[wave], Qs0, Gs0, Ls0[wave], Ds0[wave]);
     }
-  } else {   // code for each stage does not leave registers enough for two waves
+  } else {   // at d > 64 code for each stage does not leave registers enough for two waves
     for (int t = 0; t < total; ++t) {
       const bool o = t & 1;
       tile(t, o ? Qs1 : Qs0, o ? Gs1 : Gs0, o ? Ls1[wave] : Ls0[wave], o ? Ds1[wave] : Ds0[wave], o ? Qs0 : Qs1, o ? Gs0 : Gs1,

@@ -582,7 +582,7 @@ class AttnSeqs:
     """The sequences of a batch for qlora_attn_fwd and qlora_attn_bwd, marshalled once (for all layers
     of a step): entries (q0, nq, k0, nk), nq query tokens from q0 and nk key tokens from k0, with the
     queries standing at the last nq key positions. causal hides later keys; window > 0 hides keys more
-    than window - 1 positions back."""
+    than window - 1 positions back; both may be changed between calls."""
 
     def __init__(self, seqs, causal: bool = True, window: int = 0):
         flat = [int(v) for s in seqs for v in s]
@@ -604,13 +604,13 @@ class AttnSeqs:
         return AttnSeqs(seqs, causal, window)
 
     def _config(self, q, k, scale):
-        """The configuration for tensors of these sizes, marshalled when the sizes change."""
+        """The configuration for tensors of these sizes, marshalled when anything it holds changes."""
         (tq, heads, d), (tk, kv_heads, dk) = q.shape, k.shape
         if d != dk:
             raise ValueError("shape mismatch: q and k differ in head size")
-        key = (tq, heads, d, tk, kv_heads, scale)
+        key = (tq, heads, d, tk, kv_heads, scale, self.causal, self.window)
         if self._key != key:
-            self._cfg = CAttnConfig(heads, kv_heads, d, int(self.causal), self.window,
+            self._cfg = CAttnConfig(heads, kv_heads, d, int(bool(self.causal)), int(self.window),
                                     d ** -0.5 if scale is None else scale, tq, tk)
             self._key = key
         return ctypes.byref(self._cfg)

@@ -582,7 +582,8 @@ class AttnSeqs:
     """The sequences of a batch for qlora_attn_fwd and qlora_attn_bwd, marshalled once (for all layers
     of a step): entries (q0, nq, k0, nk), nq query tokens from q0 and nk key tokens from k0, with the
     queries standing at the last nq key positions. causal hides later keys; window > 0 hides keys more
-    than window - 1 positions back; both may be changed between calls."""
+    than window - 1 positions back; both may be changed between calls. Layers of different sizes, and
+    threads, may share one."""
 
     def __init__(self, seqs, causal: bool = True, window: int = 0):
         flat = [int(v) for s in seqs for v in s]
@@ -591,7 +592,7 @@ class AttnSeqs:
         self.count = len(flat) // 4
         self.causal, self.window = bool(causal), int(window)
         self._seqs = (ctypes.c_int64 * max(len(flat), 4))(*flat)
-        self._key = self._cfg = None
+        self._last = (None, None)   # what the last configuration was made of, and it
 
     @staticmethod
     def packed(lengths, causal: bool = True, window: int = 0) -> "AttnSeqs":
@@ -604,16 +605,19 @@ class AttnSeqs:
         return AttnSeqs(seqs, causal, window)
 
     def _config(self, q, k, scale):
-        """The configuration for tensors of these sizes, marshalled when anything it holds changes."""
+        """The configuration for tensors of these sizes, marshalled when anything it holds changes. The pair in
+        _last is replaced whole and a configuration is never written to again: another thread's call for other
+        sizes changes nothing here."""
         (tq, heads, d), (tk, kv_heads, dk) = q.shape, k.shape
         if d != dk:
             raise ValueError("shape mismatch: q and k differ in head size")
         key = (tq, heads, d, tk, kv_heads, scale, self.causal, self.window)
-        if self._key != key:
-            self._cfg = CAttnConfig(heads, kv_heads, d, int(bool(self.causal)), int(self.window),
-                                    d ** -0.5 if scale is None else scale, tq, tk)
-            self._key = key
-        return ctypes.byref(self._cfg)
+        last, cfg = self._last
+        if last != key:
+            cfg = CAttnConfig(heads, kv_heads, d, int(bool(self.causal)), int(self.window),
+                              d ** -0.5 if scale is None else scale, tq, tk)
+            self._last = (key, cfg)
+        return ctypes.byref(cfg)
 
     def workspace_bytes(self, q, k, backward: bool = False, scale: float | None = None) -> int:
         return int(lib.qlora_attn_workspace_bytes(self._config(q, k, scale), self.count, self._seqs,

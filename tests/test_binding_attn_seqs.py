@@ -1,5 +1,7 @@
 """AttnSeqs on the host: the configuration that a call gets is that of its own tensors and of the mask as it
 stands, whatever calls came before or run beside it. No kernel runs here."""
+import threading
+
 import pytest
 import torch
 
@@ -35,3 +37,50 @@ def test_layers_of_different_sizes_share_one():
     held = [(z, s._config(*_qk(*z), None)) for z in sizes]
     for (tokens, heads, kv, d), cfg in held:      # earlier ones keep what they were made with
         assert _read(cfg) == (heads, kv, d, 1, 0, tokens, tokens)
+
+
+class _Interrupted(float):
+    """A scale during whose comparison another call for other sizes runs to its end, as a thread may."""
+    def __new__(cls, value, other):
+        self = super().__new__(cls, value)
+        self.other = other
+        return self
+
+    def __eq__(self, x):
+        self.other()
+        return float(self) == float(x)
+
+    def __ne__(self, x):
+        return not self == x
+
+    __hash__ = float.__hash__
+
+
+def test_a_call_in_between_changes_nothing():
+    s = q.AttnSeqs.packed([40, 24])
+    a, b = _qk(64, 8, 2, 128), _qk(64, 4, 4, 64)
+    other = lambda: s._config(*b, 0.5)  # noqa: E731
+    s._config(*a, _Interrupted(0.125, other))
+    got = s._config(*a, _Interrupted(0.125, other))
+    assert _read(got) == (8, 2, 128, 1, 0, 64, 64) and got._obj.scale == 0.125
+    assert _read(s._config(*b, 0.5)) == (4, 4, 64, 1, 0, 64, 64)
+    assert _read(s._config(*a, 0.125)) == (8, 2, 128, 1, 0, 64, 64)
+
+
+def test_threads_share_one():
+    s = q.AttnSeqs.packed([40, 24])
+    wrong = []
+
+    def work(heads, kv, d):
+        Q, K = _qk(64, heads, kv, d)
+        for _ in range(2000):
+            got = _read(s._config(Q, K, None))
+            if got != (heads, kv, d, 1, 0, 64, 64):
+                wrong.append((heads, got))
+                return
+    threads = [threading.Thread(target=work, args=z) for z in ((8, 2, 128), (4, 4, 64), (16, 1, 80))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong

@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import os
 from array import array
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -156,6 +157,25 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _pool_of(stream, device):
+    """The context in which torch allocates from the memory pool of the stream that a call is given. A block of
+    another pool may be handed out again, or still be read, by that other stream's work while the call's kernels
+    use it."""
+    if stream is None:
+        return nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call on `stream` (None: the current one), to be dropped when the call returns."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with _pool_of(stream, device):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _dtype(t, *allowed):
     if t is not None and t.dtype not in allowed:
         raise TypeError(f"dtype {t.dtype} not in {allowed}")
@@ -279,7 +299,7 @@ def qlora_linear_fwd(weight: NF4Weight, x, A, B, scale: float, y, u_out=None, ws
             or y.shape != (M, weight.N) or (u_out is not None and u_out.numel() != M * r):
         raise ValueError("shape mismatch")
     if ws is None:
-        ws = workspace(M, weight.N, weight.K, r, x.device)
+        ws = _scratch(max(qlora_workspace_bytes(M, weight.N, weight.K, r), 256), x.device, stream)
     cw = weight.c_struct()
     _check(lib.qlora_linear_fwd(ctypes.byref(cw), _ptr(x), M, _ptr(A), _ptr(B), r, scale, _ptr(y),
                                 _ptr(u_out), _ptr(ws), ws.numel() * ws.element_size(),
@@ -319,7 +339,8 @@ def qlora_linear_fwd_group(weights: list, x, As: list, Bs: list, scale: float, y
             if u is not None and u.numel() != M * r:
                 raise ValueError("shape mismatch")
     if ws is None:
-        ws = workspace_group(M, [w.N for w in weights], weights[0].K, r, x.device)
+        nbytes = qlora_workspace_bytes_group(M, [w.N for w in weights], weights[0].K, r)
+        ws = _scratch(max(nbytes, 256), x.device, stream)
     cws = [w.c_struct() for w in weights]
     P = ctypes.c_void_p
     wp = (P * n)(*[ctypes.addressof(c) for c in cws])
@@ -348,7 +369,8 @@ def qlora_linear_fwd_recompute_group(weights: list, x, As: list, Bs: list, scale
                 or u.numel() != M * r:
             raise ValueError("shape mismatch")
     if ws is None:
-        ws = workspace_group(M, [w.N for w in weights], weights[0].K, r, x.device)
+        nbytes = qlora_workspace_bytes_group(M, [w.N for w in weights], weights[0].K, r)
+        ws = _scratch(max(nbytes, 256), x.device, stream)
     cws = [w.c_struct() for w in weights]
     P = ctypes.c_void_p
     wp = (P * n)(*[ctypes.addressof(c) for c in cws])
@@ -380,7 +402,8 @@ def qlora_linear_bwd_group(weights: list, x, dys: list, As: list, Bs: list, scal
                 or (dxs is not None and dxs[i].shape != (M, w.K)):
             raise ValueError("shape mismatch")
     if ws is None:
-        ws = workspace_group(M, [w.N for w in weights], weights[0].K, r, x.device)
+        nbytes = qlora_workspace_bytes_group(M, [w.N for w in weights], weights[0].K, r)
+        ws = _scratch(max(nbytes, 256), x.device, stream)
     cws = [w.c_struct() for w in weights]
     P = ctypes.c_void_p
     arr = lambda ts: (P * n)(*[_ptr(t) for t in ts])  # noqa: E731
@@ -431,7 +454,7 @@ def qlora_linear_fwd_recompute(weight: NF4Weight, x, A, B, scale: float, u, y, w
             or y.shape != (M, weight.N) or u.numel() != M * r:
         raise ValueError("shape mismatch")
     if ws is None:   # with the forward's workspace the launches (and y) are the forward's own
-        ws = workspace(M, weight.N, weight.K, r, x.device)
+        ws = _scratch(max(qlora_workspace_bytes(M, weight.N, weight.K, r), 256), x.device, stream)
     cw = weight.c_struct()
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib.qlora_linear_fwd_recompute(ctypes.byref(cw), _ptr(x), M, _ptr(A), _ptr(B), r, scale,
@@ -452,7 +475,7 @@ def qlora_linear_bwd(weight: NF4Weight, x, dy, A, B, scale: float, u, dx, dA, dB
             or dB.shape != (weight.N, r) or (dx is not None and dx.shape != (M, weight.K)):
         raise ValueError("shape mismatch")
     if ws is None:
-        ws = workspace(M, weight.N, weight.K, r, x.device)
+        ws = _scratch(max(qlora_workspace_bytes(M, weight.N, weight.K, r), 256), x.device, stream)
     cw = weight.c_struct()
     _check(lib.qlora_linear_bwd(ctypes.byref(cw), _ptr(x), _ptr(dy), M, _ptr(A), _ptr(B), r, scale,
                                 _ptr(u), _ptr(dx), _ptr(dA), _ptr(dB), int(bool(accumulate)),
@@ -530,7 +553,7 @@ def qlora_linear_bwd_act8(weights: list, act8: Act8, dys: list, As: list, Bs: li
     pdx = None if dxs is None else _mptrs(P, dxs, _BF16, [(M, K)] * n)
     pda, pdb = _mptrs(P, dAs, _F32, r_cols), _mptrs(P, dBs, _F32, rows_r)
     if ws is None:
-        ws = workspace_act8(M, [w.N for w in weights], K, r, act8.codes.device)
+        ws = _scratch(max(qlora_workspace_bytes_act8(M, [w.N for w in weights], K, r), 256), act8.codes.device, stream)
     cws = [w.c_struct() for w in weights]
     x8 = act8.c_struct()
     _check(lib.qlora_linear_bwd_act8(n, P(*[ctypes.addressof(c) for c in cws]), ctypes.byref(x8), pdy, M, pa, pb, r, scale,
@@ -571,7 +594,7 @@ def qlora_rmsnorm_bwd(dy, h, weight, rstd, dx, dw=None, dh=None, accumulate: boo
             or (dh is not None and dh.shape != shape) or (dw is not None and dw.numel() != K):
         raise ValueError("shape mismatch")
     if ws is None and dw is not None:
-        ws = torch.empty(max(int(lib.qlora_rmsnorm_workspace_bytes(M, K)), 256), dtype=torch.uint8, device=h.device)
+        ws = _scratch(max(int(lib.qlora_rmsnorm_workspace_bytes(M, K)), 256), h.device, stream)
     _check(lib.qlora_rmsnorm_bwd(pdy, pdh, ph, pw, ps, M, K, pdx, pdw, int(bool(accumulate)), _ptr(ws),
                                  0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
            "qlora_rmsnorm_bwd")
@@ -654,12 +677,12 @@ def _lse_ptr(lse, q):
     return _dptr(lse, _F32)
 
 
-def _attn_ws(seqs, cfg, backward, ws, device):
+def _attn_ws(seqs, cfg, backward, ws, device, stream):
     if ws is None:
         need = int(lib.qlora_attn_workspace_bytes(cfg, seqs.count, seqs._seqs, backward))
         if not need:
             return None, None, 0
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _scratch(need, device, stream)
     return ws, _ptr(ws), ws.numel() * ws.element_size()
 
 
@@ -670,7 +693,7 @@ def qlora_attn_fwd(seqs: AttnSeqs, q, k, v, o, lse=None, scale: float | None = N
     keep, tq, tk, tv, to = _attn_tensors((q, q.shape), (k, k.shape), (v, k.shape), (o, q.shape))
     cfg = seqs._config(q, k, scale)
     plse = _lse_ptr(lse, q)
-    ws, pws, nbytes = _attn_ws(seqs, cfg, 0, ws, q.device)
+    ws, pws, nbytes = _attn_ws(seqs, cfg, 0, ws, q.device, stream)
     _check(lib.qlora_attn_fwd(cfg, seqs.count, seqs._seqs, tq, tk, tv, to, plse, pws, nbytes, _stream(stream)),
            "qlora_attn_fwd")
 
@@ -685,7 +708,7 @@ def qlora_attn_bwd(seqs: AttnSeqs, q, k, v, o, lse, dout, dq, dk, dv, scale: flo
     keep, *ts = _attn_tensors((q, sq), (k, sk), (v, sk), (o, sq), (dout, sq), (dq, sq), (dk, sk), (dv, sk))
     cfg = seqs._config(q, k, scale)
     plse = _lse_ptr(lse, q)
-    ws, pws, nbytes = _attn_ws(seqs, cfg, 1, ws, q.device)
+    ws, pws, nbytes = _attn_ws(seqs, cfg, 1, ws, q.device, stream)
     _check(lib.qlora_attn_bwd(cfg, seqs.count, seqs._seqs, *ts[:4], plse, *ts[4:], pws, nbytes, _stream(stream)),
            "qlora_attn_bwd")
 
@@ -854,13 +877,14 @@ def quantize_weight(w: torch.Tensor, stream=None, absmax: torch.Tensor | None = 
     the fp32 absmax as its scales."""
     N, K = w.shape
     book = _book(codebook)
-    if absmax is None:
-        absmax = torch.empty(N * K // 64, dtype=torch.float32, device=w.device)
-    if not double_quant:
-        qw = NF4Weight(torch.empty(N * K // 2, dtype=torch.uint8, device=w.device), None, None, N, K, absmax,
-                       codebook=book)
-    else:
-        qw = empty_weight(N, K, w.device, book)
+    with _pool_of(stream, w.device):
+        if absmax is None:
+            absmax = torch.empty(N * K // 64, dtype=torch.float32, device=w.device)
+        if not double_quant:
+            qw = NF4Weight(torch.empty(N * K // 2, dtype=torch.uint8, device=w.device), None, None, N, K, absmax,
+                           codebook=book)
+        else:
+            qw = empty_weight(N, K, w.device, book)
     if book == 0:
         nf4_quantize(w, qw.packed, absmax, stream)
     else:

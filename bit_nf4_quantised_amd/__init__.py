@@ -609,9 +609,11 @@ class AttnSeqs:
     threads, may share one."""
 
     def __init__(self, seqs, causal: bool = True, window: int = 0):
-        flat = [int(v) for s in seqs for v in s]
-        if any(len(s) != 4 for s in seqs):
-            raise ValueError("a sequence is (q0, nq, k0, nk)")
+        flat = []
+        for s in seqs:   # any iterable, read once
+            if len(s) != 4:
+                raise ValueError("a sequence is (q0, nq, k0, nk)")
+            flat += [int(v) for v in s]
         self.count = len(flat) // 4
         self.causal, self.window = bool(causal), int(window)
         self._seqs = (ctypes.c_int64 * max(len(flat), 4))(*flat)

@@ -84,3 +84,10 @@ def test_threads_share_one():
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+def test_entries_from_an_iterator_are_checked():
+    good = q.AttnSeqs((i, 1, 10 * i, 10) for i in range(3))
+    assert good.count == 3 and list(good._seqs) == [0, 1, 0, 10, 1, 1, 10, 10, 2, 1, 20, 10]
+    with pytest.raises(ValueError):
+        q.AttnSeqs((i, 1, 10 * i) for i in range(4))     # twelve values: no three sequences

@@ -3,10 +3,15 @@
 // Blocks of 64 values along a row: absmax a (the largest |x| of the block, bf16, exact because x is
 // bf16) and codes round(127 x / a) in -127..127, nearest integer of the exact quotient, ties to even;
 // a block of zeros stores a = 0 and codes 0. The value a code stands for is code * a / 127.
+// A block that holds a NaN or an infinity stores it as a (a NaN before an infinity) and codes 0: it stands
+// for NaN throughout, so that what is lost in 8 bits cannot pass for numbers. Magnitudes are compared as
+// integers, in which order NaN > infinity > numbers; a maximum of floats drops NaN.
 #pragma once
 #include "common.h"
 
 namespace nf4 {
+
+constexpr uint32_t kBf16Inf = 0x7F80u;
 
 // The codes of a block's values: num(x) / den, with one Newton step after the hardware reciprocal.
 // 127 x is exact in fp32 (15 significant bits), and a quotient of such numbers that is not a tie is
@@ -28,9 +33,9 @@ struct Act8Block {
   }
 };
 
-// Codes of 8 consecutive bf16 values (4 dwords) whose block maximum is a, in byte order.
-__device__ __forceinline__ u32x2 act8_codes(const u32x4& x, float a) {
-  const Act8Block b(a);
+// Codes of 8 consecutive bf16 values (4 dwords) whose block maximum has the bf16 bits `absmax`, in byte order.
+__device__ __forceinline__ u32x2 act8_codes(const u32x4& x, uint32_t absmax) {
+  const Act8Block b(__uint_as_float(absmax << 16));
   u32x2 o;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -38,18 +43,18 @@ __device__ __forceinline__ u32x2 act8_codes(const u32x4& x, float a) {
     const uint32_t c0 = (uint32_t)b.code(__uint_as_float(p << 16)), c1 = (uint32_t)b.code(__uint_as_float(p & 0xFFFF0000u));
     const uint32_t c2 = (uint32_t)b.code(__uint_as_float(q << 16)), c3 = (uint32_t)b.code(__uint_as_float(q & 0xFFFF0000u));
     const uint32_t lo = __builtin_amdgcn_perm(c1, c0, 0x0C0C0400u), hi = __builtin_amdgcn_perm(c3, c2, 0x0C0C0400u);
-    o[k] = lo | (hi << 16);
+    o[k] = absmax < kBf16Inf ? lo | (hi << 16) : 0u;
   }
   return o;
 }
 
-// largest |x| of 8 bf16 values
-__device__ __forceinline__ float absmax8(const u32x4& x) {
-  float m = 0.f;
+// bf16 bits of the largest magnitude among the 8 values of each of 8 neighbouring lanes (a block), in all of them
+__device__ __forceinline__ uint32_t act8_absmax(const u32x4& x) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m{0, 0};
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    m = fmaxf(m, fmaxf(__uint_as_float((x[k] << 16) & 0x7FFFFFFFu), __uint_as_float(x[k] & 0x7FFF0000u)));
-  return m;
+  for (int k = 0; k < 4; ++k) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[k] & 0x7FFF7FFFu));
+  return umax8(max((uint32_t)m.x, (uint32_t)m.y));
 }
 
 }  // namespace nf4

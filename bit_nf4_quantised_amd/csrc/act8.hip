@@ -24,10 +24,10 @@ __global__ __launch_bounds__(256) void act8_pack_kernel(const u32x4* __restrict_
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int64_t i = i0 + k * step;
-      const float a = max8(absmax8(v[k]));   // vecs is a multiple of 8: a block's lanes are in or out together
+      const uint32_t a = act8_absmax(v[k]);   // vecs is a multiple of 8: a block's lanes are in or out together
       if (i < vecs) {
         codes[i] = act8_codes(v[k], a);
-        if ((i & 7) == 0) absmax[i >> 3] = (uint16_t)(__float_as_uint(a) >> 16);
+        if ((i & 7) == 0) absmax[i >> 3] = (uint16_t)a;
       }
     }
   }

@@ -142,6 +142,13 @@ __device__ __forceinline__ float max8(float v) {
   v = fmaxf(v, dpp_f<0x141>(v));   // row_half_mirror
   return v;
 }
+// the same of unsigned integers
+__device__ __forceinline__ uint32_t umax8(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+  return v;
+}
 // max over the whole wave (all lanes receive the result)
 __device__ __forceinline__ float wave_max(float v) {
   v = max8(v);

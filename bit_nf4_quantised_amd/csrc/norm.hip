@@ -101,13 +101,13 @@ __global__ __launch_bounds__(W * R * 64) void rmsnorm_fwd_kernel(const NormFwdAr
     for (int e = 0; e < 8; ++e) y[e] = h[v][e] * rstd * w[e];
     const u32x4 py = pack8f(y);
     // all lanes take part: vecs is a multiple of 8 where codes are asked for
-    const float am = a.codes ? max8(absmax8(py)) : 0.f;
+    const uint32_t am = a.codes ? act8_absmax(py) : 0u;
     if (i < vecs) {
       if (a.h) *reinterpret_cast<u32x4*>(a.h + base + 8 * i) = pack8f(h[v]);
       *reinterpret_cast<u32x4*>(a.y + base + 8 * i) = py;
       if (a.codes) {
         *reinterpret_cast<u32x2*>(a.codes + base + 8 * i) = act8_codes(py, am);
-        if ((i & 7) == 0) a.absmax[(base + 8 * i) / 64] = (uint16_t)(__float_as_uint(am) >> 16);
+        if ((i & 7) == 0) a.absmax[(base + 8 * i) / 64] = (uint16_t)am;
       }
     }
   }

@@ -344,7 +344,10 @@ int qlora_adamw_plan_destroy(qlora_adamw_plan *plan);
  *   absmax  uint16[M*K/64]: bf16 bits of the block's largest |x| (exact, as x is bf16);
  *   codes   int8[M*K]: round(127 x / absmax), the nearest integer of the exact quotient, ties to even;
  *           a block of zeros has absmax 0 and codes 0.
- * A code stands for code * absmax / 127: within absmax / 254 of x. */
+ * A code stands for code * absmax / 127: within absmax / 254 of x.
+ * NaN and Inf are allowed in x here: a block that holds one keeps the largest magnitude's bits as its
+ * absmax (a NaN before an Inf) and codes 0. It stands for NaN throughout, in qlora_act8_unpack and in
+ * the dA of qlora_linear_bwd_act8, so a diverged step stays visible. */
 typedef struct {
   int8_t *codes;      /* [M*K]    */
   uint16_t *absmax;   /* [M*K/64] */

@@ -87,13 +87,16 @@ def rmsnorm_bwd(dy, dh, h, w, rstd):
 def act8(x):
     """8-bit codes (int8) and block maxima of [M, K] values that bf16 holds: absmax over blocks of 64,
     codes the integers nearest to 127 x / absmax, ties to even. The float64 quotient decides rightly: a
-    quotient of bf16 values times 127 is a tie (which float64 holds) or further than 2^-20 from one."""
+    quotient of bf16 values times 127 is a tie (which float64 holds) or further than 2^-20 from one. A block
+    with a NaN or an infinity has that as its maximum and codes 0."""
     b = np.asarray(x, dtype=np.float64).reshape(x.shape[0], -1, 64)
     a = np.abs(b).max(axis=2)
-    codes = np.rint(127.0 * b / np.where(a > 0, a, 1.0)[:, :, None])
+    b = np.where(np.isfinite(a)[:, :, None], b, 0.0)
+    codes = np.rint(127.0 * b / np.where((a > 0) & np.isfinite(a), a, 1.0)[:, :, None])
     return codes.astype(np.int8).reshape(x.shape), a
 
 
 def act8_values(codes, absmax):
     """The values codes stand for: code * absmax / 127."""
-    return codes.astype(np.float64) * np.repeat(absmax, 64, axis=1) / 127.0
+    with np.errstate(invalid="ignore"):   # 0 times infinity: NaN
+        return codes.astype(np.float64) * np.repeat(absmax, 64, axis=1) / 127.0

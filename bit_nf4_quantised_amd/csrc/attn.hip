@@ -269,6 +269,12 @@ __device__ __forceinline__ Range visible(int p, int nk, int causal, int window) 
   return r;
 }
 
+// A row's sum l is exactly 0 when the row saw no key, and NaN once a score was NaN (which no maximum shows:
+// fmaxf drops it, and the reference maximum may still be -inf). So l alone tells a row without keys, which
+// gives 0 and -inf, from one that is lost, which gives NaN, on every path alike.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float lse_of(float mc, float l) { return l == 0.f ? -INFINITY : mc * kLn2 + __logf(l); }
+
 // Running softmax of a wave's 32 owned rows (one per lane column) over NT blocks of 32 streamed keys.
 template <int DT>
 struct Online {
@@ -452,7 +458,7 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
   float l = half_sum(acc.l);
   uint16_t* dst = row < s.nq ? a.o.p + (s.q0 + row) * a.o.token + (int64_t)head * a.o.head : nullptr;
   if constexpr (GR == 1) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = inverse_sum(l);
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) store_cols(dst, acc.o[dt], inv, dt, a.d, lane);
   } else {
@@ -475,7 +481,7 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
     const float fo = mo == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mo * a.c - mc);
     l = l * fm + lo * fo;
     acc.mc = mc;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = inverse_sum(l);
 #pragma unroll
     for (int dt = 0; dt < H; ++dt) {
       f32x16 v = taken_half<H>(Ks0, Ks1, dt, grp, wave, lane);
@@ -485,7 +491,7 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs
     }
   }
   if (a.lse && grp == 0 && lane < 32 && row < s.nq)
-    a.lse[(int64_t)head * a.lse_stride + s.q0 + row] = l > 0.f ? acc.mc * kLn2 + __logf(l) : -INFINITY;
+    a.lse[(int64_t)head * a.lse_stride + s.q0 + row] = lse_of(acc.mc, l);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -600,7 +606,10 @@ __global__ __launch_bounds__(256, DP == 128 ? 1 : 2) void attn_split_kernel(cons
   const float mxc = mx == -INFINITY ? 0.f : mx * a.c;
   l = 0.f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) l += Ms[k][col] == -INFINITY ? 0.f : Ls[k][col] * __builtin_amdgcn_exp2f(Ms[k][col] * a.c - mxc);
+  for (int k = 0; k < 4; ++k) {
+    const float w = Ms[k][col] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(Ms[k][col] * a.c - mxc);
+    l += Ls[k][col] * w;   // 0 times NaN stays NaN
+  }
   const float f = acc.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(acc.mc - mxc);
   __syncthreads();
   // the waves' outputs as [wave][d][32 rows]
@@ -632,7 +641,7 @@ __global__ __launch_bounds__(256, DP == 128 ? 1 : 2) void attn_split_kernel(cons
     }
     if (c0 >= a.d) continue;
     if (ns == 1) {
-      const float inv = rl > 0.f ? 1.f / rl : 0.f;
+      const float inv = inverse_sum(rl);
       u32x4 o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
@@ -645,10 +654,10 @@ __global__ __launch_bounds__(256, DP == 128 ? 1 : 2) void attn_split_kernel(cons
   }
   if ((tid & 7) == 0) {
     if (ns == 1) {
-      if (a.lse) a.lse[(int64_t)ohead * a.lse_stride + s.q0 + otok] = rl > 0.f ? rm * kLn2 + __logf(rl) : -INFINITY;
+      if (a.lse) a.lse[(int64_t)ohead * a.lse_stride + s.q0 + otok] = lse_of(rm, rl);
     } else {
       float* part = sp.part + (sp.row0[si] + ((int64_t)grow * a.kv_heads + u.kvh) * ns + split) * (int64_t)(a.d + 8);
-      part[a.d] = rl > 0.f ? rm : -INFINITY;
+      part[a.d] = rl == 0.f ? -INFINITY : rm;   // finite (0 at least) where the sum is NaN: the join reads it
       part[a.d + 1] = rl;
     }
   }
@@ -698,12 +707,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnFwdArgs a, con
       }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = inverse_sum(l);
   if (c < a.d)
     *reinterpret_cast<uint32_t*>(a.o.p + (s.q0 + tok) * a.o.token + (int64_t)head * a.o.head + c) =
         pack_bf16x2(v0 * inv, v1 * inv);
   if (a.lse && lane == 0)
-    a.lse[(int64_t)head * a.lse_stride + s.q0 + tok] = l > 0.f ? mx * kLn2 + __logf(l) : -INFINITY;
+    a.lse[(int64_t)head * a.lse_stride + s.q0 + tok] = lse_of(mx, l);
 }
 
 // ------------------------------------------------------------------------------------------

@@ -931,9 +931,10 @@ __global__ __launch_bounds__(256, WV) void attn_dkv_kernel(const AttnBwdArgs a, 
   else
     Stream::values(vt, a, s, u.kvh, j0 + wave * 32, lane);
 
-  // query rows [i_lo, i_hi) that see some key of the workgroup
+  // query rows [i_lo, i_hi) that see some key of the workgroup, from a multiple of BM on; but none that sees no
+  // key at all (when causal the first nq - nk), whose q and dout may hold anything: 0 times NaN is no zero
   const int jl = min(s.nk, j0 + 128) - 1;
-  const int i_lo = (a.causal ? max(0, j0 - shift) : 0) & ~(BM - 1);
+  const int i_lo = a.causal ? max(max(0, j0 - shift) & ~(BM - 1), -shift) : 0;
   const int i_hi = a.window ? (int)min((int64_t)s.nq, (int64_t)jl + a.window - shift) : s.nq;
   const int tiles = i_hi > i_lo ? (i_hi - i_lo + BM - 1) / BM : 0;
   const int g0 = u.sub * sp.gper, g1 = min(G, g0 + sp.gper);
@@ -1324,7 +1325,7 @@ static bool two_groups(const AttnSeqs& q, int heads, int causal, int window) {
 // 64-row tiles of queries that see some key of key tile t (as attn_dkv_kernel counts them)
 static int64_t dkv_row_tiles(const AttnSeq& s, int t, int causal, int window) {
   const int64_t shift = (int64_t)s.nk - s.nq, j0 = 128 * (int64_t)t, jl = std::min<int64_t>(s.nk, j0 + 128) - 1;
-  const int64_t lo = (causal ? std::max<int64_t>(0, j0 - shift) : 0) & ~int64_t(63);
+  const int64_t lo = causal ? std::max(std::max<int64_t>(0, j0 - shift) & ~int64_t(63), -shift) : 0;
   const int64_t hi = window ? std::min<int64_t>(s.nq, jl + window - shift) : s.nq;
   return hi > lo ? ceil64(hi - lo, 64) : 0;
 }

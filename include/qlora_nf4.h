@@ -407,10 +407,11 @@ size_t qlora_rmsnorm_workspace_bytes(int64_t M, int64_t K);   /* 0 for refused s
  * p = nk - nq + i of the sequence's keys and sees key j when
  *   (not causal or j <= p) and (window == 0 or j > p - window).
  *   z_ij = scale q_i.k_j;  lse_i = ln sum_j exp(z_ij);  o_i = sum_j exp(z_ij - lse_i) v_j.
- * A query that sees no key gives o = 0, lse = -inf and no gradient. Keys that no query of their sequence
- * sees may hold anything, NaN too; their gradients are zero. A NaN in a query, or in a key that it sees,
- * gives NaN in the query's o and lse, however the keys are split over the GPU. Queries and keys outside
- * every sequence are neither read nor written. heads / kv_heads query heads share a key head in turn. */
+ * A query that sees no key gives o = 0, lse = -inf and no gradient, whatever its q and dout hold. Keys
+ * that no query of their sequence sees may hold anything, NaN too; their gradients are zero. A NaN in a
+ * query, or in a key that it sees, gives NaN in the query's o and lse, however the keys are split over the
+ * GPU. Queries and keys outside every sequence are neither read nor written. heads / kv_heads query heads
+ * share a key head in turn. */
 typedef struct {
   int64_t q0, nq;   /* query tokens q0 .. q0 + nq - 1 of q, o, lse and their gradients; nq >= 0 */
   int64_t k0, nk;   /* key tokens k0 .. k0 + nk - 1 of k, v and their gradients; nk >= 0 */

@@ -6,6 +6,9 @@
 
 namespace nf4 {
 
+// A launch holds fewer than 2^32 threads.
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
+
 struct Codes;   // common.h
 
 hipError_t launch_quantize(const float* w, int64_t numel, uint8_t* packed, float* absmax,

@@ -244,11 +244,28 @@ static int norm_bwd_groups(int64_t M, int64_t K) {
 }
 size_t norm_bwd_ws_floats(int64_t M, int64_t K) { return (size_t)norm_bwd_groups(M, K) * (size_t)K; }
 
-hipError_t launch_rmsnorm_fwd(const NormFwdArgs& a, hipStream_t stream) {
-  norm_shape(a.K, [&](auto s) {
+// A workgroup has its R rows to itself; more rows than one launch holds threads for take several.
+hipError_t launch_rmsnorm_fwd(const NormFwdArgs& args, hipStream_t stream) {
+  norm_shape(args.K, [&](auto s) {
     using S = decltype(s);
-    hipLaunchKernelGGL((rmsnorm_fwd_kernel<S::kW, S::kR, S::kV>), dim3((unsigned)((a.M + S::kR - 1) / S::kR)),
-                       dim3(S::kW * S::kR * 64), 0, stream, a);
+    constexpr int threads = S::kW * S::kR * 64;
+    constexpr int64_t most = kMaxThreads / threads * S::kR;
+    for (int64_t row = 0; row < args.M; row += most) {
+      NormFwdArgs a = args;
+      const int64_t at = row * a.K;
+      a.M = args.M - row < most ? args.M - row : most;
+      a.x += at;
+      if (a.res) a.res += at;
+      if (a.h) a.h += at;
+      a.y += at;
+      if (a.rstd) a.rstd += row;
+      if (a.codes) {
+        a.codes += at;
+        a.absmax += at / 64;
+      }
+      hipLaunchKernelGGL((rmsnorm_fwd_kernel<S::kW, S::kR, S::kV>), dim3((unsigned)((a.M + S::kR - 1) / S::kR)), dim3(threads), 0,
+                         stream, a);
+    }
   });
   return hipGetLastError();
 }

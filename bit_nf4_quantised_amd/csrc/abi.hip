@@ -563,10 +563,12 @@ int check_attn_config(const qlora_attn_config* c) {
 }
 
 // Sequences inside the tensors; query ranges in order and apart (each output row has one writer), and
-// for the backward key ranges too. Launches count workgroups in 32 bits.
+// for the backward key ranges too. A sequence's tiles of 128 queries, over the heads, fit a launch of workgroups
+// of 256 threads; for the backward its tiles of 128 keys, over the key heads, too.
 int check_attn_seqs(const qlora_attn_config* c, int64_t count, const qlora_attn_seq* s, bool backward) {
   if (count < 0 || count > (int64_t(1) << 24)) return NF4_ERR_SHAPE;
   if (count && !s) return NF4_ERR_NULL;
+  constexpr int64_t most = nf4::kMaxThreads / 256;
   int64_t q_end = 0, k_end = 0, workgroups = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (s[i].nq < 0 || s[i].nk < 0 || s[i].nq >= kAttnLimit || s[i].nk >= kAttnLimit) return NF4_ERR_SHAPE;
@@ -574,7 +576,9 @@ int check_attn_seqs(const qlora_attn_config* c, int64_t count, const qlora_attn_
     if (s[i].k0 < (backward ? k_end : 0) || s[i].k0 > c->k_tokens - s[i].nk) return NF4_ERR_SHAPE;
     q_end = s[i].q0 + s[i].nq;
     k_end = s[i].k0 + s[i].nk;
-    workgroups += ((s[i].nq + 127) / 128 + (s[i].nk + 127) / 128) * c->heads;
+    const int64_t q_tiles = (s[i].nq + 127) / 128, k_tiles = (s[i].nk + 127) / 128;
+    if (q_tiles * c->heads > most || (backward && k_tiles * c->kv_heads > most)) return NF4_ERR_SHAPE;
+    workgroups += (q_tiles + k_tiles) * c->heads;
     if (workgroups >= (int64_t(1) << 30)) return NF4_ERR_SHAPE;
   }
   return NF4_OK;

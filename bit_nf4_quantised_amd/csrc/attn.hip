@@ -1179,6 +1179,7 @@ __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(const AttnBwdArgs a, 
 
 // ------------------------------------------------------------------------------------------
 // Host side: sequences in order of falling length, in launches of up to kAttnSeqs.
+constexpr int64_t kAttnGroups = kMaxThreads / 256;   // workgroups of a launch
 static int64_t ceil64(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
 // the heaviest sequences first, so that the last workgroups to start are short ones
@@ -1191,13 +1192,17 @@ static std::vector<AttnSeq> by_work(const AttnSeq* seqs, int64_t count, bool key
   return v;
 }
 
-// one launch's sequences, `tiles_of(seq)` workgroup tiles each
+// The sequences of one launch from v[from] on, `tiles_of(seq)` workgroup tiles each and `per_tile` workgroups a
+// tile: up to kAttnSeqs, and no more workgroups than a launch holds. One sequence alone always fits (the entry
+// points refuse those that do not).
 template <typename F>
-static AttnSeqs pack_seqs(const std::vector<AttnSeq>& v, size_t from, F tiles_of) {
+static AttnSeqs pack_seqs(const std::vector<AttnSeq>& v, size_t from, int64_t per_tile, F tiles_of) {
   AttnSeqs q{};
   for (size_t i = from; i < v.size() && q.count < kAttnSeqs; ++i) {
+    const int64_t end = q.first[q.count] + (int64_t)tiles_of(v[i]);
+    if (q.count && end * per_tile > kAttnGroups) break;
     q.seq[q.count] = v[i];
-    q.first[q.count + 1] = q.first[q.count] + (int)tiles_of(v[i]);
+    q.first[q.count + 1] = (int)end;
     ++q.count;
   }
   return q;
@@ -1246,12 +1251,14 @@ static int64_t split_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, i
   *cost_us = -1;
   for (const AttnSeq& s : v) longest = std::max(longest, s.nk - first_key(s, window));
   for (int64_t chunk = 256;; chunk += std::max<int64_t>(128, chunk / 8 / 128 * 128)) {
-    int64_t wgs = 0, ranges = 0;
+    int64_t wgs = 0, ranges = 0, most = 0;
     for (const AttnSeq& s : v) {
       const int64_t n = (int64_t)split_count(s, window, chunk) * kv_heads;
       ranges += n;
       wgs += row_tiles(s, G) * n;
+      most = std::max(most, row_tiles(s, G) * n);
     }
+    if (most > kAttnGroups && chunk < longest) continue;   // a sequence has to fit a launch
     const double key = size * std::max({0.0064, 0.0096 * std::min<int64_t>(wgs, kUnits) / kUnits,
                                         0.022 * std::min<int64_t>(ranges, kUnits) / kUnits});
     const double cost = ceil64(wgs, kUnits) * (5 + key * std::min(chunk, longest)) + (chunk < longest ? 4 : 0);
@@ -1261,6 +1268,11 @@ static int64_t split_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, i
     }
     if (chunk >= longest) return best;
   }
+}
+// the sequences of the attn_split_kernel launch from p.few[from] on
+static AttnSeqs few_seqs(const FwdPlan& p, size_t from, int G, int kv_heads, int window) {
+  return pack_seqs(p.few, from, kv_heads,
+                   [&](const AttnSeq& s) { return row_tiles(s, G) * split_count(s, window, p.chunk); });
 }
 static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, int d, int window) {
   FwdPlan p;
@@ -1292,13 +1304,15 @@ static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, 
   }
   if (p.few.empty()) return p;
   p.chunk = split_chunk(p.few, G, kv_heads, d, window, &cost);
-  for (size_t from = 0; from < p.few.size(); from += kAttnSeqs) {
+  for (size_t from = 0; from < p.few.size();) {
+    const AttnSeqs q = few_seqs(p, from, G, kv_heads, window);
     int64_t f = 0;
-    for (size_t i = from; i < p.few.size() && i < from + kAttnSeqs; ++i) {
-      const int ns = split_count(p.few[i], window, p.chunk);
-      if (ns > 1) f += (int64_t)p.few[i].nq * heads * ns * (d + 8);
+    for (int i = 0; i < q.count; ++i) {
+      const int ns = split_count(q.seq[i], window, p.chunk);
+      if (ns > 1) f += (int64_t)q.seq[i].nq * heads * ns * (d + 8);
     }
     p.part_floats = std::max(p.part_floats, f);
+    from += (size_t)q.count;
   }
   return p;
 }
@@ -1307,6 +1321,7 @@ static FwdPlan fwd_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, 
 // attn_fwd_kernel): when its work, spread over the compute units, is at most 1.2 times that of its longest
 // workgroup, in tiles of 64 keys (1.13 gains 15 % in the forward, 1.25 loses 14 %).
 static bool two_groups(const AttnSeqs& q, int heads, int causal, int window) {
+  if ((int64_t)q.first[q.count] * heads > kMaxThreads / 512) return false;
   int64_t longest = 0, total = 0;
   for (int i = 0; i < q.count; ++i) {
     const AttnSeq& s = q.seq[i];
@@ -1358,6 +1373,7 @@ static KvPlan kv_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, in
   double best_cost = -1;
   for (int want = 1; want <= G; ++want) {
     if (G % want) continue;   // equal parts (packed batch as above: 3 parts 10 us slower than 4)
+    if (want > 1 && tiles * kv_heads * want > kAttnGroups) break;
     const int gper = G / want;
     const double mean = (double)total * G * kv_heads / kUnits, most = (double)longest * gper;
     const double wgs = (double)tiles * kv_heads * want / kUnits;
@@ -1376,7 +1392,7 @@ static KvPlan kv_plan(const std::vector<AttnSeq>& v, int heads, int kv_heads, in
   return best;
 }
 static int64_t dkv_part_floats(const std::vector<AttnSeq>& v, int splits, int kv_heads, int dp) {
-  if (splits == 1) return 0;
+  if (splits == 1) return 0;   // with parts the workgroups of the whole call fit a launch: kAttnSeqs to each
   int64_t most = 0;
   for (size_t from = 0; from < v.size(); from += kAttnSeqs) {
     int64_t t = 0;
@@ -1403,8 +1419,9 @@ hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t co
   if (v.empty()) return hipSuccess;
   const int G = a.heads / a.kv_heads;
   const FwdPlan plan = fwd_plan(v, a.heads, a.kv_heads, a.d, a.window);
-  for (size_t from = 0; from < plan.many.size(); from += kAttnSeqs) {
-    const AttnSeqs q = pack_seqs(plan.many, from, q_tiles);
+  for (size_t from = 0; from < plan.many.size();) {
+    const AttnSeqs q = pack_seqs(plan.many, from, a.heads, q_tiles);
+    from += (size_t)q.count;
     const dim3 grid((unsigned)(q.first[q.count] * a.heads));
     if (two_groups(q, a.heads, a.causal, a.window)) {
       if (a.d <= 64) hipLaunchKernelGGL((attn_fwd_kernel<64, 2>), grid, dim3(512), 0, stream, a, q);
@@ -1414,10 +1431,9 @@ hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t co
       else hipLaunchKernelGGL((attn_fwd_kernel<128, 1>), grid, dim3(256), 0, stream, a, q);
     }
   }
-  for (size_t from = 0; from < plan.few.size(); from += kAttnSeqs) {
-    const AttnSeqs q = pack_seqs(plan.few, from, [&](const AttnSeq& s) {
-      return row_tiles(s, G) * split_count(s, a.window, plan.chunk);
-    });
+  for (size_t from = 0; from < plan.few.size();) {
+    const AttnSeqs q = few_seqs(plan, from, G, a.kv_heads, a.window);
+    from += (size_t)q.count;
     AttnSplit sp{};
     sp.part = ws;
     sp.chunk = (int)plan.chunk;
@@ -1445,8 +1461,9 @@ hipError_t launch_attn_bwd(const AttnBwdArgs& args, const AttnSeq* seqs, int64_t
   a.lse2 = ws;
   a.less_delta = ws + round64(q_tokens * a.heads);
   const std::vector<AttnSeq> vq = by_work(seqs, count, false), vk = by_work(seqs, count, true);
-  for (size_t from = 0; from < vq.size(); from += kAttnSeqs) {
-    const AttnSeqs q = pack_seqs(vq, from, q_tiles);
+  for (size_t from = 0; from < vq.size();) {
+    const AttnSeqs q = pack_seqs(vq, from, a.heads, q_tiles);
+    from += (size_t)q.count;
     const dim3 grid((unsigned)(q.first[q.count] * a.heads));
     if (two_groups(q, a.heads, a.causal, a.window)) {
       if (a.d <= 64) hipLaunchKernelGGL((attn_dq_kernel<64, 2>), grid, dim3(512), 0, stream, a, q);
@@ -1458,8 +1475,9 @@ hipError_t launch_attn_bwd(const AttnBwdArgs& args, const AttnSeq* seqs, int64_t
   }
   const KvPlan plan = kv_plan(vk, a.heads, a.kv_heads, a.d, a.causal, a.window);
   const AttnKvSplit sp{ws + 2 * round64(q_tokens * a.heads), plan.splits, plan.gper};
-  for (size_t from = 0; from < vk.size(); from += kAttnSeqs) {
-    const AttnSeqs q = pack_seqs(vk, from, k_tiles);
+  for (size_t from = 0; from < vk.size();) {
+    const AttnSeqs q = pack_seqs(vk, from, (int64_t)a.kv_heads * sp.splits, k_tiles);
+    from += (size_t)q.count;
     const int units = q.first[q.count] * a.kv_heads;
     const dim3 grid((unsigned)(units * sp.splits)), sums((unsigned)(units * 2));
     if (a.d <= 64) {

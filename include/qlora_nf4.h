@@ -434,7 +434,9 @@ typedef struct {
 
 /* Forward. seqs: HOST array of count entries, their query ranges in ascending order and apart (key
  * ranges may be shared and in any order, as for caches); packed training batches and padded or shared
- * caches are both lists of such sequences. Up to 64 sequences travel in one launch's arguments.
+ * caches are both lists of such sequences. Up to 64 sequences travel in one launch's arguments. Of one
+ * sequence ceil(nq / 128) * heads (in the backward ceil(nk / 128) * kv_heads too) is below 2^24, and the
+ * call's sum of (ceil(nq / 128) + ceil(nk / 128)) * heads below 2^30.
  *   lse   [heads][q_tokens] float output, or NULL (it is needed by the backward).
  *   ws    at least qlora_attn_workspace_bytes(cfg, count, seqs, 0) bytes (0: may be NULL).
  * Few queries over many keys (decoding) split the keys over the GPU and join the parts in order.

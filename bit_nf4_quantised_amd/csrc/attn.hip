@@ -8,7 +8,7 @@
 //   dq_i = scale sum_j dS_ij k_j    dk_j = scale sum_i dS_ij q_i    dv_j = sum_i P_ij do_i
 // (dk, dv also sum over the query heads that share the key head). Scores, softmax statistics and all
 // sums are fp32; P and dS are rounded to bf16 where they enter the second product of each pair, as
-// the matrix instructions take bf16 operands (relative error 2^-9 a term, independent over terms).
+// the matrix instructions take bf16 operands (relative error up to 2^-8 a term, independent over terms).
 //
 // Layout. Every product is taken with v_mfma_f32_32x32x16_bf16, whose result holds in lane l column
 // l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4 for i < 16. The scores are formed with the rows that
@@ -352,16 +352,17 @@ __device__ __forceinline__ f32x16 taken_half(const void* to0, const void* to1, i
 // ------------------------------------------------------------------------------------------
 // Forward. 4 waves take 128 query rows of one head, 32 per wave; keys and values stream through LDS in
 // tiles of 64, two tiles deep, by LDS-DMA. Bound by the matrix unit and, in launches that fill the GPU,
-// by its power: 8192 tokens, 32 heads over 8, d 128, not causal, 980 us = 1120 TFLOP/s, where a plain
-// product of 16384^3 reaches 1355. A tile costs a workgroup that shares its compute unit with another
+// by its power: 8192 tokens, 32 heads over 8, d 128, not causal, 962 us = 1143 TFLOP/s, where a plain
+// product of 16384^3 reaches 1355 (d 64: 572 us = 961 TFLOP/s, d 80 and 96 take d 128's tiles: 873 and 906 us). A tile costs a workgroup that shares its compute unit with another
 // 0.93 us, but 1.15 to 1.4 us alone, with one wave a SIMD that waits for its own reads and exponentials.
 // So where the longest workgroups decide, a workgroup has GR = 2 groups of 4 waves, which take the tiles of
 // the same rows in turn and are joined at the end; two_groups() says where. Measured, one group and two, us:
-// 256 workgroups of up to 4096 keys 94 and 77; one causal sequence, 32 heads over 8, of 1536 tokens 36 and
-// 30, of 2048 57 and 56; 3000 tokens, 16 heads over 4, 70 and 53. Where the work spreads evenly the
+// 256 workgroups of up to 4096 keys 94 and 77; one causal sequence, 32 heads over 8, of 1536 tokens 31.7 and
+// 27.8, of 2048 44.7 and 42.3; 3000 tokens, 16 heads over 4, 55.3 and 45.7. Where the work spreads evenly the
 // other form is better, as two workgroups on a unit start and end at different times: four causal sequences
-// of 512, 32 heads over 8, 22 and 25, 2048 tokens without a mask 75 and 79, 2368 workgroups of packed
-// sequences 109 and 137.
+// of 512, 32 heads over 8, 20.8 and 23.6, 2048 tokens without a mask 68.7 and 70.8, 8192 causal ones 493 and
+// 518, 2368 workgroups of packed sequences 109 and 137. At d = 64: 1536 tokens 22.8 and 19.1, 2048 31.5 and 29.3,
+// 3000 37.3 and 30.0, four of 512 14.3 and 16.0, 2048 without a mask 43.4 and 44.2, 8192 293 and 322.
 template <int DP, int GR>
 __global__ __launch_bounds__(256 * GR, 2) void attn_fwd_kernel(const AttnFwdArgs a, const AttnSeqs sq) {
   constexpr int BN = 64, KS = DP / 16, DT = DP / 32;
@@ -718,13 +719,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnFwdArgs a, con
 // ------------------------------------------------------------------------------------------
 // Backward, first launch: delta (and, for the second launch, lse log2(e) and -delta) and dq. As the
 // forward (128 query rows a workgroup, keys streamed), with the probabilities recomputed from lse: three
-// products a tile instead of two, 8192 tokens, 32 heads over 8, d 128, not causal 1380 us = 1195 TFLOP/s.
-// delta is formed from the forward's rounded o, as the call gets it: an error of up to 2^-9 |do||o| in every
+// products a tile instead of two, 8192 tokens, 32 heads over 8, d 128, not causal 1303 us = 1266 TFLOP/s.
+// delta is formed from the forward's rounded o, as the call gets it: an error of up to 2^-8 |do||o| in every
 // dS of a row, which with the rounding of dS itself puts dq and dk at 2.5e-3 of their norm from the exact
 // ones (their own rounding to bf16 alone is 1.7e-3), and at 4e-3 where rows see few keys. -delta enters the
 // products as their starting value, which saves a subtraction per score.
-// GR as in the forward: one causal sequence, 32 heads over 8, of 2048 tokens 193 and 187 us for the whole
-// backward, 3000 tokens, 16 heads over 4, 221 and 200; four causal sequences of 512 84 and 91.
+// GR as in the forward, one group and two, us for the whole backward: one causal sequence, 32 heads over 8, of
+// 1536 tokens 110.5 and 107.2, of 2048 154.8 and 153.9, 3000 tokens, 16 heads over 4, 184 and 170; four causal
+// sequences of 512 74.9 and 81.8, 8192 tokens 1706 and 1755. At d = 64: 78.6 and 75.5, 102.7 and 99.4, 131 and 120;
+// 48.1 and 51.6, 935 and 983.
 // One pass over the pairs could give dq, dk and dv together with five products instead of seven, but its
 // sums of dq over key tiles would need atomics, in no fixed order, or a partial dq per key tile.
 template <int DP, int GR>
@@ -863,8 +866,8 @@ __global__ __launch_bounds__(256 * GR, 2) void attn_dq_kernel(const AttnBwdArgs 
 // rows, two blocks that overlap. WV = 2: the values' operands are read from LDS and tiles have 32 rows, which
 // leaves room for two waves a SIMD. A workgroup of the first kind alone on a compute unit takes 1.9 us for 64
 // rows of 128 keys at d = 128, of the second 2.25 us, and two of the second 3.9 us for both (kv_plan chooses):
-// 32 heads over 8, one causal sequence of 2048 tokens 92 us and 96, four of 512 43 and 35, 8192 tokens, not
-// causal, 2.21 ms and 2.02 (1090 TFLOP/s of the four products).
+// 32 heads over 8, one causal sequence of 2048 tokens 94 us and 97, four of 512 42 and 34, 8192 tokens, not
+// causal, 2.06 ms and 1.94 (1130 TFLOP/s of the four products).
 template <int DP, int ROWS, int NW>
 struct RowStream {   // rows [lo, hi) of q, do, lse2 and less_delta, head after head, in tiles of ROWS <= 64
   typedef TileDma<DP, ROWS, NW> Dma;
@@ -1221,8 +1224,11 @@ static int64_t first_key(const AttnSeq& s, int window) {
 // to attn_fwd_kernel when its workgroups outnumber the compute units (256), or when its estimate, the
 // longest workgroup at 0.94 us for 64 keys and 7 us around it, is below that of attn_split_kernel
 // (split_chunk); all sequences of a launch of attn_split_kernel have one length of key range. Measured,
-// forward and split: 512 tokens of 600 keys, 32 heads over 8, 17 and 20 us; four sequences of 300, 8 heads
-// over 2, 11 and 15; 128 tokens of 4096 keys, 32 heads over 8, 64 and 29.
+// forward and split, us: 512 tokens of 600 keys, 32 heads over 8, 15 and 19; four sequences of 300, 8 heads
+// over 2, 10.5 and 14.5; 2000 tokens, 8 heads, 29 and 31; 1000 tokens, 8 heads over 2, 18 and 14; 128 tokens of
+// 4096 keys, 32 heads over 8, 52 and 28. The estimate of attn_fwd_kernel is for d = 128 and not made smaller for
+// d <= 64, where a tile costs a wave alone nearly as much: at d = 64 the same take 11.1 and 10.8, 10.5 and 10.6, 21
+// and 16, 13 and 11, 37 and 20.5, and the split is chosen for all but the four sequences.
 // Beside attn_fwd_kernel a launch of attn_split_kernel costs 4 us even for one token, so the short sequences
 // stay with the others if that adds less work than 4 us and none is longer than the longest of these (a
 // sequence of one token packed with 4095 others, 64 heads over 8: 106 us against 110).
@@ -1351,9 +1357,13 @@ static int64_t dkv_row_tiles(const AttnSeq& s, int t, int causal, int window) {
 // the workgroups and, with a mask, the tiles on its edge of every key tile and head; the parts' fp32 results
 // (written, read and added) cost 0.03 us for every tile of 128 keys and part. The coefficients (us) are
 // fitted to d = 128. Estimated and measured, sums included: 32 heads over 8, one causal sequence of 2048, 4
-// parts, one wave 109 and 106, two waves 112 and 110; four of 512, 4 parts, one wave 60 and 57, two 49 and 49;
+// parts, one wave 109 and 109, two waves 113 and 111; four of 512, 4 parts, one wave 60 and 56, two 50 and 47;
 // 64 heads over 8, packed sequences of 1500, 1031, 783, 700, 64, 17 and 1 tokens, one wave, 2 parts 232 and
-// 260, two waves, 4 parts 230 and 239; 8 heads, one sequence of 4096, one wave 135 and 125, two 176 and 151.
+// 234, two waves, 4 parts 230 and 219; 8 heads, one sequence of 4096, one wave 135 and 133, two 176 and 155; 8192
+// tokens, not causal, 2113 and 2055, 2024 and 1941. At d <= 64 the times are smaller but the number of parts that
+// they choose is still the best or within 1 % of it (d = 64, the whole backward with 1, 2, 4, 8 parts: 2048 tokens
+// 235, 143, 99; four of 512 72, 54, 48; the packed batch 361, 232, 186, 204; 1000 tokens, 32 heads over 4, 220, 125,
+// 77, 56, where 4, 4, 4 and 8 are chosen).
 struct KvPlan {
   int splits, gper, waves;
 };

@@ -876,7 +876,8 @@ def quantize_weight(w: torch.Tensor, stream=None, absmax: torch.Tensor | None = 
                     double_quant: bool = True, codebook=0) -> NF4Weight:
     """Quantise a float32 N x K device tensor: nf4_quantize (q4_quantize at blocksize 64 for the FP4
     or INT4 codebook) followed by nf4_double_quant, or with double_quant=False a weight that keeps
-    the fp32 absmax as its scales."""
+    the fp32 absmax as its scales. As under torch.cuda.stream(stream), the weight's memory comes from
+    the pool of the stream it is written on."""
     N, K = w.shape
     book = _book(codebook)
     with _pool_of(stream, w.device):

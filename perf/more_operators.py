@@ -30,6 +30,7 @@ NF4 = (-1.0, -0.6961928009986877, -0.5250729322433472, -0.39491742849349976, -0.
        0.24611225724220276, 0.3379151225090027, 0.4407097399234772, 0.5626168847084045, 0.722956657409668, 1.0)
 E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)     # the values of the bit patterns 0 .. 7; 8 .. 15 negate them
 INT4 = tuple(range(-7, 8))
+TOP = {"nf4": 1.0, "fp4": 6.0, "int4": 7.0}         # the value that a block's largest magnitude maps to
 
 
 def _book(name, dev):
@@ -37,8 +38,8 @@ def _book(name, dev):
     if name == "nf4":
         return torch.tensor(NF4, device=dev), torch.arange(16, device=dev)
     if name == "int4":
-        return torch.tensor(INT4 + (7,), dtype=torch.float32, device=dev) / 7, torch.arange(15, device=dev)
-    plus = torch.tensor(E2M1, device=dev) / 6
+        return torch.tensor(INT4 + (7,), dtype=torch.float32, device=dev), torch.arange(15, device=dev)
+    plus = torch.tensor(E2M1, device=dev)
     return torch.cat([plus, -plus]), torch.tensor([15, 14, 13, 12, 11, 10, 9, 0, 1, 2, 3, 4, 5, 6, 7], device=dev)
 
 
@@ -156,17 +157,19 @@ def _encode(x, book):
     zero = int((v == 0).nonzero()[0])
     at = torch.zeros(b.shape, dtype=torch.int64, device=x.device)
     for i in range(v.numel() - 1):      # codes below the value: a tie takes the lower code
-        at += b > (v[i] + v[i + 1]) / 2 * a
+        at += b * TOP[book] > (v[i] + v[i + 1]) / 2 * a
     at = torch.where(a == 0, torch.full_like(at, zero), at)
     p = order[at].to(torch.uint8)
     return p[..., 0::2] * 16 + p[..., 1::2], a.squeeze(-1).to(torch.bfloat16)
 
 
 def _decode(codes, absmax, d, book):
-    """The values that blocks stand for, in float32."""
+    """The values that blocks stand for, in float32. The format's value is the bf16 rounding of the float32 product
+    of the code and the block's step, so it is formed so."""
     value, _ = _book(book, codes.device)
+    step = absmax.float() * torch.tensor(1.0 / TOP[book], device=codes.device)
     p = torch.stack([codes >> 4, codes & 15], -1).long().flatten(-2)
-    return (value[p] * absmax.float()[..., None]).flatten(-2)[..., :d]
+    return (value[p] * step[..., None]).to(torch.bfloat16).float().flatten(-2)[..., :d]
 
 
 def _new_cache(tokens, kv, d, dev):
@@ -420,25 +423,29 @@ def _exact_rotate(s):
 
 
 def _exact_values(codes, absmax, d, book):
-    """float64 values of [rows, kv, blocks, 16] codes."""
+    """float64 values of [rows, kv, blocks, 16] codes: bf16 roundings by the format, as in _decode."""
     at = torch.empty(*codes.shape, 2, dtype=torch.int64, device=codes.device)
     at[..., 0], at[..., 1] = codes // 16, codes % 16
-    value = _book(book, codes.device)[0].double()
-    return (value[at.flatten(-2)] * absmax.double().unsqueeze(-1)).flatten(-2)[..., :d]
+    step = torch.mul(absmax.float(), torch.full((), 1.0 / TOP[book], dtype=torch.float32, device=at.device))
+    value = torch.mul(_book(book, codes.device)[0][at.flatten(-2)], step.unsqueeze(-1))
+    return value.bfloat16().double().flatten(-2)[..., :d]
 
 
 def _exact_store(s):
     c = s["case"]
     out = {}
     code = torch.sort(_book(c["book"], s["k"].device)[0].double().unique()).values
+    top = TOP[c["book"]]
     for n in ("k", "v"):
         x = torch.nn.functional.pad(s[n].double(), (0, -c["d"] % BLOCK))
         b = x.unflatten(-1, (-1, BLOCK))
         a = b.abs().max(-1, keepdim=True).values
         # the nearest of the sorted codes by distance; argmin would take either of two that tie
-        at = torch.searchsorted(code, b / torch.where(a > 0, a, torch.ones_like(a))).clamp(1, code.numel() - 1)
-        lower, upper = code[at - 1] * a, code[at] * a
-        new = torch.where(b - lower <= upper - b, lower, upper).flatten(-2)[..., :c["d"]]
+        at = torch.searchsorted(code, b * top / torch.where(a > 0, a, torch.ones_like(a))).clamp(1, code.numel() - 1)
+        lower, upper = code[at - 1], code[at]
+        near = torch.where(b * top - lower * a <= upper * a - b * top, lower, upper)
+        step = a.float() * torch.full((), 1.0 / top, dtype=torch.float32, device=a.device)
+        new = (near.float() * step).bfloat16().double().flatten(-2)[..., :c["d"]]     # rounded by the format
         if c["read"] == "new":
             out[n] = new
             continue

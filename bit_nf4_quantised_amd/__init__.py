@@ -12,12 +12,14 @@ byte, double quantisation of the scales to E4M3, two-level dequantisation to bf1
 linear's forward y = x W~^T + s x A^T B^T and backward (dX, dA, dB; no gradient for W), the
 adapter merged into the base for serving, and the adapter update of a training step (global
 gradient-norm clipping, then AdamW over A and B). Around the linears: root-mean-square norm with the
-residual's addition, attention over packed sequences or a key/value cache, both with their backward
-passes, and 8-bit activation checkpoints that the linears' backward reads.
+residual's addition, rotary positions with norms of the query and key heads, attention over packed
+sequences or a key/value cache, all with their backward passes, 8-bit activation checkpoints that the
+linears' backward reads, and a key/value cache in 4 bits with the attention over it.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from array import array
 from contextlib import nullcontext
@@ -70,6 +72,19 @@ class CAttnTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+class CRopeConfig(ctypes.Structure):
+    """Mirror of ``qlora_rope_config`` in include/qlora_nf4.h."""
+    _fields_ = [("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("factor", ctypes.c_float), ("tokens", ctypes.c_int64)]
+
+
+class CKv4(ctypes.Structure):
+    """Mirror of ``qlora_kv4`` in include/qlora_nf4.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("codebook", ctypes.c_int32)]
+
+
 _p, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 _W = ctypes.POINTER(CNF4Weight)
 _SIGS = {
@@ -110,6 +125,13 @@ _SIGS = {
     "qlora_attn_fwd": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "qlora_attn_bwd": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "qlora_attn_workspace_bytes": (_sz, [_p, _i64, _p, ctypes.c_int]),
+    "qlora_rope_fwd": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p]),
+    "qlora_rope_bwd": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, ctypes.c_int, _p, _sz, _p]),
+    "qlora_rope_workspace_bytes": (_sz, [_p]),
+    "qlora_kv4_write": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p]),
+    "qlora_kv4_read": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p]),
+    "qlora_attn_kv4_fwd": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "qlora_attn_kv4_workspace_bytes": (_sz, [_p, _i64, _p]),
     "nf4_storage_bytes": (_i64, [_i64]),
     "nf4_codebook": (None, [ctypes.POINTER(ctypes.c_float)]),
     "nf4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -715,6 +737,213 @@ def qlora_attn_bwd(seqs: AttnSeqs, q, k, v, o, lse, dout, dq, dk, dv, scale: flo
            "qlora_attn_bwd")
 
 
+# ------------------------------------------------------------------------- rotary positions
+class Rope:
+    """Rotary positions, marshalled once (for all layers of a model): the first `rot` features of a head in pairs,
+    (2i, 2i+1) if interleaved, else (i, i + rot/2), pair i turned by inv_freq[i] radians a position, by default
+    base ** (-2 i / rot). `factor` multiplies the rotated features.
+
+    For contexts longer than the model was trained on, `stretch` divides the frequencies: all of them when `trained`
+    is 0 (positions are interpolated); else those that make less than `low` turns in `trained` positions, while
+    those that make more than `high` stay, and in between the share that stays grows linearly with the turns."""
+
+    def __init__(self, rot: int, base: float = 10000.0, interleaved: bool = False, stretch: float = 1.0, trained: int = 0,
+                 low: float = 1.0, high: float = 4.0, factor: float = 1.0, inv_freq=None):
+        self.rot, self.interleaved, self.factor = int(rot), bool(interleaved), float(factor)
+        if inv_freq is None:
+            if not stretch > 0 or not base > 0 or (trained and not high > low):
+                raise ValueError("base and stretch must be above 0, and high above low")
+            inv_freq = []
+            for i in range(self.rot // 2):
+                f = float(base) ** (-2.0 * i / self.rot)
+                keep = min(1.0, max(0.0, (trained * f / (2 * math.pi) - low) / (high - low))) if trained else 0.0
+                inv_freq.append(f * (keep + (1.0 - keep) / stretch))
+        self.inv_freq = tuple(float(f) for f in inv_freq)
+        if len(self.inv_freq) * 2 != self.rot:
+            raise ValueError("one frequency for each of the rot / 2 pairs")
+        self._freq = (ctypes.c_double * max(len(self.inv_freq), 1))(*self.inv_freq)
+        self._last = (None, None)   # as AttnSeqs: what the last configuration was made of, and it
+
+    def _config(self, q, k, eps):
+        tokens, heads, d = q.shape
+        kv_heads = 0 if k is None else k.shape[1]
+        key = (tokens, heads, kv_heads, d, eps)
+        last, cfg = self._last
+        if last != key:
+            cfg = CRopeConfig(heads, kv_heads, d, self.rot, int(self.interleaved), eps, self.factor, tokens)
+            self._last = (key, cfg)
+        return ctypes.byref(cfg)
+
+
+def _rope_positions(rope, positions, q):
+    if positions is None:
+        if rope.rot:
+            raise ValueError("positions are needed to rotate")
+        return None
+    if positions.shape != q.shape[:1]:
+        raise ValueError("positions must hold one value a token")
+    return _dptr(positions, (torch.int64,))
+
+
+def _rope_weight(w, like):
+    if w is not None and (like is None or w.numel() != like.shape[2]):
+        raise ValueError("a head weight must hold d values")
+    return _dptr(w, _BF16)
+
+
+def _rope_pair(q, k, name):
+    """Shapes of the query and key rows of a call; k may be None."""
+    if q.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2])):
+        raise ValueError(f"shape mismatch: {name} are [tokens, heads, d] of the same tokens and head size")
+    return q.shape, None if k is None else k.shape
+
+
+def qlora_rope_fwd(rope: Rope, positions, q, k, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6,
+                   stream=None) -> None:
+    """Query and key heads [tokens, heads, d] (bf16, tokens and heads may be strided), normed over d where a weight
+    [d] is given, then rotated by their tokens' positions (int64 [tokens]). k and k_out may be None; an output may
+    be its input."""
+    sq, sk = _rope_pair(q, k, "q and k")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    pq, pw = _rope_positions(rope, positions, q), (_rope_weight(q_weight, q), _rope_weight(k_weight, k))
+    if k is None:
+        keep, tq, to = _attn_tensors((q, sq), (q_out, sq))
+        tk = tko = None
+    else:
+        keep, tq, to, tk, tko = _attn_tensors((q, sq), (q_out, sq), (k, sk), (k_out, sk))
+    _check(lib.qlora_rope_fwd(rope._config(q, k, eps), rope._freq, pq, tq, tk, *pw, to, tko, _stream(stream)),
+           "qlora_rope_fwd")
+
+
+def qlora_rope_bwd(rope: Rope, positions, dq_out, dk_out, dq, dk, q=None, k=None, q_weight=None, k_weight=None,
+                   dq_weight=None, dk_weight=None, eps: float = 1e-6, accumulate: bool = False, ws=None,
+                   stream=None) -> None:
+    """Backward of qlora_rope_fwd: dq, dk from the gradients dq_out, dk_out of its outputs, and, where asked for, the
+    weights' (float32 [d], added to with accumulate). Normed heads need the forward's inputs q and k."""
+    sq, sk = _rope_pair(dq_out, dk_out, "dq_out and dk_out")
+    if (dk_out is None) != (dk is None):
+        raise ValueError("dk_out and dk go together")
+    if (q_weight is not None and q is None) or (k_weight is not None and k is None):
+        raise ValueError("the backward of normed heads needs their inputs")
+    pp = _rope_positions(rope, positions, dq_out)
+    pw = _rope_weight(q_weight, dq_out), _rope_weight(k_weight, dk_out)
+    for dw, w in ((dq_weight, q_weight), (dk_weight, k_weight)):
+        if dw is not None and (w is None or dw.numel() != sq[2]):
+            raise ValueError("a head weight's gradient goes with the weight and holds d values")
+    pdw = _dptr(dq_weight, _F32), _dptr(dk_weight, _F32)
+    pairs = [(dq_out, sq), (dq, sq)]
+    if q_weight is not None:
+        pairs.append((q, sq))
+    if dk is not None:
+        pairs += [(dk_out, sk), (dk, sk)]
+        if k_weight is not None:
+            pairs.append((k, sk))
+    keep, *ts = _attn_tensors(*pairs)
+    ts = iter(ts)
+    tgo, tdq = next(ts), next(ts)
+    tq = next(ts) if q_weight is not None else None
+    tgk = tdk = tk = None
+    if dk is not None:
+        tgk, tdk = next(ts), next(ts)
+        tk = next(ts) if k_weight is not None else None
+    cfg = rope._config(dq_out, dk_out, eps)
+    nbytes = 0
+    if pdw[0] is not None or pdw[1] is not None:
+        if ws is None:
+            ws = _scratch(max(int(lib.qlora_rope_workspace_bytes(cfg)), 256), dq.device, stream)
+        nbytes = ws.numel() * ws.element_size()
+    _check(lib.qlora_rope_bwd(cfg, rope._freq, pp, tq, tk, *pw, tgo, tgk, tdq, tdk, *pdw, int(bool(accumulate)),
+                              _ptr(ws), nbytes, _stream(stream)), "qlora_rope_bwd")
+
+
+# ------------------------------------------------------------------------- a key/value cache in 4 bits
+class Kv4:
+    """The keys or the values of a cache in 4 bits: codes uint8 [tokens, kv_heads, blocks, 16] and absmax bf16
+    [tokens, kv_heads, blocks] for blocks of 32 along the head (format in include/qlora_nf4.h). Tokens and heads
+    may be strided, in the same way in both; empty_kv4 makes one whose heads come first in memory."""
+
+    def __init__(self, codes, absmax, d: int, codebook="nf4"):
+        nb = (int(d) + 31) // 32
+        _dtype(codes, torch.uint8)
+        _dtype(absmax, *_BF16)
+        if codes.dim() != 4 or absmax.dim() != 3 or codes.shape[:3] != absmax.shape or codes.shape[2:] != (nb, 16):
+            raise ValueError(f"codes must be [tokens, kv_heads, {nb}, 16] and absmax [tokens, kv_heads, {nb}]")
+        if not codes.is_cuda or codes.device != absmax.device:
+            raise ValueError("codes and absmax must live on one GPU")
+        tokens, heads = codes.shape[:2]
+        ts, hs, bs, one = codes.stride()
+        at, ah, ab = absmax.stride()
+        # the stride of a single head, token or block carries no meaning: give it a valid value
+        if heads <= 1:
+            hs, ah = 16 * nb, nb
+        if tokens <= 1:
+            ts = at = max(nb, ah * (heads - 1) + nb)
+            ts, at = (16 * at, at) if at < 1 << 20 else (16 * nb, nb)
+        if nb == 1:
+            bs, ab = 16, 1
+        if one != 1 or bs != 16 or ab != 1 or (ts, hs) != (16 * at, 16 * ah):
+            raise ValueError("codes and absmax must have whole blocks and the same order of tokens and heads")
+        self.codes, self.absmax, self.d, self.codebook = codes, absmax, int(d), _book(codebook)
+        self.shape = (tokens, heads, self.d)
+        self._c = CKv4(codes.data_ptr(), absmax.data_ptr(), at, ah, self.codebook)
+
+
+def empty_kv4(tokens: int, kv_heads: int, d: int, device="cuda", codebook="nf4") -> Kv4:
+    """An uninitialised 4-bit cache for `tokens` keys or values of kv_heads heads of size d."""
+    nb = (d + 31) // 32
+    return Kv4(torch.empty(kv_heads, tokens, nb, 16, dtype=torch.uint8, device=device).permute(1, 0, 2, 3),
+               torch.empty(kv_heads, tokens, nb, dtype=torch.bfloat16, device=device).permute(1, 0, 2), d, codebook)
+
+
+def _kv4_pair(k4, v4, heads, d):
+    if k4.shape != v4.shape or k4.codebook != v4.codebook:
+        raise ValueError("k4 and v4 must be alike")
+    if k4.d != d or (heads is not None and k4.shape[1] != heads):
+        raise ValueError("shape mismatch between the cache and the tensors")
+    return ctypes.byref(k4._c), ctypes.byref(v4._c)
+
+
+def _kv4_copy(seqs, k, v, k4, v4):
+    if k.dim() != 3:
+        raise ValueError("k and v are [tokens, kv heads, d]")
+    pk, pv = _kv4_pair(k4, v4, k.shape[1], k.shape[2])
+    keep, tk, tv = _attn_tensors((k, k.shape), (v, k.shape))
+    return seqs._config(k, k4, None), (tk, tv), (pk, pv), keep
+
+
+def qlora_kv4_write(seqs: AttnSeqs, k, v, k4: Kv4, v4: Kv4, stream=None) -> None:
+    """New keys and values k, v [tokens, kv heads, d] (bf16, strided) into a 4-bit cache: the nq tokens of every
+    sequence (q0, nq, k0, nk) become its last nq keys, so the list that the attention then takes says where."""
+    cfg, (tk, tv), (pk, pv), keep = _kv4_copy(seqs, k, v, k4, v4)
+    _check(lib.qlora_kv4_write(cfg, seqs.count, seqs._seqs, tk, tv, pk, pv, _stream(stream)), "qlora_kv4_write")
+
+
+def qlora_kv4_read(seqs: AttnSeqs, k4: Kv4, v4: Kv4, k, v, stream=None) -> None:
+    """The last nq keys and values of every sequence out of a 4-bit cache, in bf16: into tokens q0 .. of k and v."""
+    cfg, (tk, tv), (pk, pv), keep = _kv4_copy(seqs, k, v, k4, v4)
+    _check(lib.qlora_kv4_read(cfg, seqs.count, seqs._seqs, pk, pv, tk, tv, _stream(stream)), "qlora_kv4_read")
+
+
+def qlora_attn_kv4_fwd(seqs: AttnSeqs, q, k4: Kv4, v4: Kv4, o, lse=None, scale: float | None = None, ws=None,
+                       stream=None) -> None:
+    """qlora_attn_fwd over a 4-bit cache: q, o [query tokens, heads, d] (bf16, strided)."""
+    if q.dim() != 3:
+        raise ValueError("q is [query tokens, heads, d]")
+    pk, pv = _kv4_pair(k4, v4, None, q.shape[2])
+    keep, tq, to = _attn_tensors((q, q.shape), (o, q.shape))
+    cfg = seqs._config(q, k4, scale)
+    plse = _lse_ptr(lse, q)
+    pws, nbytes = None, 0
+    if ws is None:
+        need = int(lib.qlora_attn_kv4_workspace_bytes(cfg, seqs.count, seqs._seqs))
+        ws = _scratch(need, q.device, stream) if need else None
+    if ws is not None:
+        pws, nbytes = _ptr(ws), ws.numel() * ws.element_size()
+    _check(lib.qlora_attn_kv4_fwd(cfg, seqs.count, seqs._seqs, tq, pk, pv, to, plse, pws, nbytes, _stream(stream)),
+           "qlora_attn_kv4_fwd")
+
+
 # ------------------------------------------------------------------------- format variants
 Q4_CODEBOOKS = {"nf4": 0, "fp4": 1, "int4": 2}
 
@@ -908,5 +1137,7 @@ __all__ = ["lib", "LIB_PATH", "EXPORTED", "NF4Error", "NF4Weight", "CNF4Weight",
            "Act8", "CAct8", "empty_act8", "qlora_act8_pack", "qlora_act8_unpack", "qlora_linear_bwd_act8",
            "qlora_workspace_bytes_act8", "workspace_act8", "qlora_rmsnorm_fwd", "qlora_rmsnorm_bwd",
            "AttnSeqs", "CAttnConfig", "CAttnTensor", "qlora_attn_fwd", "qlora_attn_bwd",
+           "Rope", "CRopeConfig", "qlora_rope_fwd", "qlora_rope_bwd", "Kv4", "CKv4", "empty_kv4", "qlora_kv4_write",
+           "qlora_kv4_read", "qlora_attn_kv4_fwd",
            "qlora_workspace_bytes", "nf4_storage_bytes", "nf4_codebook", "workspace",
            "empty_weight", "quantize_weight"]

@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqlora_nf4.so")
 SOURCES = ["quant.hip", "gemm.hip", "lora.hip", "skinny.hip", "merge.hip", "optim.hip", "variants.hip",
-           "act8.hip", "norm.hip", "attn.hip", "abi.hip"]
+           "act8.hip", "norm.hip", "attn.hip", "rope.hip", "kv4.hip", "attn_kv4.hip", "abi.hip"]
 ARCH = os.environ.get("NF4_OFFLOAD_ARCH", "gfx950")
 
 

@@ -5,9 +5,11 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "common.h"
@@ -680,6 +682,228 @@ int qlora_attn_bwd(const qlora_attn_config* cfg, int64_t count, const qlora_attn
   }
 }
 
+// ---- rotary positions and head norms
+namespace {
+
+int check_rope(const qlora_rope_config* c, const double* inv_freq) {
+  if (!c) return NF4_ERR_NULL;
+  if (c->heads < 1 || c->heads > 65535 || c->kv_heads < 0 || c->kv_heads > 65535) return NF4_ERR_SHAPE;
+  if (c->d < 8 || c->d > 128 || c->d % 8 || c->rot < 0 || c->rot > c->d || c->rot % 8) return NF4_ERR_SHAPE;
+  if (!(c->eps >= 0.f) || !isfinite(c->eps) || !isfinite(c->factor)) return NF4_ERR_SHAPE;
+  if (c->tokens < 0 || c->tokens > (int64_t(1) << 40)) return NF4_ERR_SHAPE;
+  if (c->tokens && c->rot) {
+    if (!inv_freq) return NF4_ERR_NULL;
+    for (int i = 0; i < c->rot / 2; ++i)
+      if (!isfinite(inv_freq[i])) return NF4_ERR_SHAPE;
+  }
+  return NF4_OK;
+}
+
+// q and k like tensors of a rope call; k is not looked at without key heads
+int check_rope_pair(const qlora_rope_config* c, const qlora_attn_tensor* q, const qlora_attn_tensor* k, bool output) {
+  const int st = check_attn_tensor(q, c->tokens, c->heads, c->d, output);
+  if (st || !c->kv_heads) return st;
+  return check_attn_tensor(k, c->tokens, c->kv_heads, c->d, output);
+}
+
+// turns a position, modulo one, in units of 2^-64
+uint64_t turn_of(double radians) {
+  constexpr long double pi2 = 6.283185307179586476925286766559L;
+  const long double t = (long double)radians / pi2;
+  const long double f = ldexpl(t - floorl(t), 64);
+  return f >= 18446744073709551616.0L ? 0 : (uint64_t)f;
+}
+
+nf4::AttnTensor rope_tensor(const qlora_attn_tensor* t) { return t ? attn_tensor(t) : nf4::AttnTensor{nullptr, 0, 0}; }
+
+nf4::RopeArgs rope_args(const qlora_rope_config* c, const double* inv_freq, const int64_t* positions,
+                        const qlora_attn_tensor* q, const qlora_attn_tensor* k, const uint16_t* qw, const uint16_t* kw) {
+  nf4::RopeArgs a{};
+  a.q = rope_tensor(q);
+  a.k = rope_tensor(k);
+  a.qw = qw;
+  a.kw = c->kv_heads ? kw : nullptr;
+  a.pos = positions;
+  a.tokens = c->tokens;
+  a.heads = c->heads;
+  a.kv_heads = c->kv_heads;
+  a.d = c->d;
+  a.rot = c->rot;
+  a.interleaved = c->interleaved != 0;
+  a.eps = c->eps;
+  a.factor = c->factor;
+  for (int i = 0; i < c->rot / 2; ++i) a.turn[i] = turn_of(inv_freq[i]);
+  return a;
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+}  // namespace
+
+int qlora_rope_fwd(const qlora_rope_config* cfg, const double* inv_freq, const int64_t* positions,
+                   const qlora_attn_tensor* q, const qlora_attn_tensor* k, const uint16_t* q_weight,
+                   const uint16_t* k_weight, const qlora_attn_tensor* q_out, const qlora_attn_tensor* k_out,
+                   hipStream_t stream) {
+  int st = check_rope(cfg, inv_freq);
+  if (st || (st = check_rope_pair(cfg, q, k, false)) || (st = check_rope_pair(cfg, q_out, k_out, true))) return st;
+  if (cfg->tokens == 0) return NF4_OK;
+  if (cfg->rot && !positions) return NF4_ERR_NULL;
+  if (!aligned8(positions) || !aligned16(q_weight) || !aligned16(k_weight)) return NF4_ERR_ALIGN;
+  nf4::RopeArgs a = rope_args(cfg, inv_freq, positions, q, k, q_weight, k_weight);
+  a.qo = rope_tensor(q_out);
+  a.ko = rope_tensor(k_out);
+  return from_hip(nf4::launch_rope_fwd(a, stream));
+}
+
+size_t qlora_rope_workspace_bytes(const qlora_rope_config* cfg) {
+  static const double none[64] = {};   // the sizes alone are checked
+  if (check_rope(cfg, none) || cfg->tokens == 0) return 0;
+  return align_up(nf4::rope_bwd_ws_floats(rope_args(cfg, none, nullptr, nullptr, nullptr, nullptr, nullptr)) * 4);
+}
+
+int qlora_rope_bwd(const qlora_rope_config* cfg, const double* inv_freq, const int64_t* positions,
+                   const qlora_attn_tensor* q, const qlora_attn_tensor* k, const uint16_t* q_weight,
+                   const uint16_t* k_weight, const qlora_attn_tensor* dq_out, const qlora_attn_tensor* dk_out,
+                   const qlora_attn_tensor* dq, const qlora_attn_tensor* dk, float* dq_weight, float* dk_weight,
+                   int accumulate, void* ws, size_t ws_bytes, hipStream_t stream) {
+  int st = check_rope(cfg, inv_freq);
+  if (st) return st;
+  const bool keys = cfg->kv_heads != 0;
+  if ((q_weight && (st = check_attn_tensor(q, cfg->tokens, cfg->heads, cfg->d, false))) ||
+      (k_weight && keys && (st = check_attn_tensor(k, cfg->tokens, cfg->kv_heads, cfg->d, false))) ||
+      (st = check_rope_pair(cfg, dq_out, dk_out, false)) || (st = check_rope_pair(cfg, dq, dk, true)))
+    return st;
+  if ((dq_weight && !q_weight) || (dk_weight && (!k_weight || !keys))) return NF4_ERR_NULL;
+  if (cfg->tokens == 0) return NF4_OK;
+  if (cfg->rot && !positions) return NF4_ERR_NULL;
+  if (!aligned8(positions) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(dq_weight) || !aligned16(dk_weight) ||
+      !aligned16(ws))
+    return NF4_ERR_ALIGN;
+  if ((dq_weight || dk_weight) && (!ws || ws_bytes < qlora_rope_workspace_bytes(cfg))) return NF4_ERR_WORKSPACE;
+  nf4::RopeArgs a = rope_args(cfg, inv_freq, positions, q, k, q_weight, k_weight);
+  a.qo = rope_tensor(dq_out);
+  a.ko = rope_tensor(dk_out);
+  a.dq = rope_tensor(dq);
+  a.dk = rope_tensor(dk);
+  return from_hip(nf4::launch_rope_bwd(a, dq_weight, dk_weight, accumulate, static_cast<float*>(ws), stream));
+}
+
+// ---- keys and values in 4 bits
+namespace {
+
+// One cache of `tokens` x `heads` rows of nb blocks; a written one's rows must not overlap.
+int check_kv4(const qlora_kv4* t, int64_t tokens, int heads, int nb, bool output) {
+  if (!t) return NF4_ERR_NULL;
+  if (t->codebook < Q4_CODEBOOK_NF4 || t->codebook > Q4_CODEBOOK_INT4) return NF4_ERR_SHAPE;
+  if (t->token_stride < nb || t->token_stride >= (int64_t(1) << 20)) return NF4_ERR_SHAPE;
+  if (t->head_stride < 0 || t->head_stride > (int64_t(1) << 40)) return NF4_ERR_SHAPE;
+  if (output && heads > 1) {
+    const bool tokens_outer = t->head_stride >= nb && t->token_stride >= t->head_stride * (heads - 1) + nb;
+    const bool heads_outer = tokens == 0 || t->head_stride >= t->token_stride * (tokens - 1) + nb;
+    if (!tokens_outer && !heads_outer) return NF4_ERR_SHAPE;
+  }
+  if (tokens == 0) return NF4_OK;
+  if (!t->codes || !t->absmax) return NF4_ERR_NULL;
+  return aligned16(t->codes) && (reinterpret_cast<uintptr_t>(t->absmax) & 1u) == 0 ? NF4_OK : NF4_ERR_ALIGN;
+}
+
+int kv4_blocks(int d) { return (d + 31) / 32; }
+
+int check_kv4_pair(const qlora_attn_config* c, const qlora_kv4* k4, const qlora_kv4* v4, bool output) {
+  const int nb = kv4_blocks(c->d);
+  int st = check_kv4(k4, c->k_tokens, c->kv_heads, nb, output);
+  if (st || (st = check_kv4(v4, c->k_tokens, c->kv_heads, nb, output))) return st;
+  if (k4->codebook != v4->codebook) return NF4_ERR_SHAPE;
+  if (output && c->k_tokens && (k4->codes == v4->codes || k4->absmax == v4->absmax)) return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+nf4::Kv4Tensor kv4_tensor(const qlora_kv4* t) { return nf4::Kv4Tensor{t->codes, t->absmax, t->token_stride, t->head_stride}; }
+
+int kv4_copy(bool write, const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs, const qlora_attn_tensor* k,
+             const qlora_attn_tensor* v, const qlora_kv4* k4, const qlora_kv4* v4, hipStream_t stream) {
+  int st = check_attn_config(cfg);
+  if (st || (st = check_attn_seqs(cfg, count, seqs, false))) return st;
+  if ((st = check_attn_tensor(k, cfg->q_tokens, cfg->kv_heads, cfg->d, !write)) ||
+      (st = check_attn_tensor(v, cfg->q_tokens, cfg->kv_heads, cfg->d, !write)) || (st = check_kv4_pair(cfg, k4, v4, write)))
+    return st;
+  const int nb = kv4_blocks(cfg->d);
+  for (int64_t i = 0; i < count; ++i) {
+    if (seqs[i].nq > seqs[i].nk) return NF4_ERR_SHAPE;
+    if ((seqs[i].nq * cfg->kv_heads * nb + 63) / 64 > nf4::kMaxThreads / 512) return NF4_ERR_SHAPE;
+  }
+  try {
+    if (write && count > 1) {   // two sequences that write the same token would leave either's blocks
+      std::vector<std::pair<int64_t, int64_t>> to;
+      to.reserve((size_t)count);
+      for (int64_t i = 0; i < count; ++i)
+        if (seqs[i].nq) to.emplace_back(seqs[i].k0 + seqs[i].nk - seqs[i].nq, seqs[i].k0 + seqs[i].nk);
+      std::sort(to.begin(), to.end());
+      for (size_t i = 1; i < to.size(); ++i)
+        if (to[i].first < to[i - 1].second) return NF4_ERR_SHAPE;
+    }
+    const std::vector<nf4::AttnSeq> s = attn_seqs(count, seqs);
+    nf4::Kv4Args a{attn_tensor(k), attn_tensor(v), kv4_tensor(k4), kv4_tensor(v4), cfg->kv_heads, cfg->d, nb, 0.f, {}};
+    nf4::kv4_codes(k4->codebook, a.t, &a.unit);
+    return from_hip(nf4::launch_kv4(a, k4->codebook, write, s.data(), count, stream));
+  } catch (...) {
+    return NF4_ERR_HIP;   // no host memory for the sequence list
+  }
+}
+
+// sequences whose rows, 32 to a workgroup, fit a launch
+int check_kv4_rows(const qlora_attn_config* c, int64_t count, const qlora_attn_seq* s) {
+  const int64_t G = c->heads / c->kv_heads;
+  for (int64_t i = 0; i < count; ++i)
+    if ((s[i].nq * G + 31) / 32 * c->kv_heads > nf4::kMaxThreads / 256) return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+}  // namespace
+
+int qlora_kv4_write(const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs, const qlora_attn_tensor* k,
+                    const qlora_attn_tensor* v, const qlora_kv4* k4, const qlora_kv4* v4, hipStream_t stream) {
+  return kv4_copy(true, cfg, count, seqs, k, v, k4, v4, stream);
+}
+
+int qlora_kv4_read(const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs, const qlora_kv4* k4,
+                   const qlora_kv4* v4, const qlora_attn_tensor* k, const qlora_attn_tensor* v, hipStream_t stream) {
+  return kv4_copy(false, cfg, count, seqs, k, v, k4, v4, stream);
+}
+
+size_t qlora_attn_kv4_workspace_bytes(const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs) {
+  if (check_attn_config(cfg) || check_attn_seqs(cfg, count, seqs, false) || count == 0 || check_kv4_rows(cfg, count, seqs)) return 0;
+  try {
+    const std::vector<nf4::AttnSeq> v = attn_seqs(count, seqs);
+    return align_up(nf4::attn_kv4_ws_floats(v.data(), count, cfg->heads, cfg->kv_heads, cfg->d, attn_window(cfg)) * 4);
+  } catch (...) {
+    return 0;
+  }
+}
+
+int qlora_attn_kv4_fwd(const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs, const qlora_attn_tensor* q,
+                       const qlora_kv4* k4, const qlora_kv4* v4, const qlora_attn_tensor* o, float* lse, void* ws,
+                       size_t ws_bytes, hipStream_t stream) {
+  int st = check_attn_config(cfg);
+  if (st || (st = check_attn_seqs(cfg, count, seqs, false)) || (st = check_kv4_rows(cfg, count, seqs))) return st;
+  if ((st = check_attn_tensor(q, cfg->q_tokens, cfg->heads, cfg->d, false)) || (st = check_kv4_pair(cfg, k4, v4, false)) ||
+      (st = check_attn_tensor(o, cfg->q_tokens, cfg->heads, cfg->d, true)))
+    return st;
+  if (!aligned16(lse) || !aligned16(ws)) return NF4_ERR_ALIGN;
+  try {
+    const std::vector<nf4::AttnSeq> s = attn_seqs(count, seqs);
+    const size_t need = nf4::attn_kv4_ws_floats(s.data(), count, cfg->heads, cfg->kv_heads, cfg->d, attn_window(cfg)) * 4;
+    if (need && (!ws || ws_bytes < need)) return NF4_ERR_WORKSPACE;
+    const nf4::AttnTensor none{nullptr, 0, 0};
+    nf4::AttnKv4Args a{{attn_tensor(q), none, none, attn_tensor(o), lse, cfg->q_tokens, cfg->heads, cfg->kv_heads, cfg->d,
+                        cfg->causal != 0, attn_window(cfg), cfg->scale * 1.4426950408889634f},
+                       kv4_tensor(k4), kv4_tensor(v4), kv4_blocks(cfg->d), 0.f, {}};
+    nf4::kv4_codes(k4->codebook, a.t, &a.unit);
+    return from_hip(nf4::launch_attn_kv4(a, k4->codebook, s.data(), count, static_cast<float*>(ws), stream));
+  } catch (...) {
+    return NF4_ERR_HIP;   // no host memory for the sequence list
+  }
+}
 
 int qlora_linear_fwd_noalloc(const nf4_weight* W, const uint16_t* x, int64_t M, const uint16_t* A,
                              const uint16_t* B, int32_t r, float scale, uint16_t* y, float* u_out,

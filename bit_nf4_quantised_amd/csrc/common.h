@@ -11,6 +11,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "launch.h"
+
 namespace nf4 {
 
 constexpr int kBlock = 64;     // values per absmax block
@@ -65,12 +67,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // (idx >= 8), sB = sA ^ 0x48 = idx - 8 (idx >= 8) or >= 0x48 (idx < 8).
 struct BlockLut {
   uint32_t lo[4], hi[4];
-};
-
-// The 16 values a 4-bit index selects (NF4, FP4 or INT4, ascending; a 15-value codebook repeats
-// its last value at index 15), passed to kernels by value in their arguments.
-struct Codes {
-  float v[16];
 };
 
 __device__ __forceinline__ BlockLut make_lut(float c1p, const float (&q)[16]) {

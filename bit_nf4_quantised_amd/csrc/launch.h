@@ -9,7 +9,11 @@ namespace nf4 {
 // A launch holds fewer than 2^32 threads.
 constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
 
-struct Codes;   // common.h
+// The 16 values a 4-bit index selects (NF4, FP4 or INT4, ascending; a 15-value codebook repeats
+// its last value at index 15), passed to kernels by value in their arguments.
+struct Codes {
+  float v[16];
+};
 
 hipError_t launch_quantize(const float* w, int64_t numel, uint8_t* packed, float* absmax,
                            hipStream_t stream);
@@ -223,6 +227,49 @@ hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t co
 void launch_attn_join(const AttnFwdArgs& a, const AttnSeqs& q, const AttnSplit& sp, hipStream_t stream);
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, const AttnSeq* seqs, int64_t count, int64_t q_tokens, float* ws,
                            hipStream_t stream);
+
+// ---- Rotary positions and head norms (rope.hip)
+struct RopeArgs {
+  AttnTensor q, k, qo, ko, dq, dk;   // forward: qo, ko from q, k; backward: dq, dk from the gradients qo, ko (and q, k)
+  const uint16_t *qw, *kw;           // [d] or null: not normed
+  const int64_t* pos;                // [tokens]
+  int64_t tokens;
+  int heads, kv_heads, d, rot, interleaved;
+  float eps, factor;
+  uint64_t turn[64];                 // the pairs' frequencies, in 2^-64 turns a position
+};
+hipError_t launch_rope_fwd(const RopeArgs& a, hipStream_t stream);
+// dqw, dkw: [d] or null; part holds rope_bwd_ws_floats floats where one is asked for
+size_t rope_bwd_ws_floats(const RopeArgs& a);
+hipError_t launch_rope_bwd(const RopeArgs& a, float* dqw, float* dkw, int accumulate, float* part, hipStream_t stream);
+
+// ---- Keys and values in 4 bits (kv4.hip, attn_kv4.hip; format in kv4.h). Block b of (token, head) is block
+// token * token + head * head + b of the arrays.
+struct Kv4Tensor {
+  uint8_t* codes;
+  uint16_t* absmax;
+  int64_t token, head;
+};
+struct Kv4Args {
+  AttnTensor k, v;
+  Kv4Tensor k4, v4;
+  int kv_heads, d, nb;
+  float unit;
+  Codes t;
+};
+struct AttnKv4Args {
+  AttnFwdArgs f;                     // k and v unused
+  Kv4Tensor k4, v4;
+  int nb;
+  float unit;
+  Codes t;
+};
+// the values that a nibble selects and one over the largest; false for an unknown codebook
+bool kv4_codes(int book, Codes& t, float* unit);
+// every sequence's last nq tokens: k and v into the cache, or the cache into k and v
+hipError_t launch_kv4(const Kv4Args& a, int book, bool write, const AttnSeq* seqs, int64_t count, hipStream_t stream);
+size_t attn_kv4_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window);
+hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream);
 
 // ---- 8-bit activation checkpoints (act8.hip; format in act8.h). numel a multiple of 64.
 hipError_t launch_act8_pack(const uint16_t* x, int64_t numel, int8_t* codes, uint16_t* absmax, hipStream_t stream);

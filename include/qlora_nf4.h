@@ -18,8 +18,9 @@
  *                     such a merged weight again.
  *   qlora_adamw_plan_*   sections "The algorithm, step by step" and "Minimal implementation":
  *                     global gradient-norm clipping, then AdamW over A and B.
- *   qlora_act8_*, qlora_linear_bwd_act8, qlora_rmsnorm_*, qlora_attn_*   what a layer runs around its
- *                     adapted linears: 8-bit activation checkpoints, the norm and the attention.
+ *   qlora_act8_*, qlora_linear_bwd_act8, qlora_rmsnorm_*, qlora_rope_*, qlora_kv4_*, qlora_attn_*   what a
+ *                     layer runs around its adapted linears: 8-bit activation checkpoints, the norm,
+ *                     positions, a key/value cache in 4 bits and the attention.
  *   q4_*              sections "A toy run" and "Double quantisation": FP4 and INT4 codebooks,
  *                     blocksizes 16..4096, and fp32 scales without double quantisation.
  *
@@ -461,6 +462,97 @@ int qlora_attn_bwd(const qlora_attn_config *cfg, int64_t count, const qlora_attn
 /* Workspace bytes of qlora_attn_fwd (backward 0) or qlora_attn_bwd (1); 0 for refused arguments. */
 size_t qlora_attn_workspace_bytes(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs,
                                   int backward);
+
+/* ---- Rotary positions of query and key heads, with norms of the heads in the same pass (bf16 in and out,
+ * fp32 inside, each output rounded once). Per token and head a row x of d values:
+ *   z = x rsqrt(mean(x^2) + eps) weight, or z = x without a weight;
+ *   the first `rot` features of z in pairs (a, b): (2 i, 2 i + 1) when interleaved, else (i, i + rot / 2), turned
+ *   by the angle t = position * inv_freq[i]:
+ *     y_a = factor (z_a cos t - z_b sin t),  y_b = factor (z_b cos t + z_a sin t);  the others y = z.
+ * The angle is formed modulo a turn from 64-bit fractions of turns, so far positions lose nothing. */
+typedef struct {
+  int32_t heads, kv_heads;   /* rows a token in q and in k: 1..65535, and 0..65535 (0: no k) */
+  int32_t d;                 /* head size: a multiple of 8 in 8..128 */
+  int32_t rot;               /* rotated features: a multiple of 8 in 0..d */
+  int32_t interleaved;
+  float eps;                 /* >= 0 */
+  float factor;              /* on the rotated features, finite; 1 for most models */
+  int64_t tokens;            /* 0: a no-op */
+} qlora_rope_config;
+/* Forward.
+ *   inv_freq     HOST array of rot / 2 angles a position, in radians, finite (may be NULL with rot 0).
+ *   positions    [tokens] int64, of any sign; may be NULL with rot 0.
+ *   q, k         [tokens][heads][d] and [tokens][kv_heads][d] (qlora_attn_tensor: strided); k may be NULL without
+ *                key heads. q_out and k_out may be their inputs' memory with the same strides; apart from that
+ *                outputs overlap neither inputs nor each other.
+ *   q_weight, k_weight   [d] bf16 or NULL: those heads are not normed.
+ * Errors: NF4_ERR_SHAPE, NF4_ERR_NULL, NF4_ERR_ALIGN, NF4_ERR_HIP. */
+int qlora_rope_fwd(const qlora_rope_config *cfg, const double *inv_freq, const int64_t *positions,
+                   const qlora_attn_tensor *q, const qlora_attn_tensor *k, const uint16_t *q_weight,
+                   const uint16_t *k_weight, const qlora_attn_tensor *q_out, const qlora_attn_tensor *k_out,
+                   hipStream_t stream);
+/* Backward: with g the gradients dq_out, dk_out of the outputs turned back (and times factor) and
+ * n = x rsqrt(mean(x^2) + eps),
+ *   dq, dk = rsqrt(mean(x^2) + eps) (weight g - n mean(weight g n)), or g without a weight;
+ *   dq_weight, dk_weight [d] float = sum over tokens and heads of g n, or NULL (a frozen weight);
+ *     accumulate adds into them.
+ *   q, k: the forward's inputs; read, and needed, only where the heads are normed (else they may be NULL).
+ *   dq and dk may be the memory of dq_out and dk_out, or of q and k, with the same strides.
+ *   ws: with dq_weight or dk_weight, at least qlora_rope_workspace_bytes(cfg) bytes.
+ * The sums run in a fixed order. Errors: as the forward; NF4_ERR_NULL also for a weight's gradient without the
+ * weight; NF4_ERR_WORKSPACE. */
+int qlora_rope_bwd(const qlora_rope_config *cfg, const double *inv_freq, const int64_t *positions,
+                   const qlora_attn_tensor *q, const qlora_attn_tensor *k, const uint16_t *q_weight,
+                   const uint16_t *k_weight, const qlora_attn_tensor *dq_out, const qlora_attn_tensor *dk_out,
+                   const qlora_attn_tensor *dq, const qlora_attn_tensor *dk, float *dq_weight, float *dk_weight,
+                   int accumulate, void *ws, size_t ws_bytes, hipStream_t stream);
+size_t qlora_rope_workspace_bytes(const qlora_rope_config *cfg);   /* 0 for refused sizes */
+
+/* ---- A key/value cache in 4 bits: 0.5625 bytes a value instead of 2. Format of one row (a token's key or value
+ * head, d values): nb = ceil(d / 32) blocks of 32 values, the last filled up with zeros;
+ *   absmax  uint16: bf16 bits of the block's largest magnitude (exact, as the values are bf16);
+ *   codes   16 bytes, byte j holding value 2j in its high nibble and value 2j+1 in its low nibble: the code
+ *           nearest to the exact quotient x / absmax, ties to the lower value. The codebooks:
+ *             Q4_CODEBOOK_NF4   t = the 16 NF4 codes, ascending; largest 1;
+ *             Q4_CODEBOOK_INT4  t = -7..7 for nibbles 0..14; largest 7;
+ *             Q4_CODEBOOK_FP4   t = the values of the E2M1 bit patterns (sign, two bits of exponent, one of mantissa),
+ *                               not the ascending indices of a weight; largest 6. -0 is not written.
+ *           x / absmax * largest is what t is nearest to.
+ * A code stands for bf16_rne(fl32(t * fl32(absmax * fl32(1 / largest)))).
+ * NaN and Inf are allowed: a block that holds one keeps the largest magnitude's bits (a NaN before an Inf) and the
+ * codes of zero, and stands for NaN throughout.
+ * Block b of (token, head) is block token * token_stride + head * head_stride + b of both arrays, 16 bytes of
+ * codes and one absmax each. Strides in blocks: nb <= token_stride < 2^20, 0 <= head_stride <= 2^40; caches with
+ * the tokens or the heads outermost both fit (heads outermost reads fastest). */
+typedef struct {
+  uint8_t *codes;       /* 16-byte aligned */
+  uint16_t *absmax;     /* 2-byte aligned */
+  int64_t token_stride, head_stride;
+  int32_t codebook;     /* Q4_CODEBOOK_* */
+} qlora_kv4;
+
+/* New keys and values into a cache, or rows of a cache back to bf16, for the sequences of a batch (HOST array of
+ * count entries as qlora_attn_fwd takes them, so one list serves the write and the attention that follows): the last
+ * nq of a sequence's nk keys, cache tokens k0 + nk - nq .. k0 + nk - 1, from or to tokens q0 .. q0 + nq - 1 of k
+ * and v. A cache read whole has nq = nk. cfg: kv_heads, d, q_tokens (of k and v) and k_tokens (of the cache) are
+ * used; the rest is checked as for qlora_attn_fwd. k4 and v4 have the same codebook.
+ * Of one sequence ceil(nq * kv_heads * nb / 64) is below 2^23.
+ * Errors: as qlora_attn_fwd; NF4_ERR_SHAPE also for nq > nk and, when writing, for two sequences that would write
+ * the same cache token, a cache whose rows overlap, and k4 and v4 in the same memory. */
+int qlora_kv4_write(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs, const qlora_attn_tensor *k,
+                    const qlora_attn_tensor *v, const qlora_kv4 *k4, const qlora_kv4 *v4, hipStream_t stream);
+int qlora_kv4_read(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs, const qlora_kv4 *k4,
+                   const qlora_kv4 *v4, const qlora_attn_tensor *k, const qlora_attn_tensor *v, hipStream_t stream);
+
+/* Attention over a cache in 4 bits: qlora_attn_fwd over the bf16 values that k4 and v4 stand for, which are never
+ * written to memory. All its rules hold (masks, windows, rows without keys, lse); moreover a NaN in a key or in a
+ * value reaches exactly the queries that see it, and gives NaN in their o and lse.
+ *   ws    at least qlora_attn_kv4_workspace_bytes(cfg, count, seqs) bytes (0: may be NULL).
+ * Of one sequence ceil(nq * heads / kv_heads / 32) * kv_heads is below 2^24. Errors: as qlora_attn_fwd. */
+int qlora_attn_kv4_fwd(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs, const qlora_attn_tensor *q,
+                       const qlora_kv4 *k4, const qlora_kv4 *v4, const qlora_attn_tensor *o, float *lse, void *ws,
+                       size_t ws_bytes, hipStream_t stream);
+size_t qlora_attn_kv4_workspace_bytes(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs);
 
 /* Workspace bytes that qlora_linear_fwd and qlora_linear_bwd need for these sizes (the larger of
  * the two). Returns 0 for invalid sizes. */

@@ -23,6 +23,7 @@ from .linear import linear_fwd, linear_bwd, linear_fwd_f64, linear_bwd_f64, line
 from .merge import bf16_bits_from_f64, merge
 from .optim import AdamWConfig, global_grad_norm, clip_coefficient, adamw_step
 from .layer import (visible, attention_head, attention, rmsnorm, rmsnorm_bwd, act8, act8_values)
+from .heads import (rope_turn, head_norm, rope_fwd, rope_bwd, kv4_book, kv4, kv4_values)
 from .toy import int4_codebook, fp4_codebook, relative_mse, residual_capture
 
 __all__ = [
@@ -33,4 +34,5 @@ __all__ = [
     "global_grad_norm", "clip_coefficient", "adamw_step", "int4_codebook",
     "visible", "attention_head", "attention", "rmsnorm", "rmsnorm_bwd", "act8", "act8_values",
     "fp4_codebook", "relative_mse", "residual_capture",
+    "rope_turn", "head_norm", "rope_fwd", "rope_bwd", "kv4_book", "kv4", "kv4_values",
 ]

@@ -681,9 +681,11 @@ def _attn_tensors(*pairs):
             _dtype(t, *_BF16)
         if not t.is_cuda:
             raise ValueError("tensor must live on the GPU")
-        if t.shape != shape or len(shape) != 3 or t.stride(2) != 1:
+        if t.shape != shape or len(shape) != 3:
             raise ValueError("shape mismatch: attention tensors are [tokens, heads, d] with d contiguous")
-        token, head, _ = t.stride()
+        token, head, one = t.stride()
+        if one != 1:
+            raise ValueError("shape mismatch: attention tensors are [tokens, heads, d] with d contiguous")
         tokens, heads, d = shape
         # the stride of a single head or token carries no meaning: give it a valid value
         if heads <= 1:

@@ -1,92 +1,167 @@
 // Attention over a key/value cache in 4 bits (gfx950): as attention over the bf16 values that its blocks stand
 // for (kv4.h), which exist only in registers and LDS.
 //
-// Scores, softmax and sums are those of attn.hip: 32 x 32 products, streamed keys as result rows and query rows as
-// result columns, fp32 statistics, probabilities rounded to bf16 where they enter the second product (2^-8). The query
-// heads that share a key head are packed with the tokens into rows (row = token * group + head in group), 32 rows
-// a workgroup; its keys are one range of the sequence's, and its 4 waves take 32-key tiles of that range in turn.
-//
-// A lane holds one key of the tile and, of its row, the blocks 2 b + h (h the lane's half of the wave): 16 bytes of codes
-// and a scale each, for the key and for the value. The keys' blocks, dequantised, are the first product's operand as
-// they are (its contraction runs over d in that order, and the queries are loaded in the same); the values' go
-// through an LDS tile of the wave's own, from which they are read across with transpose loads. The codes of the
-// next tile are on their way while a tile is worked on; there are no barriers until the waves are joined.
+// Scores, softmax and sums are those of attn.hip: streamed keys as result rows and query rows as result columns of the
+// first product, fp32 statistics, probabilities rounded to bf16 where they enter the second product (2^-8). The query
+// heads that share a key head are packed with the tokens into rows (row = token * group + head in group), so a block is
+// dequantised for all of them. Blocks are dequantised in the order of Kv4Table::eight(); the queries are put
+// in the same order, and the output's columns back into theirs.
 //
 // A value block that stands for NaN enters as zeros, and the same block of its key as NaN: a query that sees the
 // key gets NaN through the score, and one that does not gets nothing of it (0 times NaN would be NaN).
+//
+// Keys of a range that end within a tile: the lanes past it take the last key again, which the mask hides.
 #include "attn.h"
 #include "kv4.h"
 
 namespace nf4 {
 
-// A lane's blocks of one tile, as they lie in the cache.
-template <int NB>
-struct Kv4Blocks {
-  u32x4 k[NB], v[NB];
-  uint32_t ka[NB], va[NB];
-};
+__device__ __forceinline__ bool kv4_lost(uint32_t absmax) { return absmax >= kBf16Infinity; }   // absmax has no sign
+constexpr uint32_t kBf16Nan = 0x7FC0u;
 
+// ------------------------------------------------------------------------------------------
+// Few rows: 16 NR rows a workgroup, its keys one range of the sequence's, of which its NW waves take 32-key tiles in
+// turn; there are no barriers until the waves are joined. Products are v_mfma_f32_16x16x32_bf16: lane (n, q) = (lane
+// % 16, lane / 16) holds of a result column n and rows 4 q .. 4 q + 3, of an operand row (or column) n and 8 values.
+// The contraction of the first product may run over d in any order, so lane (n, q) takes the block q (d <= 64: half
+// the block q / 2) of keys n and 16 + n as it lies in the cache, 16 bytes, and its dequantised dwords are the
+// operand. Values go through an LDS tile of the wave's own, from which transpose loads read them across.
 template <int DP>
-struct Kv4Wave {
-  static constexpr int BN = 32, KS = DP / 16, DT = DP / 32, NB = DP / 64;
-  typedef Tile<DP> T;
-  bf16x8 qf[KS];
-  Online<DT> acc;
-  Range mine, first, last;   // keys that the lane's row, the tile's first and its last row see
-  float c, slack;
-  int lane;
-
-  // The tile of keys from j0; keys from `end` on repeat the last one (they are hidden), blocks past the
-  // row's repeat its last (their queries are zero, and their columns of the output are not stored).
-  __device__ __forceinline__ void load(Kv4Blocks<NB>& x, const AttnKv4Args& a, int64_t kbase, int64_t vbase, int j0, int end) const {
-    const int key = min(lane & 31, end - 1 - j0), h = lane >> 5;
-    const int64_t kt = kbase + (int64_t)j0 * a.k4.token, vt = vbase + (int64_t)j0 * a.v4.token;
+struct Kv4Few;
+// d > 64: lane (n, q) holds block q of keys n and 16 + n, key and value
+template <>
+struct Kv4Few<128> {
+  u32x4 k[2], v[2];
+  uint32_t ka[2], va[2];
+  __device__ __forceinline__ void load(const AttnKv4Args& a, int64_t kt, int64_t vt, int last, int lane) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t at = (uint32_t)min(2 * b + h, a.nb - 1);
-      const uint32_t ko = (uint32_t)key * (uint32_t)a.k4.token + at, vo = (uint32_t)key * (uint32_t)a.v4.token + at;
-      x.k[b] = *reinterpret_cast<const u32x4*>(a.k4.codes + 16 * kt + 16u * ko);
-      x.v[b] = *reinterpret_cast<const u32x4*>(a.v4.codes + 16 * vt + 16u * vo);
-      x.ka[b] = a.k4.absmax[kt + ko];
-      x.va[b] = a.v4.absmax[vt + vo];
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t key = (uint32_t)min(16 * i + (lane & 15), last), b = (uint32_t)min(lane >> 4, a.nb - 1);
+      const uint32_t ko = key * (uint32_t)a.k4.token + b, vo = key * (uint32_t)a.v4.token + b;
+      k[i] = *reinterpret_cast<const u32x4*>(a.k4.codes + 16 * kt + 16u * ko);
+      v[i] = *reinterpret_cast<const u32x4*>(a.v4.codes + 16 * vt + 16u * vo);
+      ka[i] = a.k4.absmax[kt + ko];
+      va[i] = a.v4.absmax[vt + vo];
     }
   }
+  __device__ __forceinline__ float step(int i, float unit) const { return kv4_step(kv4_lost(va[i]) ? kBf16Nan : ka[i], unit); }
+  template <class Deq>
+  __device__ __forceinline__ void values(uint16_t* tile, const AttnKv4Args& a, int lane) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const Deq q(a.t, kv4_step(kv4_lost(va[i]) ? 0u : va[i], a.unit));
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        *reinterpret_cast<u32x4*>(tile + Tile<128>::elem(16 * i + (lane & 15), 4 * (lane >> 4) + t)) = q.eight(v[i][t]);
+    }
+  }
+  // column of the lane's 8 values of the first product's step t
+  static __device__ __forceinline__ int column(int t, int lane) { return 32 * (lane >> 4) + 8 * t; }
+};
+// d <= 64: half the block q / 2 of keys n and 16 + n, and block lane / 32 of value lane % 32
+template <>
+struct Kv4Few<64> {
+  u32x2 k[2];
+  u32x4 v;
+  uint32_t ka[2], kva[2], va;
+  __device__ __forceinline__ void load(const AttnKv4Args& a, int64_t kt, int64_t vt, int last, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t key = (uint32_t)min(16 * i + (lane & 15), last), b = (uint32_t)min(lane >> 5, a.nb - 1);
+      const uint32_t ko = key * (uint32_t)a.k4.token + b;
+      k[i] = *reinterpret_cast<const u32x2*>(a.k4.codes + 16 * kt + (16u * ko + 8u * ((uint32_t)lane >> 4 & 1u)));
+      ka[i] = a.k4.absmax[kt + ko];
+      kva[i] = a.v4.absmax[vt + (key * (uint32_t)a.v4.token + b)];
+    }
+    const uint32_t vo = (uint32_t)min(lane & 31, last) * (uint32_t)a.v4.token + (uint32_t)min(lane >> 5, a.nb - 1);
+    v = *reinterpret_cast<const u32x4*>(a.v4.codes + 16 * vt + 16u * vo);
+    va = a.v4.absmax[vt + vo];
+  }
+  __device__ __forceinline__ float step(int i, float unit) const { return kv4_step(kv4_lost(kva[i]) ? kBf16Nan : ka[i], unit); }
+  template <class Deq>
+  __device__ __forceinline__ void values(uint16_t* tile, const AttnKv4Args& a, int lane) const {
+    const Deq q(a.t, kv4_step(kv4_lost(va) ? 0u : va, a.unit));
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      *reinterpret_cast<u32x4*>(tile + Tile<64>::elem(lane & 31, 4 * (lane >> 5) + t)) = q.eight(v[t]);
+  }
+  static __device__ __forceinline__ int column(int t, int lane) { return 16 * (lane >> 4) + 8 * t; }
+};
 
-  // x: the tile of keys from j0; vt: the wave's tile in LDS
-  __device__ __forceinline__ void tile(const Kv4Blocks<NB>& x, const AttnKv4Args& a, uint16_t* vt, int j0) {
-    f32x16 sc[1];
-    sc[0] = zero16();
-    const int h = lane >> 5;
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// maximum and sum over the four lanes of a column, in all of them
+__device__ __forceinline__ float quarter_max(float v) {
+  v = half_max(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float quarter_sum(float v) {
+  v = half_sum(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// the operand whose rows are tile columns 16 dt .. 16 dt + 15 and whose contraction runs over 32 tile rows in the order of
+// two 16-row score accumulators: lane quarter q takes rows 4 q .. 4 q + 3, then 16 + 4 q .. 16 + 4 q + 3
+template <int DP>
+__device__ __forceinline__ bf16x8 cols16(const uint16_t* t, int dt, int lane) {
+  const int j = lane & 15, m = 4 * (lane >> 4) + (j >> 2), c = 2 * dt + ((j & 3) >> 1);
+  const uint16_t* base = t + 4 * (j & 1);
+  bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(base + Tile<DP>::elem(m, c)));
+  bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(base + Tile<DP>::elem(m + 16, c)));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Running softmax of 16 rows (one per lane column) over 32 streamed keys a step, as Online.
+template <int DT>
+struct Online16 {
+  float m, mc, l;
+  f32x4 o[DT];
+  __device__ __forceinline__ void init() {
+    m = -INFINITY;
+    mc = 0.f;
+    l = 0.f;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const bool lost = x.va[b] >= kBf16Infinity;   // absmax has no sign
-      const Kv4Table kt(a.t, kv4_step(lost ? 0x7FC0u : x.ka[b], a.unit)), vv(a.t, kv4_step(lost ? 0u : x.va[b], a.unit));
+    for (int i = 0; i < DT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  __device__ __forceinline__ void update(f32x4 (&s)[2], float c, float slack) {
+    float mx = -INFINITY;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        sc[0] = mfma(__builtin_bit_cast(bf16x8, kt.eight(x.k[b][t])), qf[4 * b + t], sc[0]);
-        *reinterpret_cast<u32x4*>(vt + T::elem(lane & 31, 4 * (2 * b + h) + t)) = vv.eight(x.v[b][t]);
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[t][i]);
+    mx = quarter_max(mx);
+    if (__any(mx > m + slack)) {
+      const float mn = fmaxf(m, mx);
+      const float mnc = mn == -INFINITY ? 0.f : mn * c;
+      const float a = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mc - mnc);   // no key yet: l and o are zero
+      m = mn;
+      mc = mnc;
+      l *= a;
+#pragma unroll
+      for (int k = 0; k < DT; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[k][i] *= a;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[t][i] = __builtin_amdgcn_exp2f(__fmaf_rn(s[t][i], c, -mc));
+        l += s[t][i];
       }
-    }
-    // some row does not see some key
-    if (j0 + BN > first.hi || j0 < last.lo) hide(sc[0], mine, j0, lane, -INFINITY);
-    acc.update(sc, c, slack);
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const bf16x8 p = pack8(sc[0], kk);
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) acc.o[dt] = mfma(T::cols(vt, 16 * kk, dt, lane), p, acc.o[dt]);
-    }
   }
 };
 
-template <int DP>
-__global__ __launch_bounds__(256, 2) void attn_kv4_kernel(const AttnKv4Args a, const AttnSeqs sq, const AttnSplit sp) {
-  typedef Kv4Wave<DP> Wave;
-  constexpr int BN = Wave::BN, DT = Wave::DT, KS = Wave::KS, P = 33;
-  // the waves' tiles of values, later their outputs as [wave][d][32 rows]
-  __shared__ __attribute__((aligned(16))) float lds[4 * DP * P];
-  __shared__ float Ms[4][32], Ls[4][32];
-  static_assert(4 * BN * DP * 2 <= (int)sizeof(lds), "the tiles fit");
+template <int DP, class Deq, int NW, int NR>
+__global__ __launch_bounds__(NW * 64, NR == 1 ? 4 : 2) void attn_kv4_few_kernel(const AttnKv4Args a, const AttnSeqs sq, const AttnSplit sp) {
+  constexpr int BN = 32, KS = DP / 32, DT = DP / 16, R = 16 * NR, P = DP + 4;
+  typedef Kv4Few<DP> Blocks;
+  // a wave's tile of values, later its outputs as [row][d + 4]
+  __shared__ __attribute__((aligned(16))) float lds[NW][R * P];
+  __shared__ float Ms[NW][R], Ls[NW][R];
+  static_assert(BN * DP * 2 <= R * P * 4, "the tile fits");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = a.f.heads / a.f.kv_heads;
@@ -96,184 +171,433 @@ __global__ __launch_bounds__(256, 2) void attn_kv4_kernel(const AttnKv4Args a, c
   const int si = at_seq.index, local = u.tile - at_seq.first;
   const int ns = sp.nsplit[si], split = local % ns, rt = local / ns;
   const int shift = s.nk - s.nq, rows = s.nq * G;
-  const int row = rt * 32 + (lane & 31);
-  const int tok = min(row, rows - 1) / G, head = u.kvh * G + min(row, rows - 1) % G;
-  const int t0 = rt * 32 / G, t1 = min(rows - 1, rt * 32 + 31) / G;   // tokens of the row tile
-  Wave w;
-  w.first = visible(t0 + shift, s.nk, a.f.causal, a.f.window);
-  w.last = visible(t1 + shift, s.nk, a.f.causal, a.f.window);
-  w.mine = visible(tok + shift, s.nk, a.f.causal, a.f.window);
-  w.lane = lane;
+  const int t0 = rt * R / G, t1 = min(rows - 1, rt * R + R - 1) / G;   // tokens of the row tile
+  const Range first = visible(t0 + shift, s.nk, a.f.causal, a.f.window), last = visible(t1 + shift, s.nk, a.f.causal, a.f.window);
   // tiles are counted from the first key that the sequence's first row sees (none before it is read)
   const int lo = sp.lo[si];
-  const int k_lo = lo + max((w.first.lo - lo) & ~(BN - 1), split * sp.chunk);
-  const int k_hi = min(w.last.hi, lo + (split + 1) * sp.chunk);
+  const int k_lo = lo + max((first.lo - lo) & ~(BN - 1), split * sp.chunk);
+  const int k_hi = min(last.hi, lo + (split + 1) * sp.chunk);
   const int64_t kbase = s.k0 * a.k4.token + (int64_t)u.kvh * a.k4.head, vbase = s.k0 * a.v4.token + (int64_t)u.kvh * a.v4.head;
-  const int j_w = k_lo + wave * BN;   // the wave's first tile; its tiles are 4 apart
-  Kv4Blocks<Wave::NB> now, next;
-  if (j_w < k_hi) w.load(now, a, kbase, vbase, j_w, k_hi);
-  {
+  const int j_w = k_lo + wave * BN;   // the wave's first tile; its tiles are NW apart
+  Blocks now, next;
+  if (j_w < k_hi) now.load(a, kbase + (int64_t)j_w * a.k4.token, vbase + (int64_t)j_w * a.v4.token, k_hi - 1 - j_w, lane);
+
+  bf16x8 qf[NR][KS];
+  Range mine[NR];   // keys that the lane's rows see
+  Online16<DT> acc[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const int row = rt * R + 16 * r + (lane & 15);
+    const int tok = min(row, rows - 1) / G, head = u.kvh * G + min(row, rows - 1) % G;
+    mine[r] = visible(tok + shift, s.nk, a.f.causal, a.f.window);
     const uint16_t* q = a.f.q.p + (s.q0 + tok) * a.f.q.token + (int64_t)head * a.f.q.head;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int col = 64 * (ks >> 2) + 32 * (lane >> 5) + 8 * (ks & 3);
+    for (int t = 0; t < KS; ++t) {
+      const int col = Blocks::column(t, lane);
       u32x4 v = u32x4{0u, 0u, 0u, 0u};
       if (row < rows && col < a.f.d) v = *reinterpret_cast<const u32x4*>(q + col);
-      w.qf[ks] = __builtin_bit_cast(bf16x8, v);
+      qf[r][t] = __builtin_bit_cast(bf16x8, kv4_order(v));
     }
+    acc[r].init();
   }
-  w.acc.init();
-  w.c = a.f.c;
-  w.slack = slack_of(a.f.c);
-  uint16_t* const vt = reinterpret_cast<uint16_t*>(lds) + wave * BN * DP;
-  for (int j = j_w; j < k_hi; j += 4 * BN) {
-    if (j + 4 * BN < k_hi) w.load(next, a, kbase, vbase, j + 4 * BN, k_hi);
-    w.tile(now, a, vt, j);
+  const float slack = slack_of(a.f.c);
+  uint16_t* const vt = reinterpret_cast<uint16_t*>(lds[wave]);
+
+  for (int j = j_w; j < k_hi; j += NW * BN) {
+    const int jn = j + NW * BN;
+    if (jn < k_hi) next.load(a, kbase + (int64_t)jn * a.k4.token, vbase + (int64_t)jn * a.v4.token, k_hi - 1 - jn, lane);
+    f32x4 sc[NR][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const Deq kq(a.t, now.step(i, a.unit));
+#pragma unroll
+      for (int t = 0; t < KS; ++t) {
+        const bf16x8 kf = __builtin_bit_cast(bf16x8, kq.eight(now.k[i][t]));
+#pragma unroll
+        for (int r = 0; r < NR; ++r) sc[r][i] = mfma16(kf, qf[r][t], t ? sc[r][i] : f32x4{0.f, 0.f, 0.f, 0.f});
+      }
+    }
+    now.template values<Deq>(vt, a, lane);
+    // some row does not see some key
+    if (j + BN > first.hi || j < last.lo) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int key = j + 16 * (i >> 2) + 4 * (lane >> 4) + (i & 3);
+          if (key < mine[r].lo || key >= mine[r].hi) sc[r][i >> 2][i & 3] = -INFINITY;
+        }
+    }
+    bf16x8 p[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      acc[r].update(sc[r], a.f.c, slack);
+      p[r] = __builtin_bit_cast(bf16x8, u32x4{pack_bf16x2(sc[r][0][0], sc[r][0][1]), pack_bf16x2(sc[r][0][2], sc[r][0][3]),
+                                              pack_bf16x2(sc[r][1][0], sc[r][1][1]), pack_bf16x2(sc[r][1][2], sc[r][1][3])});
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      const bf16x8 vf = cols16<DP>(vt, dt, lane);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) acc[r].o[dt] = mfma16(vf, p[r], acc[r].o[dt]);
+    }
     now = next;
   }
-  Online<DT>& acc = w.acc;
 
-  // join the waves: the common maximum, then the scaled sums, added in wave order
-  float l = half_sum(acc.l);
-  if (lane < 32) {
-    Ms[wave][lane] = acc.m;
-    Ls[wave][lane] = l;
+  // join the waves: each leaves its statistics and sums, which are scaled to the common maximum and added in wave order
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const float l = quarter_sum(acc[r].l);
+    const int at = 16 * r + (lane & 15);
+    if (lane < 16) {
+      Ms[wave][at] = acc[r].m;
+      Ls[wave][at] = l;
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<f32x4*>(&lds[wave][at * P + 16 * dt + 4 * (lane >> 4)]) = acc[r].o[dt];
   }
   __syncthreads();
-  const int col = lane & 31;
-  float mx = -INFINITY;
+  constexpr int E = NW == 4 ? 8 : 2;   // columns a thread
+  for (int x = tid; x < R * (DP / E); x += NW * 64) {
+    const int row = x / (DP / E), c0 = x % (DP / E) * E, grow = rt * R + row;
+    if (grow >= rows) break;
+    float mx = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) mx = fmaxf(mx, Ms[k][col]);
-  const float mxc = mx == -INFINITY ? 0.f : mx * a.f.c;
-  l = 0.f;
+    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, Ms[w][row]);
+    const float mxc = mx == -INFINITY ? 0.f : mx * a.f.c;
+    float l = 0.f, v[E];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float f = Ms[k][col] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(Ms[k][col] * a.f.c - mxc);
-    l += Ls[k][col] * f;   // 0 times NaN stays NaN
-  }
-  const float f = acc.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(acc.mc - mxc);
-  float* const buf = lds + wave * (DP * P);
+    for (int e = 0; e < E; ++e) v[e] = 0.f;
 #pragma unroll
-  for (int dt = 0; dt < DT; ++dt)
+    for (int w = 0; w < NW; ++w) {
+      const float f = Ms[w][row] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(Ms[w][row] * a.f.c - mxc);
+      l += Ls[w][row] * f;   // 0 times NaN stays NaN
 #pragma unroll
-    for (int i = 0; i < 16; ++i) buf[(32 * dt + acc_row(i, lane)) * P + col] = acc.o[dt][i] * f;
-  __syncthreads();
-  // thread: row tid / 8, columns 8 (tid % 8) + 64 k
-  const int orow = tid >> 3, grow = rt * 32 + orow;
-  const float rl = __shfl(l, orow), rm = __shfl(mxc, orow);   // the row's statistics, as lane `orow` holds them
-  if (grow >= rows) return;
-  const int otok = grow / G, ohead = u.kvh * G + grow % G;
-  float* const part = sp.part + (sp.row0[si] + ((int64_t)grow * a.f.kv_heads + u.kvh) * ns + split) * (int64_t)(a.f.d + 8);
-#pragma unroll
-  for (int k = 0; k < DP / 64; ++k) {
-    const int c0 = 8 * (tid & 7) + 64 * k;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[e] = 0.f;
-#pragma unroll
-      for (int k2 = 0; k2 < 4; ++k2) v[e] += lds[k2 * (DP * P) + (c0 + e) * P + orow];
+      for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(lds[w][row * P + (c0 & ~7) + kv4_place_of((c0 & 7) + e)], f, v[e]);
     }
     if (c0 >= a.f.d) continue;
+    const int tok = grow / G, head = u.kvh * G + grow % G;
     if (ns == 1) {
-      const float inv = inverse_sum(rl);
-      u32x4 o;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
-      *reinterpret_cast<u32x4*>(a.f.o.p + (s.q0 + otok) * a.f.o.token + (int64_t)ohead * a.f.o.head + c0) = o;
+      const float inv = inverse_sum(l);
+      uint32_t* o = reinterpret_cast<uint32_t*>(a.f.o.p + (s.q0 + tok) * a.f.o.token + (int64_t)head * a.f.o.head + c0);
+      if constexpr (E == 8)
+        *reinterpret_cast<u32x4*>(o) = u32x4{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv),
+                                             pack_bf16x2(v[4] * inv, v[5] * inv), pack_bf16x2(v[6] * inv, v[7] * inv)};
+      else *o = pack_bf16x2(v[0] * inv, v[1] * inv);
+      if (c0 == 0 && a.f.lse) a.f.lse[(int64_t)head * a.f.lse_stride + s.q0 + tok] = lse_of(mxc, l);
     } else {
-      *reinterpret_cast<f32x4*>(part + c0) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(part + c0 + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    }
-  }
-  if ((tid & 7) == 0) {
-    if (ns == 1) {
-      if (a.f.lse) a.f.lse[(int64_t)ohead * a.f.lse_stride + s.q0 + otok] = lse_of(rm, rl);
-    } else {
-      part[a.f.d] = rl == 0.f ? -INFINITY : rm;   // finite (0 at least) where the sum is NaN: the join reads it
-      part[a.f.d + 1] = rl;
+      float* part = sp.part + (sp.row0[si] + ((int64_t)grow * a.f.kv_heads + u.kvh) * ns + split) * (int64_t)(a.f.d + 8);
+      if constexpr (E == 8) {
+        *reinterpret_cast<f32x4*>(part + c0) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4*>(part + c0 + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      } else {
+        *reinterpret_cast<float2*>(part + c0) = make_float2(v[0], v[1]);
+      }
+      if (c0 == 0) {
+        part[a.f.d] = l == 0.f ? -INFINITY : mxc;   // finite (0 at least) where the sum is NaN: the join reads it
+        part[a.f.d + 1] = l;
+      }
     }
   }
 }
 
 // ------------------------------------------------------------------------------------------
-// Host side: ranges of keys, launches
-static int64_t kv4_row_tiles(const AttnSeq& s, int G) { return ceil64((int64_t)s.nq * G, 32); }
-static int kv4_ranges(const AttnSeq& s, int window, int64_t chunk) {
-  return (int)std::max<int64_t>(1, ceil64(s.nk - first_key(s, window), chunk));
-}
+// Many rows: WV waves of 32 rows each share tiles of 64 keys in LDS, which they dequantise together, two tiles deep: while
+// a tile is multiplied, the next one's codes become values and the one after it is on its way from memory. Products are
+// v_mfma_f32_32x32x16_bf16 as in attn.hip. A workgroup's keys are one range of the sequence's.
+template <int DP, int WV>
+struct Kv4Many {
+  static constexpr int UNITS = 64 * (DP / 32) * 2, N = (UNITS + WV * 64 - 1) / (WV * 64);   // blocks of a tile, and of a thread
+  u32x4 c[N];
+  uint32_t m[N], vm[N];   // the block's maximum; for a key's block also that of the value's
+  // whole waves have work or not; a wave's units are the 64 keys of one block
+  static __device__ __forceinline__ bool works(int tid, int i) { return UNITS % (WV * 64) == 0 || i * WV * 64 + tid < UNITS; }
+  static __device__ __forceinline__ bool value(int tid, int i) { return i * WV * 64 + tid >= UNITS / 2; }
+  static __device__ __forceinline__ int block(int tid, int i) { return (i * WV * 64 + tid) / 64 % (DP / 32); }
+  __device__ __forceinline__ void load(const AttnKv4Args& a, int64_t kt, int64_t vt, int last, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (!works(tid, i)) continue;
+      const uint32_t key = (uint32_t)min(tid & 63, last), b = (uint32_t)min(block(tid, i), a.nb - 1);
+      const uint32_t ko = key * (uint32_t)a.k4.token + b, vo = key * (uint32_t)a.v4.token + b;
+      if (value(tid, i)) {
+        c[i] = *reinterpret_cast<const u32x4*>(a.v4.codes + 16 * vt + 16u * vo);
+        m[i] = 0;
+      } else {
+        c[i] = *reinterpret_cast<const u32x4*>(a.k4.codes + 16 * kt + 16u * ko);
+        m[i] = a.k4.absmax[kt + ko];
+      }
+      vm[i] = a.v4.absmax[vt + vo];
+    }
+  }
+  template <class Deq>
+  __device__ __forceinline__ void store(uint16_t* kt, uint16_t* vt, const AttnKv4Args& a, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (!works(tid, i)) continue;
+      const bool val = value(tid, i), lost = kv4_lost(vm[i]);
+      const Deq q(a.t, kv4_step(val ? (lost ? 0u : vm[i]) : (lost ? kBf16Nan : m[i]), a.unit));
+      uint16_t* tile = val ? vt : kt;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        *reinterpret_cast<u32x4*>(tile + Tile<DP>::elem(tid & 63, 4 * block(tid, i) + t)) = q.eight(c[i][t]);
+    }
+  }
+};
 
-// Keys per range, one length for all sequences of a launch: the smallest sum of rounds of workgroups (two on a
-// compute unit) times a range and a fixed part, and of the launch that joins ranges.
-static int64_t kv4_chunk(const std::vector<AttnSeq>& v, int G, int kv_heads, int d, int window) {
-  const double key = 0.011 * padded_d(d) / 128.0;
-  int64_t longest = 1, best = 0;
-  double best_cost = -1;
-  for (const AttnSeq& s : v) longest = std::max(longest, s.nk - first_key(s, window));
-  for (int64_t chunk = 128;; chunk += std::max<int64_t>(128, chunk / 8 / 128 * 128)) {
-    int64_t wgs = 0, most = 0;
-    for (const AttnSeq& s : v) {
-      const int64_t n = kv4_row_tiles(s, G) * kv4_ranges(s, window, chunk) * kv_heads;
-      wgs += n;
-      most = std::max(most, n);
-    }
-    if (most > kAttnGroups && chunk < longest) continue;   // a sequence has to fit a launch
-    const double cost = ceil64(wgs, 512) * (5 + key * std::min(chunk, longest)) + (chunk < longest ? 4 : 0);
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = chunk;
-    }
-    if (chunk >= longest) return best;
+// Accumulator rows 8 g .. 8 g + 7 (g = 0, 2) of a 32-row result tile, whose rows are the output's columns in the order of
+// eight(), exchanged between lane halves so that a lane holds 8 neighbouring columns, 16 (g / 2) + 8 (lane / 32), in order.
+__device__ __forceinline__ void kv4_columns(float (&o)[8], const f32x16& v, int g) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[4 * g + k]), __float_as_uint(v[4 * g + 4 + k]), false, false);
+    o[2 * k] = __uint_as_float(r[0]);
+    o[2 * k + 1] = __uint_as_float(r[1]);
   }
 }
 
-static AttnSeqs kv4_seqs(const std::vector<AttnSeq>& v, size_t from, int G, int kv_heads, int window, int64_t chunk) {
-  return pack_seqs(v, from, kv_heads, [&](const AttnSeq& s) { return kv4_row_tiles(s, G) * kv4_ranges(s, window, chunk); });
+template <int DP, class Deq, int WV>
+__global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4Args a, const AttnSeqs sq, const AttnSplit sp) {
+  constexpr int BN = 64, KS = DP / 16, DT = DP / 32, R = 32 * WV;
+  typedef Tile<DP> T;
+  __shared__ __attribute__((aligned(16))) uint16_t K0[BN * DP], V0[BN * DP], K1[BN * DP], V1[BN * DP];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int G = a.f.heads / a.f.kv_heads;
+  const Unit u = unit_of((int)blockIdx.x, a.f.kv_heads, 1);
+  const Found at_seq = find_seq(sq, u.tile);
+  const AttnSeq s = at_seq.seq;
+  const int si = at_seq.index, local = at_seq.next - 1 - u.tile;   // from the last rows (the most keys when causal) to the first
+  const int ns = sp.nsplit[si], split = local % ns, rt = local / ns;
+  const int shift = s.nk - s.nq, rows = s.nq * G;
+  const int row = rt * R + wave * 32 + (lane & 31);
+  const int tok = min(row, rows - 1) / G, head = u.kvh * G + min(row, rows - 1) % G;
+  auto sees = [&](int r) { return visible(min(r, rows - 1) / G + shift, s.nk, a.f.causal, a.f.window); };
+  const Range mine = visible(tok + shift, s.nk, a.f.causal, a.f.window);
+  const Range wa = sees(rt * R + wave * 32), wb = sees(rt * R + wave * 32 + 31);   // of the wave's first and last row
+  const int lo = sp.lo[si];
+  const int k_lo = lo + max((sees(rt * R).lo - lo) & ~(BN - 1), split * sp.chunk);
+  const int k_hi = min(sees(rt * R + R - 1).hi, lo + (split + 1) * sp.chunk);
+  const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
+  const int64_t kbase = (s.k0 + k_lo) * a.k4.token + (int64_t)u.kvh * a.k4.head, vbase = (s.k0 + k_lo) * a.v4.token + (int64_t)u.kvh * a.v4.head;
+  Kv4Many<DP, WV> codes;
+  auto load = [&](int t) __attribute__((always_inline)) {
+    codes.load(a, kbase + (int64_t)(t * BN) * a.k4.token, vbase + (int64_t)(t * BN) * a.v4.token, k_hi - 1 - (k_lo + t * BN), tid);
+  };
+  if (nt > 0) load(0);
+  bf16x8 qf[KS];
+  {
+    const uint16_t* q = a.f.q.p + (s.q0 + tok) * a.f.q.token + (int64_t)head * a.f.q.head;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int col = 8 * (2 * ks + (lane >> 5));
+      u32x4 v = u32x4{0u, 0u, 0u, 0u};
+      if (row < rows && col < a.f.d) v = *reinterpret_cast<const u32x4*>(q + col);
+      qf[ks] = __builtin_bit_cast(bf16x8, kv4_order(v));
+    }
+  }
+  Online<DT> acc;
+  acc.init();
+  const float slack = slack_of(a.f.c);
+  if (nt > 0) {
+    codes.template store<Deq>(K0, V0, a, tid);
+    if (nt > 1) load(1);
+  }
+  auto tile = [&](int t, const uint16_t* Kt, const uint16_t* Vt, uint16_t* kn, uint16_t* vn) __attribute__((always_inline)) {
+    lds_barrier();   // tile t is in, and every wave is done with tile t - 1
+    if (t + 1 < nt) {
+      codes.template store<Deq>(kn, vn, a, tid);
+      if (t + 2 < nt) load(t + 2);
+    }
+    const int j0 = k_lo + t * BN;
+    if (j0 < wb.hi && j0 + BN > wa.lo) {
+      f32x16 sc[2];
+      bf16x8 f[KS];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) f[ks] = T::rows(Kt, 0, ks, lane);
+      sc[0] = zero16();
+      sc[1] = zero16();
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        sc[0] = mfma(f[ks], qf[ks], sc[0]);
+        f[ks] = T::rows(Kt, 32, ks, lane);
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        sc[1] = mfma(f[ks], qf[ks], sc[1]);
+        f[ks] = T::cols(Vt, 16 * (ks / DT), ks % DT, lane);
+      }
+      if (j0 + BN > wa.hi || j0 < wb.lo) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) hide(sc[kt], mine, j0 + 32 * kt, lane, -INFINITY);
+      }
+      acc.update(sc, a.f.c, slack);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        acc.o[i % DT] = mfma(f[i], pack8(sc[0], i / DT), acc.o[i % DT]);
+        f[i] = T::cols(Vt, 32 + 16 * (i / DT), i % DT, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < KS; ++i) acc.o[i % DT] = mfma(f[i], pack8(sc[1], i / DT), acc.o[i % DT]);
+    }
+  };
+  for (int t = 0; t < nt; t += 2) {
+    tile(t, K0, V0, K1, V1);
+    if (t + 1 < nt) tile(t + 1, K1, V1, K0, V0);
+  }
+
+  const float l = half_sum(acc.l);
+  const bool in = row < rows;   // both lanes of a row alike
+  if (ns == 1) {
+    const float inv = inverse_sum(l);
+    uint16_t* o = a.f.o.p + (s.q0 + tok) * a.f.o.token + (int64_t)head * a.f.o.head;
+#pragma unroll
+    for (int i = 0; i < 2 * DT; ++i) {
+      const int c = 16 * i + 8 * (lane >> 5);
+      float v[8];
+      kv4_columns(v, acc.o[i / 2], 2 * (i & 1));
+      if (in && c < a.f.d)
+        *reinterpret_cast<u32x4*>(o + c) = u32x4{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv),
+                                                 pack_bf16x2(v[4] * inv, v[5] * inv), pack_bf16x2(v[6] * inv, v[7] * inv)};
+    }
+    if (in && a.f.lse && lane < 32) a.f.lse[(int64_t)head * a.f.lse_stride + s.q0 + tok] = lse_of(acc.mc, l);
+  } else {
+    float* part = sp.part + (sp.row0[si] + ((int64_t)row * a.f.kv_heads + u.kvh) * ns + split) * (int64_t)(a.f.d + 8);
+#pragma unroll
+    for (int i = 0; i < 2 * DT; ++i) {
+      const int c = 16 * i + 8 * (lane >> 5);
+      float v[8];
+      kv4_columns(v, acc.o[i / 2], 2 * (i & 1));
+      if (in && c < a.f.d) {
+        *reinterpret_cast<f32x4*>(part + c) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4*>(part + c + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      }
+    }
+    if (in && lane < 32) {
+      part[a.f.d] = l == 0.f ? -INFINITY : acc.mc;   // finite (0 at least) where the sum is NaN: the join reads it
+      part[a.f.d + 1] = l;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Host side: kernels, ranges of keys, launches
+constexpr int kKv4Few = 32;   // rows of a sequence up to which attn_kv4_few_kernel takes it
+
+static int64_t kv4_keys(const AttnSeq& s, int window) { return std::max<int64_t>(1, s.nk - first_key(s, window)); }
+
+// The sequences of one kernel: their rows in tiles of `rows`, their keys in ranges of `chunk`.
+struct Kv4Class {
+  std::vector<AttnSeq> seqs;
+  int rows = 0, waves = 0;
+  int64_t chunk = 0;
+  int64_t tiles(const AttnSeq& s, int G) const { return ceil64((int64_t)s.nq * G, rows); }
+  int ranges(const AttnSeq& s, int window) const { return (int)ceil64(kv4_keys(s, window), chunk); }
+};
+struct Kv4Plan {
+  Kv4Class few, many;
+  int64_t part_floats = 0;   // workspace of one launch (the largest)
+};
+
+static AttnSeqs kv4_seqs(const Kv4Class& c, size_t from, int G, int kv_heads, int window) {
+  return pack_seqs(c.seqs, from, kv_heads, [&](const AttnSeq& s) { return c.tiles(s, G) * c.ranges(s, window); });
+}
+
+// The shortest range, in multiples of `step`, for which the class has no more than `slots` workgroups (or one range a
+// sequence).
+static int64_t kv4_chunk(const Kv4Class& c, int G, int kv_heads, int window, int64_t slots, int64_t step) {
+  int64_t longest = 1, work = 0;
+  for (const AttnSeq& s : c.seqs) {
+    const int64_t n = kv4_keys(s, window);
+    longest = std::max(longest, n);
+    work += n * c.tiles(s, G) * kv_heads;
+  }
+  int64_t chunk = std::max(step, ceil64(work / slots, step) * step);
+  for (;; chunk += std::max(step, chunk / 16 / step * step)) {
+    if (chunk >= longest) return ceil64(longest, step) * step;
+    int64_t wgs = 0;
+    for (const AttnSeq& s : c.seqs) wgs += ceil64(kv4_keys(s, window), chunk) * c.tiles(s, G) * kv_heads;
+    if (wgs <= slots) return chunk;
+  }
+}
+
+static Kv4Plan kv4_plan(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window) {
+  Kv4Plan p;
+  const int G = heads / kv_heads;
+  int64_t most = 0;
+  for (const AttnSeq& s : by_work(seqs, count, false)) {
+    const int64_t rows = (int64_t)s.nq * G;
+    if (rows <= kKv4Few) {
+      p.few.seqs.push_back(s);
+      most = std::max(most, rows);
+    } else {
+      p.many.seqs.push_back(s);
+    }
+  }
+  for (Kv4Class* c : {&p.few, &p.many}) {
+    if (c->seqs.empty()) continue;
+    const bool few = c == &p.few;
+    c->waves = 4;
+    c->rows = few ? (most <= 16 ? 16 : 32) : 32 * c->waves;
+    c->chunk = kv4_chunk(*c, G, kv_heads, window, few && c->rows == 16 ? 1024 : 512, few ? 128 : 256);
+    for (size_t from = 0; from < c->seqs.size();) {
+      const AttnSeqs q = kv4_seqs(*c, from, G, kv_heads, window);
+      int64_t f = 0;
+      for (int i = 0; i < q.count; ++i) {
+        const int ns = c->ranges(q.seq[i], window);
+        if (ns > 1) f += (int64_t)q.seq[i].nq * heads * ns * (d + 8);
+      }
+      p.part_floats = std::max(p.part_floats, f);
+      from += (size_t)q.count;
+    }
+  }
+  return p;
 }
 
 size_t attn_kv4_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window) {
-  const std::vector<AttnSeq> v = by_work(seqs, count, false);
-  if (v.empty()) return 0;
-  const int G = heads / kv_heads;
-  const int64_t chunk = kv4_chunk(v, G, kv_heads, d, window);
-  int64_t most = 0;
-  for (size_t from = 0; from < v.size();) {
-    const AttnSeqs q = kv4_seqs(v, from, G, kv_heads, window, chunk);
-    int64_t f = 0;
-    for (int i = 0; i < q.count; ++i) {
-      const int ns = kv4_ranges(q.seq[i], window, chunk);
-      if (ns > 1) f += (int64_t)q.seq[i].nq * heads * ns * (d + 8);
-    }
-    most = std::max(most, f);
-    from += (size_t)q.count;
-  }
-  return (size_t)most;
+  return (size_t)kv4_plan(seqs, count, heads, kv_heads, d, window).part_floats;
 }
 
-hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream) {
-  const std::vector<AttnSeq> v = by_work(seqs, count, false);
-  if (v.empty()) return hipSuccess;
+template <int DP, class Deq>
+static void kv4_launch(const Kv4Class& c, bool few, const AttnKv4Args& a, const AttnSeqs& q, const AttnSplit& sp, hipStream_t stream) {
+  const dim3 grid((unsigned)(q.first[q.count] * a.f.kv_heads)), wg((unsigned)c.waves * 64);
+  if (!few) hipLaunchKernelGGL((attn_kv4_many_kernel<DP, Deq, 4>), grid, wg, 0, stream, a, q, sp);
+  else if (c.rows == 16) hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 4, 1>), grid, wg, 0, stream, a, q, sp);
+  else hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 4, 2>), grid, wg, 0, stream, a, q, sp);
+}
+
+hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, int64_t count, float* ws, size_t ws_floats,
+                           bool* fits, hipStream_t stream) {
+  const Kv4Plan plan = kv4_plan(seqs, count, a.f.heads, a.f.kv_heads, a.f.d, a.f.window);
+  *fits = !plan.part_floats || (ws && ws_floats >= (size_t)plan.part_floats);
+  if (!*fits) return hipSuccess;
   const int G = a.f.heads / a.f.kv_heads;
-  const int64_t chunk = kv4_chunk(v, G, a.f.kv_heads, a.f.d, a.f.window);
-  for (size_t from = 0; from < v.size();) {
-    const AttnSeqs q = kv4_seqs(v, from, G, a.f.kv_heads, a.f.window, chunk);
-    from += (size_t)q.count;
-    AttnSplit sp{};
-    sp.part = ws;
-    sp.chunk = (int)chunk;
-    int64_t row0 = 0;
-    for (int i = 0; i < q.count; ++i) {
-      sp.lo[i] = (int)first_key(q.seq[i], a.f.window);
-      sp.nsplit[i] = kv4_ranges(q.seq[i], a.f.window, chunk);
-      sp.row0[i] = row0;
-      const int64_t items = sp.nsplit[i] > 1 ? (int64_t)q.seq[i].nq * a.f.heads : 0;
-      row0 += items * sp.nsplit[i];
-      sp.join_first[i + 1] = sp.join_first[i] + (int)items;
+  for (const Kv4Class* c : {&plan.few, &plan.many}) {
+    for (size_t from = 0; from < c->seqs.size();) {
+      const AttnSeqs q = kv4_seqs(*c, from, G, a.f.kv_heads, a.f.window);
+      from += (size_t)q.count;
+      AttnSplit sp{};
+      sp.part = ws;
+      sp.chunk = (int)c->chunk;
+      int64_t row0 = 0;
+      for (int i = 0; i < q.count; ++i) {
+        sp.lo[i] = (int)first_key(q.seq[i], a.f.window);
+        sp.nsplit[i] = c->ranges(q.seq[i], a.f.window);
+        sp.row0[i] = row0;
+        const int64_t items = sp.nsplit[i] > 1 ? (int64_t)q.seq[i].nq * a.f.heads : 0;
+        row0 += items * sp.nsplit[i];
+        sp.join_first[i + 1] = sp.join_first[i] + (int)items;
+      }
+      const bool few = c == &plan.few;
+      if (a.f.d <= 64) {
+        if (book == 1) kv4_launch<64, Kv4E2m1>(*c, few, a, q, sp, stream);
+        else kv4_launch<64, Kv4Table>(*c, few, a, q, sp, stream);
+      } else {
+        if (book == 1) kv4_launch<128, Kv4E2m1>(*c, few, a, q, sp, stream);
+        else kv4_launch<128, Kv4Table>(*c, few, a, q, sp, stream);
+      }
+      launch_attn_join(a.f, q, sp, stream);
     }
-    const dim3 grid((unsigned)(q.first[q.count] * a.f.kv_heads));
-    if (a.f.d <= 64) hipLaunchKernelGGL(attn_kv4_kernel<64>, grid, dim3(256), 0, stream, a, q, sp);
-    else hipLaunchKernelGGL(attn_kv4_kernel<128>, grid, dim3(256), 0, stream, a, q, sp);
-    launch_attn_join(a.f, q, sp, stream);
   }
   return hipGetLastError();
 }

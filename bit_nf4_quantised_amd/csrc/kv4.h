@@ -16,15 +16,43 @@ constexpr uint32_t kBf16Infinity = 0x7F80u;
 
 __device__ __forceinline__ float kv4_step(uint32_t absmax, float unit) { return __fmul_rn(__uint_as_float(absmax << 16), unit); }
 
-// One packed dword (8 values) as 4 bf16 pairs, from the block's table of values.
+// A block's codes as bf16: eight() takes one packed dword (8 values) and gives them in the order 0 2 4 6 1 3 5 7,
+// which costs no byte moves; in_order() in their own.
+//
+// Any 16 values: a table of the block's 16 bf16 values, looked up with byte permutes (32 instructions for a table of 32
+// values, 23 for 8 values).
 struct Kv4Table {
   BlockLut lut;
   __device__ __forceinline__ Kv4Table(const Codes& t, float step) : lut(make_lut(step, t.v)) {}
   __device__ __forceinline__ u32x4 eight(uint32_t p) const {
+    uint32_t a, b, c, d;
+    lut4(lut, (p >> 4) & 0x0F0F0F0Fu, a, b);
+    lut4(lut, p & 0x0F0F0F0Fu, c, d);
+    return u32x4{a, b, c, d};
+  }
+  __device__ __forceinline__ u32x4 in_order(uint32_t p) const {
     uint32_t o[4];
     dequant8(lut, p, o);
     return u32x4{o[0], o[1], o[2], o[3]};
   }
 };
+// E2M1: converted by the hardware, two codes an instruction, then multiplied and rounded (16 instructions for 8 values)
+struct Kv4E2m1 {
+  float step;
+  __device__ __forceinline__ Kv4E2m1(const Codes&, float s) : step(s) {}
+  __device__ __forceinline__ u32x4 eight(uint32_t p) const {
+    const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(p, 1.f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(p, 1.f, 1),
+               c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(p, 1.f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(p, 1.f, 3);
+    return u32x4{pack_bf16x2(a[1] * step, b[1] * step), pack_bf16x2(c[1] * step, d[1] * step),
+                 pack_bf16x2(a[0] * step, b[0] * step), pack_bf16x2(c[0] * step, d[0] * step)};
+  }
+};
+// 8 bf16 values in order to the order of eight()
+__device__ __forceinline__ u32x4 kv4_order(const u32x4& x) {
+  return u32x4{__builtin_amdgcn_perm(x[1], x[0], 0x05040100u), __builtin_amdgcn_perm(x[3], x[2], 0x05040100u),
+               __builtin_amdgcn_perm(x[1], x[0], 0x07060302u), __builtin_amdgcn_perm(x[3], x[2], 0x07060302u)};
+}
+// where value e of 8 stands in that order
+constexpr int kv4_place_of(int e) { return (e & 1) * 4 + e / 2; }
 
 }  // namespace nf4

@@ -121,7 +121,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(const Kv4Args a, const At
   const int64_t at = p.at * src.token + (int64_t)p.head * src.head + p.block;
   const uint32_t codes = *reinterpret_cast<const uint32_t*>(src.codes + 16 * at + 4 * p.e);
   const uint32_t m = src.absmax[at];
-  u32x4 o = Kv4Table(a.t, kv4_step(m, a.unit)).eight(codes);
+  u32x4 o = Kv4Table(a.t, kv4_step(m, a.unit)).in_order(codes);
   // infinity stands for NaN with every code
   if (m >= kBf16Infinity) o = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
   *reinterpret_cast<u32x4*>(dst.p + p.token * dst.token + (int64_t)p.head * dst.head + 32 * p.block + 8 * p.e) = o;

@@ -269,7 +269,9 @@ bool kv4_codes(int book, Codes& t, float* unit);
 // every sequence's last nq tokens: k and v into the cache, or the cache into k and v
 hipError_t launch_kv4(const Kv4Args& a, int book, bool write, const AttnSeq* seqs, int64_t count, hipStream_t stream);
 size_t attn_kv4_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window);
-hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream);
+// *fits false: ws_floats are too few, and nothing was enqueued
+hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, int64_t count, float* ws, size_t ws_floats,
+                           bool* fits, hipStream_t stream);
 
 // ---- 8-bit activation checkpoints (act8.hip; format in act8.h). numel a multiple of 64.
 hipError_t launch_act8_pack(const uint16_t* x, int64_t numel, int8_t* codes, uint16_t* absmax, hipStream_t stream);

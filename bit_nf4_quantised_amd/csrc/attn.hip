@@ -1092,11 +1092,6 @@ size_t attn_bwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_
   return (size_t)(2 * round64(q_tokens * heads) + dkv_part_floats(v, plan.splits, kv_heads, padded_d(d)));
 }
 
-void launch_attn_join(const AttnFwdArgs& a, const AttnSeqs& q, const AttnSplit& sp, hipStream_t stream) {
-  const int items = sp.join_first[q.count];
-  if (items) hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a, q, sp);
-}
-
 hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream) {
   const std::vector<AttnSeq> v = by_work(seqs, count, false);
   if (v.empty()) return hipSuccess;
@@ -1132,7 +1127,8 @@ hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t co
     const dim3 grid((unsigned)(q.first[q.count] * a.kv_heads));
     if (a.d <= 64) hipLaunchKernelGGL(attn_split_kernel<64>, grid, dim3(256), 0, stream, a, q, sp);
     else hipLaunchKernelGGL(attn_split_kernel<128>, grid, dim3(256), 0, stream, a, q, sp);
-    launch_attn_join(a, q, sp, stream);
+    const int items = sp.join_first[q.count];
+    if (items) hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, a, q, sp);
   }
   return hipGetLastError();
 }

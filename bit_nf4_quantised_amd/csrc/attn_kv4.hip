@@ -16,6 +16,14 @@
 
 namespace nf4 {
 
+// The ranges of keys of a launch's sequences.
+struct Kv4Split {
+  float* part;   // per row, key head and range: d sums, maximum, sum, 6 unused
+  int lo[kAttnSeqs], chunk[kAttnSeqs], ranges[kAttnSeqs];   // first key, keys a range, how many
+  int64_t row0[kAttnSeqs];        // first record of a sequence in part
+  int join_first[kAttnSeqs + 1];  // prefix sums of rows x key heads over the sequences of several ranges
+};
+
 __device__ __forceinline__ bool kv4_lost(uint32_t absmax) { return absmax >= kBf16Infinity; }   // absmax has no sign
 constexpr uint32_t kBf16Nan = 0x7FC0u;
 
@@ -155,7 +163,7 @@ struct Online16 {
 };
 
 template <int DP, class Deq, int NW, int NR>
-__global__ __launch_bounds__(NW * 64, NR == 1 ? 4 : 2) void attn_kv4_few_kernel(const AttnKv4Args a, const AttnSeqs sq, const AttnSplit sp) {
+__global__ __launch_bounds__(NW * 64, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(const AttnKv4Args a, const AttnSeqs sq, const Kv4Split sp) {
   constexpr int BN = 32, KS = DP / 32, DT = DP / 16, R = 16 * NR, P = DP + 4;
   typedef Kv4Few<DP> Blocks;
   // a wave's tile of values, later its outputs as [row][d + 4]
@@ -169,14 +177,14 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 4 : 2) void attn_kv4_few_kernel(
   const Found at_seq = find_seq(sq, u.tile);
   const AttnSeq s = at_seq.seq;
   const int si = at_seq.index, local = u.tile - at_seq.first;
-  const int ns = sp.nsplit[si], split = local % ns, rt = local / ns;
+  const int ns = sp.ranges[si], split = local % ns, rt = local / ns;
   const int shift = s.nk - s.nq, rows = s.nq * G;
   const int t0 = rt * R / G, t1 = min(rows - 1, rt * R + R - 1) / G;   // tokens of the row tile
   const Range first = visible(t0 + shift, s.nk, a.f.causal, a.f.window), last = visible(t1 + shift, s.nk, a.f.causal, a.f.window);
   // tiles are counted from the first key that the sequence's first row sees (none before it is read)
-  const int lo = sp.lo[si];
-  const int k_lo = lo + max((first.lo - lo) & ~(BN - 1), split * sp.chunk);
-  const int k_hi = min(last.hi, lo + (split + 1) * sp.chunk);
+  const int lo = sp.lo[si], chunk = sp.chunk[si];
+  const int k_lo = lo + max((first.lo - lo) & ~(BN - 1), split * chunk);
+  const int k_hi = min(last.hi, lo + (split + 1) * chunk);
   const int64_t kbase = s.k0 * a.k4.token + (int64_t)u.kvh * a.k4.head, vbase = s.k0 * a.v4.token + (int64_t)u.kvh * a.v4.head;
   const int j_w = k_lo + wave * BN;   // the wave's first tile; its tiles are NW apart
   Blocks now, next;
@@ -203,7 +211,8 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 4 : 2) void attn_kv4_few_kernel(
   const float slack = slack_of(a.f.c);
   uint16_t* const vt = reinterpret_cast<uint16_t*>(lds[wave]);
 
-  for (int j = j_w; j < k_hi; j += NW * BN) {
+  // the tile of keys from j, in `now`; the wave's next goes to `next`
+  auto tile = [&](Blocks& now, Blocks& next, int j) __attribute__((always_inline)) {
     const int jn = j + NW * BN;
     if (jn < k_hi) next.load(a, kbase + (int64_t)jn * a.k4.token, vbase + (int64_t)jn * a.v4.token, k_hi - 1 - jn, lane);
     f32x4 sc[NR][2];
@@ -221,12 +230,14 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 4 : 2) void attn_kv4_few_kernel(
     // some row does not see some key
     if (j + BN > first.hi || j < last.lo) {
 #pragma unroll
-      for (int r = 0; r < NR; ++r)
+      for (int r = 0; r < NR; ++r) {
+        asm volatile("" : "+v"(sc[r][0]), "+v"(sc[r][1]));   // few tiles come here: keep it out of the others' way
+        const int at = mine[r].lo - j - 4 * (lane >> 4);
+        const uint32_t n = (uint32_t)max(mine[r].hi - mine[r].lo, 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int key = j + 16 * (i >> 2) + 4 * (lane >> 4) + (i & 3);
-          if (key < mine[r].lo || key >= mine[r].hi) sc[r][i >> 2][i & 3] = -INFINITY;
-        }
+        for (int i = 0; i < 8; ++i)
+          if ((uint32_t)(16 * (i >> 2) + (i & 3) - at) >= n) sc[r][i >> 2][i & 3] = -INFINITY;
+      }
     }
     bf16x8 p[NR];
 #pragma unroll
@@ -241,6 +252,9 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 4 : 2) void attn_kv4_few_kernel(
 #pragma unroll
       for (int r = 0; r < NR; ++r) acc[r].o[dt] = mfma16(vf, p[r], acc[r].o[dt]);
     }
+  };
+  for (int j = j_w; j < k_hi; j += NW * BN) {
+    tile(now, next, j);
     now = next;
   }
 
@@ -357,7 +371,7 @@ __device__ __forceinline__ void kv4_columns(float (&o)[8], const f32x16& v, int 
 }
 
 template <int DP, class Deq, int WV>
-__global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4Args a, const AttnSeqs sq, const AttnSplit sp) {
+__global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4Args a, const AttnSeqs sq, const Kv4Split sp) {
   constexpr int BN = 64, KS = DP / 16, DT = DP / 32, R = 32 * WV;
   typedef Tile<DP> T;
   __shared__ __attribute__((aligned(16))) uint16_t K0[BN * DP], V0[BN * DP], K1[BN * DP], V1[BN * DP];
@@ -368,16 +382,16 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
   const Found at_seq = find_seq(sq, u.tile);
   const AttnSeq s = at_seq.seq;
   const int si = at_seq.index, local = at_seq.next - 1 - u.tile;   // from the last rows (the most keys when causal) to the first
-  const int ns = sp.nsplit[si], split = local % ns, rt = local / ns;
+  const int ns = sp.ranges[si], split = local % ns, rt = local / ns;
   const int shift = s.nk - s.nq, rows = s.nq * G;
   const int row = rt * R + wave * 32 + (lane & 31);
   const int tok = min(row, rows - 1) / G, head = u.kvh * G + min(row, rows - 1) % G;
   auto sees = [&](int r) { return visible(min(r, rows - 1) / G + shift, s.nk, a.f.causal, a.f.window); };
   const Range mine = visible(tok + shift, s.nk, a.f.causal, a.f.window);
   const Range wa = sees(rt * R + wave * 32), wb = sees(rt * R + wave * 32 + 31);   // of the wave's first and last row
-  const int lo = sp.lo[si];
-  const int k_lo = lo + max((sees(rt * R).lo - lo) & ~(BN - 1), split * sp.chunk);
-  const int k_hi = min(sees(rt * R + R - 1).hi, lo + (split + 1) * sp.chunk);
+  const int lo = sp.lo[si], chunk = sp.chunk[si];
+  const int k_lo = lo + max((sees(rt * R).lo - lo) & ~(BN - 1), split * chunk);
+  const int k_hi = min(sees(rt * R + R - 1).hi, lo + (split + 1) * chunk);
   const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
   const int64_t kbase = (s.k0 + k_lo) * a.k4.token + (int64_t)u.kvh * a.k4.head, vbase = (s.k0 + k_lo) * a.v4.token + (int64_t)u.kvh * a.v4.head;
   Kv4Many<DP, WV> codes;
@@ -405,10 +419,13 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
   }
   auto tile = [&](int t, const uint16_t* Kt, const uint16_t* Vt, uint16_t* kn, uint16_t* vn) __attribute__((always_inline)) {
     lds_barrier();   // tile t is in, and every wave is done with tile t - 1
-    if (t + 1 < nt) {
-      codes.template store<Deq>(kn, vn, a, tid);
-      if (t + 2 < nt) load(t + 2);
-    }
+    auto prepare = [&]() __attribute__((always_inline)) {
+      if (t + 1 < nt) {
+        codes.template store<Deq>(kn, vn, a, tid);
+        if (t + 2 < nt) load(t + 2);
+      }
+    };
+    if (WV == 4 || wave < 4) prepare();
     const int j0 = k_lo + t * BN;
     if (j0 < wb.hi && j0 + BN > wa.lo) {
       f32x16 sc[2];
@@ -440,6 +457,7 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
 #pragma unroll
       for (int i = 0; i < KS; ++i) acc.o[i % DT] = mfma(f[i], pack8(sc[1], i / DT), acc.o[i % DT]);
     }
+    if (WV == 8 && wave >= 4) prepare();
   };
   for (int t = 0; t < nt; t += 2) {
     tile(t, K0, V0, K1, V1);
@@ -481,6 +499,97 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
 }
 
 // ------------------------------------------------------------------------------------------
+// Joins the ranges: an item is a row and key head of a sequence of several ranges. 32 lanes hold its columns, 4 each; S groups
+// of them take its ranges in turn, four at a time on their way, and are joined in order.
+template <int S>
+__global__ __launch_bounds__(256) void attn_kv4_join_kernel(const AttnFwdArgs a, const AttnSeqs sq, const Kv4Split sp) {
+  constexpr int ITEMS = 8 / S;
+  const int lane = threadIdx.x & 63, grp = (int)threadIdx.x >> 5;
+  const int G = a.heads / a.kv_heads;
+  const int item = (int)blockIdx.x * ITEMS + grp / S, slice = grp % S, all = sp.join_first[sq.count];
+  // sequences with one range have no items; the wave's items may be of two sequences
+  const int f = lane < sq.count ? sp.join_first[lane] : 0x7FFFFFFF;
+  const int i0 = __builtin_amdgcn_readfirstlane(min(item, all - 1));
+  int si = (int)__popcll(__ballot(f <= i0)) - 1;
+  if constexpr (ITEMS > 1) {
+    while (__any(min(item, all - 1) >= sp.join_first[si + 1])) {   // whole waves step on until each half has its own
+      if (min(item, all - 1) >= sp.join_first[si + 1]) ++si;
+    }
+  }
+  const AttnSeq s = sq.seq[si];
+  const int local = min(item, all - 1) - sp.join_first[si], ns = sp.ranges[si];
+  const int grow = local / a.kv_heads, kvh = local % a.kv_heads;
+  const int tok = grow / G, head = kvh * G + grow % G;
+  const int64_t step = a.d + 8;
+  const float* part = sp.part + (sp.row0[si] + (int64_t)local * ns) * step;
+  const int c = 4 * (lane & 31), cc = min(c, a.d - 4);   // d is a multiple of 8
+  float mx = -INFINITY, l = 0.f;
+  f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = slice; k0 < ns; k0 += 4 * S) {
+    float m[4], lk[4];
+    f32x4 x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float* p = part + min(k0 + q * S, ns - 1) * step;
+      x[q] = *reinterpret_cast<const f32x4*>(p + cc);
+      m[q] = p[a.d];
+      lk[q] = p[a.d + 1];
+    }
+    float top = mx;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (k0 + q * S >= ns) m[q] = -INFINITY;
+      top = fmaxf(top, m[q]);
+    }
+    if (top == -INFINITY) continue;
+    const float g = __builtin_amdgcn_exp2f(mx - top);   // 0 while nothing was seen
+    l *= g;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= g;
+    mx = top;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (m[q] == -INFINITY) continue;   // past the end, or a range that the row sees nothing of
+      const float w = __builtin_amdgcn_exp2f(m[q] - top);
+      l = __fmaf_rn(w, lk[q], l);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __fmaf_rn(w, x[q][e], v[e]);
+    }
+  }
+  if constexpr (S > 1) {
+    __shared__ float ms[S], ls[S];
+    __shared__ __attribute__((aligned(16))) float vs[S][128];
+    if ((lane & 31) == 0) {
+      ms[slice] = mx;
+      ls[slice] = l;
+    }
+    *reinterpret_cast<f32x4*>(&vs[slice][4 * (lane & 31)]) = v;
+    __syncthreads();
+    if (slice) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < S; ++k) top = fmaxf(top, ms[k]);
+    l = 0.f;
+    v = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const float w = ms[k] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms[k] - top);
+      l += ls[k] * w;   // 0 times NaN stays NaN
+      const f32x4 x = *reinterpret_cast<const f32x4*>(&vs[k][4 * (lane & 31)]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __fmaf_rn(w, x[e], v[e]);
+    }
+    mx = top;
+  }
+  if (item >= all) return;
+  const float inv = inverse_sum(l);
+  if (c < a.d)
+    *reinterpret_cast<u32x2*>(a.o.p + (s.q0 + tok) * a.o.token + (int64_t)head * a.o.head + c) =
+        u32x2{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
+  if (a.lse && (lane & 31) == 0) a.lse[(int64_t)head * a.lse_stride + s.q0 + tok] = lse_of(mx, l);
+}
+
+// ------------------------------------------------------------------------------------------
 // Host side: kernels, ranges of keys, launches
 constexpr int kKv4Few = 32;   // rows of a sequence up to which attn_kv4_few_kernel takes it
 
@@ -490,7 +599,7 @@ static int64_t kv4_keys(const AttnSeq& s, int window) { return std::max<int64_t>
 struct Kv4Class {
   std::vector<AttnSeq> seqs;
   int rows = 0, waves = 0;
-  int64_t chunk = 0;
+  int64_t chunk = 0, step = 0;   // a sequence's ranges are made equal, in multiples of step
   int64_t tiles(const AttnSeq& s, int G) const { return ceil64((int64_t)s.nq * G, rows); }
   int ranges(const AttnSeq& s, int window) const { return (int)ceil64(kv4_keys(s, window), chunk); }
 };
@@ -505,7 +614,8 @@ static AttnSeqs kv4_seqs(const Kv4Class& c, size_t from, int G, int kv_heads, in
 
 // The shortest range, in multiples of `step`, for which the class has no more than `slots` workgroups (or one range a
 // sequence).
-static int64_t kv4_chunk(const Kv4Class& c, int G, int kv_heads, int window, int64_t slots, int64_t step) {
+static int64_t kv4_chunk(const Kv4Class& c, int G, int kv_heads, int window, int64_t slots) {
+  const int64_t step = c.step;
   int64_t longest = 1, work = 0;
   for (const AttnSeq& s : c.seqs) {
     const int64_t n = kv4_keys(s, window);
@@ -524,7 +634,7 @@ static int64_t kv4_chunk(const Kv4Class& c, int G, int kv_heads, int window, int
 static Kv4Plan kv4_plan(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window) {
   Kv4Plan p;
   const int G = heads / kv_heads;
-  int64_t most = 0;
+  int64_t most = 0, most_many = 0;
   for (const AttnSeq& s : by_work(seqs, count, false)) {
     const int64_t rows = (int64_t)s.nq * G;
     if (rows <= kKv4Few) {
@@ -532,14 +642,16 @@ static Kv4Plan kv4_plan(const AttnSeq* seqs, int64_t count, int heads, int kv_he
       most = std::max(most, rows);
     } else {
       p.many.seqs.push_back(s);
+      most_many = std::max(most_many, rows);
     }
   }
   for (Kv4Class* c : {&p.few, &p.many}) {
     if (c->seqs.empty()) continue;
     const bool few = c == &p.few;
-    c->waves = 4;
+    c->waves = !few && most_many > 128 ? 8 : 4;
     c->rows = few ? (most <= 16 ? 16 : 32) : 32 * c->waves;
-    c->chunk = kv4_chunk(*c, G, kv_heads, window, few && c->rows == 16 ? 1024 : 512, few ? 128 : 256);
+    c->step = few ? 32 * c->waves : 64;
+    c->chunk = kv4_chunk(*c, G, kv_heads, window, few && c->rows == 16 ? 768 : c->waves == 8 ? 256 : 512);
     for (size_t from = 0; from < c->seqs.size();) {
       const AttnSeqs q = kv4_seqs(*c, from, G, kv_heads, window);
       int64_t f = 0;
@@ -559,9 +671,10 @@ size_t attn_kv4_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_
 }
 
 template <int DP, class Deq>
-static void kv4_launch(const Kv4Class& c, bool few, const AttnKv4Args& a, const AttnSeqs& q, const AttnSplit& sp, hipStream_t stream) {
+static void kv4_launch(const Kv4Class& c, bool few, const AttnKv4Args& a, const AttnSeqs& q, const Kv4Split& sp, hipStream_t stream) {
   const dim3 grid((unsigned)(q.first[q.count] * a.f.kv_heads)), wg((unsigned)c.waves * 64);
-  if (!few) hipLaunchKernelGGL((attn_kv4_many_kernel<DP, Deq, 4>), grid, wg, 0, stream, a, q, sp);
+  if (c.waves == 8) hipLaunchKernelGGL((attn_kv4_many_kernel<DP, Deq, 8>), grid, wg, 0, stream, a, q, sp);
+  else if (!few) hipLaunchKernelGGL((attn_kv4_many_kernel<DP, Deq, 4>), grid, wg, 0, stream, a, q, sp);
   else if (c.rows == 16) hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 4, 1>), grid, wg, 0, stream, a, q, sp);
   else hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 4, 2>), grid, wg, 0, stream, a, q, sp);
 }
@@ -576,17 +689,20 @@ hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, 
     for (size_t from = 0; from < c->seqs.size();) {
       const AttnSeqs q = kv4_seqs(*c, from, G, a.f.kv_heads, a.f.window);
       from += (size_t)q.count;
-      AttnSplit sp{};
+      Kv4Split sp{};
       sp.part = ws;
-      sp.chunk = (int)c->chunk;
       int64_t row0 = 0;
+      int most = 0;
       for (int i = 0; i < q.count; ++i) {
+        const int n = c->ranges(q.seq[i], a.f.window);
         sp.lo[i] = (int)first_key(q.seq[i], a.f.window);
-        sp.nsplit[i] = c->ranges(q.seq[i], a.f.window);
+        sp.ranges[i] = n;
+        sp.chunk[i] = (int)(ceil64(ceil64(kv4_keys(q.seq[i], a.f.window), n), c->step) * c->step);
         sp.row0[i] = row0;
-        const int64_t items = sp.nsplit[i] > 1 ? (int64_t)q.seq[i].nq * a.f.heads : 0;
-        row0 += items * sp.nsplit[i];
+        const int64_t items = n > 1 ? (int64_t)q.seq[i].nq * a.f.heads : 0;
+        row0 += items * n;
         sp.join_first[i + 1] = sp.join_first[i] + (int)items;
+        most = std::max(most, n);
       }
       const bool few = c == &plan.few;
       if (a.f.d <= 64) {
@@ -596,7 +712,9 @@ hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, 
         if (book == 1) kv4_launch<128, Kv4E2m1>(*c, few, a, q, sp, stream);
         else kv4_launch<128, Kv4Table>(*c, few, a, q, sp, stream);
       }
-      launch_attn_join(a.f, q, sp, stream);
+      const int items = sp.join_first[q.count];
+      if (items && most > 4) hipLaunchKernelGGL(attn_kv4_join_kernel<8>, dim3((unsigned)items), dim3(256), 0, stream, a.f, q, sp);
+      else if (items) hipLaunchKernelGGL(attn_kv4_join_kernel<1>, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, stream, a.f, q, sp);
     }
   }
   return hipGetLastError();

@@ -223,8 +223,6 @@ size_t attn_fwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_
 size_t attn_bwd_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int causal, int window,
                           int64_t q_tokens);
 hipError_t launch_attn_fwd(const AttnFwdArgs& a, const AttnSeq* seqs, int64_t count, float* ws, hipStream_t stream);
-// joins the ranges of keys that a launch has left in sp.part, in order
-void launch_attn_join(const AttnFwdArgs& a, const AttnSeqs& q, const AttnSplit& sp, hipStream_t stream);
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, const AttnSeq* seqs, int64_t count, int64_t q_tokens, float* ws,
                            hipStream_t stream);
 

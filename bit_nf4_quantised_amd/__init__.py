@@ -131,7 +131,7 @@ _SIGS = {
     "qlora_kv4_write": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p]),
     "qlora_kv4_read": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p]),
     "qlora_attn_kv4_fwd": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
-    "qlora_attn_kv4_workspace_bytes": (_sz, [_p, _i64, _p]),
+    "qlora_attn_kv4_workspace_bytes": (_sz, [_p, _i64, _p, _i32]),
     "nf4_storage_bytes": (_i64, [_i64]),
     "nf4_codebook": (None, [ctypes.POINTER(ctypes.c_float)]),
     "nf4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -640,6 +640,7 @@ class AttnSeqs:
         self.causal, self.window = bool(causal), int(window)
         self._seqs = (ctypes.c_int64 * max(len(flat), 4))(*flat)
         self._last = (None, None)   # what the last configuration was made of, and it
+        self._need4 = (None, None, 0)   # a configuration, a codebook, and the workspace of qlora_attn_kv4_fwd for them
 
     @staticmethod
     def packed(lengths, causal: bool = True, window: int = 0) -> "AttnSeqs":
@@ -938,7 +939,10 @@ def qlora_attn_kv4_fwd(seqs: AttnSeqs, q, k4: Kv4, v4: Kv4, o, lse=None, scale: 
     plse = _lse_ptr(lse, q)
     pws, nbytes = None, 0
     if ws is None:
-        need = int(lib.qlora_attn_kv4_workspace_bytes(cfg, seqs.count, seqs._seqs))
+        last, book, need = seqs._need4      # a configuration is never written to, so the same one has the same need
+        if last is not cfg._obj or book != k4.codebook:
+            need = int(lib.qlora_attn_kv4_workspace_bytes(cfg, seqs.count, seqs._seqs, k4.codebook))
+            seqs._need4 = (cfg._obj, k4.codebook, need)
         ws = _scratch(need, q.device, stream) if need else None
     if ws is not None:
         pws, nbytes = _ptr(ws), ws.numel() * ws.element_size()

@@ -872,11 +872,11 @@ int qlora_kv4_read(const qlora_attn_config* cfg, int64_t count, const qlora_attn
   return kv4_copy(false, cfg, count, seqs, k, v, k4, v4, stream);
 }
 
-size_t qlora_attn_kv4_workspace_bytes(const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs) {
-  if (check_attn_config(cfg) || check_attn_seqs(cfg, count, seqs, false) || count == 0 || check_kv4_rows(cfg, count, seqs)) return 0;
+size_t qlora_attn_kv4_workspace_bytes(const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs, int32_t codebook) {
+  if (codebook < Q4_CODEBOOK_NF4 || codebook > Q4_CODEBOOK_INT4 || check_attn_config(cfg) || check_attn_seqs(cfg, count, seqs, false) || count == 0 || check_kv4_rows(cfg, count, seqs)) return 0;
   try {
     const std::vector<nf4::AttnSeq> v = attn_seqs(count, seqs);
-    return align_up(nf4::attn_kv4_ws_floats(v.data(), count, cfg->heads, cfg->kv_heads, cfg->d, attn_window(cfg)) * 4);
+    return align_up(nf4::attn_kv4_ws_floats(v.data(), count, codebook, cfg->heads, cfg->kv_heads, cfg->d, attn_window(cfg)) * 4);
   } catch (...) {
     return 0;
   }

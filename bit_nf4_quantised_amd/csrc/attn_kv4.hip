@@ -323,34 +323,31 @@ template <int DP, int WV>
 struct Kv4Many {
   static constexpr int UNITS = 64 * (DP / 32) * 2, N = (UNITS + WV * 64 - 1) / (WV * 64);   // blocks of a tile, and of a thread
   u32x4 c[N];
-  uint32_t m[N], vm[N];   // the block's maximum; for a key's block also that of the value's
-  // whole waves have work or not; a wave's units are the 64 keys of one block
-  static __device__ __forceinline__ bool works(int tid, int i) { return UNITS % (WV * 64) == 0 || i * WV * 64 + tid < UNITS; }
-  static __device__ __forceinline__ bool value(int tid, int i) { return i * WV * 64 + tid >= UNITS / 2; }
-  static __device__ __forceinline__ int block(int tid, int i) { return (i * WV * 64 + tid) / 64 % (DP / 32); }
+  uint32_t m[N], vm[N];   // the block's maximum and that of the value's block (for values the same)
+  // a wave's units are the 64 keys of one block; in a tile of too few blocks waves do others' work again
+  static __device__ __forceinline__ int unit(int tid, int i) { return (i * WV * 64 + tid) % UNITS; }
+  static __device__ __forceinline__ bool value(int tid, int i) { return unit(tid, i) >= UNITS / 2; }
+  static __device__ __forceinline__ int block(int tid, int i) { return unit(tid, i) / 64 % (DP / 32); }
   __device__ __forceinline__ void load(const AttnKv4Args& a, int64_t kt, int64_t vt, int last, int tid) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (!works(tid, i)) continue;
       const uint32_t key = (uint32_t)min(tid & 63, last), b = (uint32_t)min(block(tid, i), a.nb - 1);
-      const uint32_t ko = key * (uint32_t)a.k4.token + b, vo = key * (uint32_t)a.v4.token + b;
-      if (value(tid, i)) {
-        c[i] = *reinterpret_cast<const u32x4*>(a.v4.codes + 16 * vt + 16u * vo);
-        m[i] = 0;
-      } else {
-        c[i] = *reinterpret_cast<const u32x4*>(a.k4.codes + 16 * kt + 16u * ko);
-        m[i] = a.k4.absmax[kt + ko];
-      }
-      vm[i] = a.v4.absmax[vt + vo];
+      const bool val = value(tid, i);
+      const uint8_t* codes = val ? a.v4.codes + 16 * vt : a.k4.codes + 16 * kt;
+      const uint16_t* absmax = val ? a.v4.absmax + vt : a.k4.absmax + kt;
+      const uint32_t at = key * (uint32_t)(val ? a.v4.token : a.k4.token) + b;
+      c[i] = *reinterpret_cast<const u32x4*>(codes + 16u * at);
+      m[i] = absmax[at];
+      vm[i] = a.v4.absmax[vt + (key * (uint32_t)a.v4.token + b)];
     }
   }
+  // the loaded blocks into a tile
   template <class Deq>
   __device__ __forceinline__ void store(uint16_t* kt, uint16_t* vt, const AttnKv4Args& a, int tid) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (!works(tid, i)) continue;
-      const bool val = value(tid, i), lost = kv4_lost(vm[i]);
-      const Deq q(a.t, kv4_step(val ? (lost ? 0u : vm[i]) : (lost ? kBf16Nan : m[i]), a.unit));
+      const bool val = value(tid, i);
+      const Deq q(a.t, kv4_step(kv4_lost(vm[i]) ? (val ? 0u : kBf16Nan) : m[i], a.unit));
       uint16_t* tile = val ? vt : kt;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -394,9 +391,11 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
   const int k_hi = min(sees(rt * R + R - 1).hi, lo + (split + 1) * chunk);
   const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
   const int64_t kbase = (s.k0 + k_lo) * a.k4.token + (int64_t)u.kvh * a.k4.head, vbase = (s.k0 + k_lo) * a.v4.token + (int64_t)u.kvh * a.v4.head;
-  Kv4Many<DP, WV> codes;
-  auto load = [&](int t) __attribute__((always_inline)) {
-    codes.load(a, kbase + (int64_t)(t * BN) * a.k4.token, vbase + (int64_t)(t * BN) * a.v4.token, k_hi - 1 - (k_lo + t * BN), tid);
+  typedef Kv4Many<DP, WV> Many;
+  Many codes;
+  auto load = [&](int t) __attribute__((always_inline)) {   // past the last tile the last one again
+    const int at = min(t, nt - 1) * BN;
+    codes.load(a, kbase + (int64_t)at * a.k4.token, vbase + (int64_t)at * a.v4.token, k_hi - 1 - (k_lo + at), tid);
   };
   if (nt > 0) load(0);
   bf16x8 qf[KS];
@@ -415,49 +414,46 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
   const float slack = slack_of(a.f.c);
   if (nt > 0) {
     codes.template store<Deq>(K0, V0, a, tid);
-    if (nt > 1) load(1);
+    load(1);
   }
+  // tile t is in (Kt, Vt); tile t + 1 is made in (kn, vn). No branches around the products: a wave whose rows see nothing of a
+  // tile hides all of it (branches made the compiler move the outputs between registers, 81 us against 76)
   auto tile = [&](int t, const uint16_t* Kt, const uint16_t* Vt, uint16_t* kn, uint16_t* vn) __attribute__((always_inline)) {
     lds_barrier();   // tile t is in, and every wave is done with tile t - 1
-    auto prepare = [&]() __attribute__((always_inline)) {
-      if (t + 1 < nt) {
-        codes.template store<Deq>(kn, vn, a, tid);
-        if (t + 2 < nt) load(t + 2);
-      }
-    };
-    if (WV == 4 || wave < 4) prepare();
+    codes.template store<Deq>(kn, vn, a, tid);
+    load(t + 2);
     const int j0 = k_lo + t * BN;
-    if (j0 < wb.hi && j0 + BN > wa.lo) {
-      f32x16 sc[2];
-      bf16x8 f[KS];
+    f32x16 sc[2];
+    bf16x8 f[KS];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) f[ks] = T::rows(Kt, 0, ks, lane);
-      sc[0] = zero16();
-      sc[1] = zero16();
+    for (int ks = 0; ks < KS; ++ks) f[ks] = T::rows(Kt, 0, ks, lane);
+    sc[0] = zero16();
+    sc[1] = zero16();
+    keep_order();
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        sc[0] = mfma(f[ks], qf[ks], sc[0]);
-        f[ks] = T::rows(Kt, 32, ks, lane);
-      }
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        sc[1] = mfma(f[ks], qf[ks], sc[1]);
-        f[ks] = T::cols(Vt, 16 * (ks / DT), ks % DT, lane);
-      }
-      if (j0 + BN > wa.hi || j0 < wb.lo) {
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) hide(sc[kt], mine, j0 + 32 * kt, lane, -INFINITY);
-      }
-      acc.update(sc, a.f.c, slack);
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        acc.o[i % DT] = mfma(f[i], pack8(sc[0], i / DT), acc.o[i % DT]);
-        f[i] = T::cols(Vt, 32 + 16 * (i / DT), i % DT, lane);
-      }
-#pragma unroll
-      for (int i = 0; i < KS; ++i) acc.o[i % DT] = mfma(f[i], pack8(sc[1], i / DT), acc.o[i % DT]);
+    for (int ks = 0; ks < KS; ++ks) {
+      sc[0] = mfma(f[ks], qf[ks], sc[0]);
+      f[ks] = T::rows(Kt, 32, ks, lane);
+      keep_order();
     }
-    if (WV == 8 && wave >= 4) prepare();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      sc[1] = mfma(f[ks], qf[ks], sc[1]);
+      f[ks] = T::cols(Vt, 16 * (ks / DT), ks % DT, lane);
+      keep_order();
+    }
+    if (j0 + BN > wa.hi || j0 < wb.lo) {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) hide(sc[kt], mine, j0 + 32 * kt, lane, -INFINITY);
+    }
+    acc.update(sc, a.f.c, slack);
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      acc.o[i % DT] = mfma(f[i], pack8(sc[0], i / DT), acc.o[i % DT]);
+      f[i] = T::cols(Vt, 32 + 16 * (i / DT), i % DT, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < KS; ++i) acc.o[i % DT] = mfma(f[i], pack8(sc[1], i / DT), acc.o[i % DT]);
   };
   for (int t = 0; t < nt; t += 2) {
     tile(t, K0, V0, K1, V1);
@@ -591,20 +587,33 @@ __global__ __launch_bounds__(256) void attn_kv4_join_kernel(const AttnFwdArgs a,
 
 // ------------------------------------------------------------------------------------------
 // Host side: kernels, ranges of keys, launches
-constexpr int kKv4Few = 32;   // rows of a sequence up to which attn_kv4_few_kernel takes it
-
 static int64_t kv4_keys(const AttnSeq& s, int window) { return std::max<int64_t>(1, s.nk - first_key(s, window)); }
 
-// The sequences of one kernel: their rows in tiles of `rows`, their keys in ranges of `chunk`.
+// The kernels: rows of a workgroup, keys of a step (a range is a multiple of it), workgroups that a compute unit holds, and
+// the time of a step in us with 1, 2 .. of them on it, for tables and for E2M1 (d = 128; d <= 64 takes 0.6 of it). Measured
+// with one, two and three workgroups a unit, on caches of 2000 to 30000 keys.
+struct Kv4Kernel {
+  int rows, waves, step, most;
+  double us[2][3];
+};
+constexpr Kv4Kernel kKv4Kernels[] = {
+    {16, 4, 128, 3, {{1.65, 2.65, 4.4}, {1.2, 1.8, 2.55}}},
+    {32, 4, 128, 2, {{2.0, 3.85, 0}, {1.6, 3.05, 0}}},
+    {128, 4, 64, 2, {{1.82, 2.95, 0}, {1.52, 2.6, 0}}},
+    {256, 8, 64, 1, {{2.07, 0, 0}, {1.9, 0, 0}}},
+};
+
+// The sequences of one launch form: their rows in tiles of the kernel's, their keys in ranges of about `chunk`.
 struct Kv4Class {
   std::vector<AttnSeq> seqs;
-  int rows = 0, waves = 0;
-  int64_t chunk = 0, step = 0;   // a sequence's ranges are made equal, in multiples of step
-  int64_t tiles(const AttnSeq& s, int G) const { return ceil64((int64_t)s.nq * G, rows); }
+  int kernel = 0;
+  int64_t chunk = 0;
+  const Kv4Kernel& k() const { return kKv4Kernels[kernel]; }
+  int64_t tiles(const AttnSeq& s, int G) const { return ceil64((int64_t)s.nq * G, k().rows); }
   int ranges(const AttnSeq& s, int window) const { return (int)ceil64(kv4_keys(s, window), chunk); }
 };
 struct Kv4Plan {
-  Kv4Class few, many;
+  Kv4Class few, many;        // sequences of up to 32 rows, and of more
   int64_t part_floats = 0;   // workspace of one launch (the largest)
 };
 
@@ -612,46 +621,70 @@ static AttnSeqs kv4_seqs(const Kv4Class& c, size_t from, int G, int kv_heads, in
   return pack_seqs(c.seqs, from, kv_heads, [&](const AttnSeq& s) { return c.tiles(s, G) * c.ranges(s, window); });
 }
 
-// The shortest range, in multiples of `step`, for which the class has no more than `slots` workgroups (or one range a
-// sequence).
-static int64_t kv4_chunk(const Kv4Class& c, int G, int kv_heads, int window, int64_t slots) {
-  const int64_t step = c.step;
-  int64_t longest = 1, work = 0;
-  for (const AttnSeq& s : c.seqs) {
-    const int64_t n = kv4_keys(s, window);
-    longest = std::max(longest, n);
-    work += n * c.tiles(s, G) * kv_heads;
+// Chooses the kernel among [from, to) and the length of a range by the smallest estimate: 5 us around the steps (launch, first
+// loads, joining the waves), the longest range's steps at the rate of a unit that holds its share of workgroups, times the
+// rounds of workgroups, and, where there are ranges to join, 3.5 us and their sums at 7 TB/s. Estimated and measured, us: 5 tokens
+// each over 8 caches of 2000 keys, 32 heads over 8, 17.7 and 17.7; one token of 30000 keys 21 and 20; 65 tokens over
+// 30000 keys 80 and 77; 65 tokens over 300 keys each of 4 (one range) 14 and 15, where ranges of 128 keys took 26.
+static inline double up(double x) {   // to a whole number; x is not large
+  const int64_t i = (int64_t)x;
+  return (double)(i + ((double)i < x));
+}
+static void kv4_choose(Kv4Class& c, int from, int to, bool e2m1, int G, int kv_heads, int d, int window) {
+  const size_t n = c.seqs.size();
+  std::vector<double> keys(n), rows(n);
+  double longest = 1;
+  for (size_t i = 0; i < n; ++i) {
+    keys[i] = (double)kv4_keys(c.seqs[i], window);
+    rows[i] = (double)c.seqs[i].nq * G;
+    longest = std::max(longest, keys[i]);
   }
-  int64_t chunk = std::max(step, ceil64(work / slots, step) * step);
-  for (;; chunk += std::max(step, chunk / 16 / step * step)) {
-    if (chunk >= longest) return ceil64(longest, step) * step;
-    int64_t wgs = 0;
-    for (const AttnSeq& s : c.seqs) wgs += ceil64(kv4_keys(s, window), chunk) * c.tiles(s, G) * kv_heads;
-    if (wgs <= slots) return chunk;
+  double best = -1;
+  for (int x = from; x < to; ++x) {
+    const Kv4Kernel& k = kKv4Kernels[x];
+    for (double chunk = k.step;; chunk = up(chunk * 1.19 / k.step) * k.step) {
+      const bool whole = chunk >= longest;
+      double large = 0, records = 0, load = 0, top = 0, most = 0;
+      for (size_t i = 0; i < n; ++i) {
+        const double r = whole ? 1 : up(keys[i] / chunk), w = up(rows[i] / k.rows) * kv_heads;
+        if (keys[i] > 0.5 * r * std::min(chunk, longest)) large += w * r;
+        most = std::max(most, w * r);
+        load += w * keys[i];
+        top = std::max(top, up(keys[i] / (r * k.step)) * k.step);
+        if (r > 1) records += rows[i] * kv_heads * r;
+      }
+      if (whole || most <= (double)kAttnGroups) {   // a sequence has to fit a launch
+        // workgroups on each of 256 units: those of more than half a range's length, or by the work
+        const double full = std::max({1.0, up(large / 256), up(load / top / 256 - 0.25)});
+        const int on = (int)std::min<double>(k.most, full);
+        const double us = 5 + top / k.step * k.us[e2m1][on - 1] * (d <= 64 ? 0.6 : 1.0) * up(full / on) +
+                          (records > 0 ? 3.5 + records * (d + 8) * 8 / 7e6 : 0);
+        if (best < 0 || us < best) {
+          best = us;
+          c.kernel = x;
+          c.chunk = (int64_t)(whole ? up(longest / k.step) * k.step : chunk);
+        }
+      }
+      if (whole) break;
+    }
   }
 }
 
-static Kv4Plan kv4_plan(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window) {
+static Kv4Plan kv4_plan(const AttnSeq* seqs, int64_t count, int book, int heads, int kv_heads, int d, int window) {
   Kv4Plan p;
   const int G = heads / kv_heads;
-  int64_t most = 0, most_many = 0;
+  int64_t few_rows = 0, many_rows = 0;
   for (const AttnSeq& s : by_work(seqs, count, false)) {
     const int64_t rows = (int64_t)s.nq * G;
-    if (rows <= kKv4Few) {
-      p.few.seqs.push_back(s);
-      most = std::max(most, rows);
-    } else {
-      p.many.seqs.push_back(s);
-      most_many = std::max(most_many, rows);
-    }
+    (rows <= 32 ? p.few : p.many).seqs.push_back(s);
+    int64_t& most = rows <= 32 ? few_rows : many_rows;
+    most = std::max(most, rows);
   }
   for (Kv4Class* c : {&p.few, &p.many}) {
     if (c->seqs.empty()) continue;
-    const bool few = c == &p.few;
-    c->waves = !few && most_many > 128 ? 8 : 4;
-    c->rows = few ? (most <= 16 ? 16 : 32) : 32 * c->waves;
-    c->step = few ? 32 * c->waves : 64;
-    c->chunk = kv4_chunk(*c, G, kv_heads, window, few && c->rows == 16 ? 768 : c->waves == 8 ? 256 : 512);
+    // 16 rows a workgroup for up to 32 rows, 32 for 17 to 512, 128 and 256 from 33 on
+    if (c == &p.few) kv4_choose(*c, 0, few_rows <= 16 ? 1 : 2, book == 1, G, kv_heads, d, window);
+    else kv4_choose(*c, many_rows <= 512 ? 1 : 2, many_rows <= 64 ? 3 : 4, book == 1, G, kv_heads, d, window);
     for (size_t from = 0; from < c->seqs.size();) {
       const AttnSeqs q = kv4_seqs(*c, from, G, kv_heads, window);
       int64_t f = 0;
@@ -666,22 +699,24 @@ static Kv4Plan kv4_plan(const AttnSeq* seqs, int64_t count, int heads, int kv_he
   return p;
 }
 
-size_t attn_kv4_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window) {
-  return (size_t)kv4_plan(seqs, count, heads, kv_heads, d, window).part_floats;
+size_t attn_kv4_ws_floats(const AttnSeq* seqs, int64_t count, int book, int heads, int kv_heads, int d, int window) {
+  return (size_t)kv4_plan(seqs, count, book, heads, kv_heads, d, window).part_floats;
 }
 
 template <int DP, class Deq>
-static void kv4_launch(const Kv4Class& c, bool few, const AttnKv4Args& a, const AttnSeqs& q, const Kv4Split& sp, hipStream_t stream) {
-  const dim3 grid((unsigned)(q.first[q.count] * a.f.kv_heads)), wg((unsigned)c.waves * 64);
-  if (c.waves == 8) hipLaunchKernelGGL((attn_kv4_many_kernel<DP, Deq, 8>), grid, wg, 0, stream, a, q, sp);
-  else if (!few) hipLaunchKernelGGL((attn_kv4_many_kernel<DP, Deq, 4>), grid, wg, 0, stream, a, q, sp);
-  else if (c.rows == 16) hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 4, 1>), grid, wg, 0, stream, a, q, sp);
-  else hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 4, 2>), grid, wg, 0, stream, a, q, sp);
+static void kv4_launch(int kernel, const AttnKv4Args& a, const AttnSeqs& q, const Kv4Split& sp, hipStream_t stream) {
+  const dim3 grid((unsigned)(q.first[q.count] * a.f.kv_heads)), wg((unsigned)kKv4Kernels[kernel].waves * 64);
+  switch (kernel) {
+    case 0: hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 4, 1>), grid, wg, 0, stream, a, q, sp); break;
+    case 1: hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 4, 2>), grid, wg, 0, stream, a, q, sp); break;
+    case 2: hipLaunchKernelGGL((attn_kv4_many_kernel<DP, Deq, 4>), grid, wg, 0, stream, a, q, sp); break;
+    default: hipLaunchKernelGGL((attn_kv4_many_kernel<DP, Deq, 8>), grid, wg, 0, stream, a, q, sp); break;
+  }
 }
 
 hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, int64_t count, float* ws, size_t ws_floats,
                            bool* fits, hipStream_t stream) {
-  const Kv4Plan plan = kv4_plan(seqs, count, a.f.heads, a.f.kv_heads, a.f.d, a.f.window);
+  const Kv4Plan plan = kv4_plan(seqs, count, book, a.f.heads, a.f.kv_heads, a.f.d, a.f.window);
   *fits = !plan.part_floats || (ws && ws_floats >= (size_t)plan.part_floats);
   if (!*fits) return hipSuccess;
   const int G = a.f.heads / a.f.kv_heads;
@@ -697,20 +732,19 @@ hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, 
         const int n = c->ranges(q.seq[i], a.f.window);
         sp.lo[i] = (int)first_key(q.seq[i], a.f.window);
         sp.ranges[i] = n;
-        sp.chunk[i] = (int)(ceil64(ceil64(kv4_keys(q.seq[i], a.f.window), n), c->step) * c->step);
+        sp.chunk[i] = (int)(ceil64(ceil64(kv4_keys(q.seq[i], a.f.window), n), c->k().step) * c->k().step);   // equal ranges
         sp.row0[i] = row0;
         const int64_t items = n > 1 ? (int64_t)q.seq[i].nq * a.f.heads : 0;
         row0 += items * n;
         sp.join_first[i + 1] = sp.join_first[i] + (int)items;
         most = std::max(most, n);
       }
-      const bool few = c == &plan.few;
       if (a.f.d <= 64) {
-        if (book == 1) kv4_launch<64, Kv4E2m1>(*c, few, a, q, sp, stream);
-        else kv4_launch<64, Kv4Table>(*c, few, a, q, sp, stream);
+        if (book == 1) kv4_launch<64, Kv4E2m1>(c->kernel, a, q, sp, stream);
+        else kv4_launch<64, Kv4Table>(c->kernel, a, q, sp, stream);
       } else {
-        if (book == 1) kv4_launch<128, Kv4E2m1>(*c, few, a, q, sp, stream);
-        else kv4_launch<128, Kv4Table>(*c, few, a, q, sp, stream);
+        if (book == 1) kv4_launch<128, Kv4E2m1>(c->kernel, a, q, sp, stream);
+        else kv4_launch<128, Kv4Table>(c->kernel, a, q, sp, stream);
       }
       const int items = sp.join_first[q.count];
       if (items && most > 4) hipLaunchKernelGGL(attn_kv4_join_kernel<8>, dim3((unsigned)items), dim3(256), 0, stream, a.f, q, sp);

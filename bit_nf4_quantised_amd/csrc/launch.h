@@ -266,7 +266,7 @@ struct AttnKv4Args {
 bool kv4_codes(int book, Codes& t, float* unit);
 // every sequence's last nq tokens: k and v into the cache, or the cache into k and v
 hipError_t launch_kv4(const Kv4Args& a, int book, bool write, const AttnSeq* seqs, int64_t count, hipStream_t stream);
-size_t attn_kv4_ws_floats(const AttnSeq* seqs, int64_t count, int heads, int kv_heads, int d, int window);
+size_t attn_kv4_ws_floats(const AttnSeq* seqs, int64_t count, int book, int heads, int kv_heads, int d, int window);
 // *fits false: ws_floats are too few, and nothing was enqueued
 hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, int64_t count, float* ws, size_t ws_floats,
                            bool* fits, hipStream_t stream);

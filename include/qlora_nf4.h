@@ -547,12 +547,13 @@ int qlora_kv4_read(const qlora_attn_config *cfg, int64_t count, const qlora_attn
 /* Attention over a cache in 4 bits: qlora_attn_fwd over the bf16 values that k4 and v4 stand for, which are never
  * written to memory. All its rules hold (masks, windows, rows without keys, lse); moreover a NaN in a key or in a
  * value reaches exactly the queries that see it, and gives NaN in their o and lse.
- *   ws    at least qlora_attn_kv4_workspace_bytes(cfg, count, seqs) bytes (0: may be NULL).
+ *   ws    at least qlora_attn_kv4_workspace_bytes(cfg, count, seqs, codebook) bytes (0: may be NULL).
  * Of one sequence ceil(nq * heads / kv_heads / 32) * kv_heads is below 2^24. Errors: as qlora_attn_fwd. */
 int qlora_attn_kv4_fwd(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs, const qlora_attn_tensor *q,
                        const qlora_kv4 *k4, const qlora_kv4 *v4, const qlora_attn_tensor *o, float *lse, void *ws,
                        size_t ws_bytes, hipStream_t stream);
-size_t qlora_attn_kv4_workspace_bytes(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs);
+size_t qlora_attn_kv4_workspace_bytes(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs,
+                                      int32_t codebook);   /* 0 for refused arguments too */
 
 /* Workspace bytes that qlora_linear_fwd and qlora_linear_bwd need for these sizes (the larger of
  * the two). Returns 0 for invalid sizes. */

@@ -844,7 +844,7 @@ int kv4_copy(bool write, const qlora_attn_config* cfg, int64_t count, const qlor
         if (to[i].first < to[i - 1].second) return NF4_ERR_SHAPE;
     }
     const std::vector<nf4::AttnSeq> s = attn_seqs(count, seqs);
-    nf4::Kv4Args a{attn_tensor(k), attn_tensor(v), kv4_tensor(k4), kv4_tensor(v4), cfg->kv_heads, cfg->d, nb, 0.f, {}};
+    nf4::Kv4Args a{attn_tensor(k), attn_tensor(v), kv4_tensor(k4), kv4_tensor(v4), cfg->kv_heads, cfg->d, nb, 0.f, {}, 0};
     nf4::kv4_codes(k4->codebook, a.t, &a.unit);
     return from_hip(nf4::launch_kv4(a, k4->codebook, write, s.data(), count, stream));
   } catch (...) {

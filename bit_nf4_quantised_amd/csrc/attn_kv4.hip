@@ -25,7 +25,6 @@ struct Kv4Split {
 };
 
 __device__ __forceinline__ bool kv4_lost(uint32_t absmax) { return absmax >= kBf16Infinity; }   // absmax has no sign
-constexpr uint32_t kBf16Nan = 0x7FC0u;
 
 // ------------------------------------------------------------------------------------------
 // Few rows: 16 NR rows a workgroup, its keys one range of the sequence's, of which its NW waves take 32-key tiles in

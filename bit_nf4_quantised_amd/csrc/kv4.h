@@ -12,7 +12,7 @@
 
 namespace nf4 {
 
-constexpr uint32_t kBf16Infinity = 0x7F80u;
+constexpr uint32_t kBf16Infinity = 0x7F80u, kBf16Nan = 0x7FC0u;
 
 __device__ __forceinline__ float kv4_step(uint32_t absmax, float unit) { return __fmul_rn(__uint_as_float(absmax << 16), unit); }
 
@@ -45,6 +45,11 @@ struct Kv4E2m1 {
                c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(p, 1.f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(p, 1.f, 3);
     return u32x4{pack_bf16x2(a[1] * step, b[1] * step), pack_bf16x2(c[1] * step, d[1] * step),
                  pack_bf16x2(a[0] * step, b[0] * step), pack_bf16x2(c[0] * step, d[0] * step)};
+  }
+  __device__ __forceinline__ u32x4 in_order(uint32_t p) const {
+    const u32x4 e = eight(p);
+    return u32x4{__builtin_amdgcn_perm(e[2], e[0], 0x05040100u), __builtin_amdgcn_perm(e[2], e[0], 0x07060302u),
+                 __builtin_amdgcn_perm(e[3], e[1], 0x05040100u), __builtin_amdgcn_perm(e[3], e[1], 0x07060302u)};
   }
 };
 // 8 bf16 values in order to the order of eight()

@@ -1,16 +1,20 @@
 // Keys and values to and from a 4-bit cache (gfx950; format in kv4.h).
 //
 // The new tokens of every sequence go behind the others it holds: token i of a sequence with nq new ones, nk in
-// all, goes to the cache's token k0 + nk - nq + i; reading goes the other way. A quad of lanes holds a block,
-// 8 values a lane; quads run over the blocks of a row, rows over the tokens of a head, then over the heads, so
-// that stores to a cache whose heads come first run on. Keys and values are the launch's two rows of workgroups.
+// all, goes to the cache's token k0 + nk - nq + i; reading goes the other way. Two lanes hold a block of a key and of
+// its value, 16 values a lane. A workgroup takes 256 / (2 B) rows (B blocks a row, 1, 2 or 4, the last of them perhaps
+// empty): neighbouring tokens of one head, so that stores to a cache whose heads come first run on, or, where the
+// sequences are shorter than that, tokens of several heads. Where a lane stands takes shifts alone: with divisions that
+// took three times the instructions of the codes, and 8191 tokens of 8 heads, d 128, FP4, 20 us to write and 14 to read.
 //
-// The nearest code to x is decided exactly, ties to the lower code:
-//   NF4   x / absmax is computed to 2^-22 and compared with the codes' midpoints. That decides as the exact quotient:
-//         x and absmax have 8 significant bits, and no quotient of two such numbers is within 1.4e-6 of a
-//         midpoint, relative to it (checked over all of them; the test suite repeats it);
-//   INT4  the code k near 7 x / absmax, put right by comparing 14 x with (2 k +- 1) absmax, which fp32 holds exactly;
-//   FP4   6 |x| against absmax times the seven midpoints of E2M1, exact in fp32 too.
+// The nearest code to x is decided exactly, ties to the lower code, by an approximate quotient (2^-22, relative): x and
+// absmax have 8 significant bits, and a quotient of two such numbers is a tie or well away from one.
+//   NF4   no quotient is within 2.1e-7 of a midpoint (checked over all of them; the test suite repeats it), and the
+//         comparison is good to 1.3e-7: y = 16 x / absmax + 16, whose whole part is a bin of width 1/16 that
+//         holds one midpoint at most; a table in LDS gives the number of midpoints below the bin and the one in it.
+//   INT4  ceil(7 x / absmax - 1/2 - 1e-5), which a tie passes downwards: other quotients are 1e-4 away from one.
+//   FP4   the hardware's conversion of 6 x / absmax, of which 1e-5 of its magnitude is taken away first, so that a
+//         tie falls to the lower code; other quotients are 1e-4 away, relative. -0 becomes 0.
 // Bound by memory: 2 bytes a value on one side, 0.5625 on the other.
 #include "kv4.h"
 
@@ -20,111 +24,150 @@
 
 namespace nf4 {
 
-// largest of the quad's values, as integers
-__device__ __forceinline__ uint32_t umax4(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
-}
-
 // Codes of a block's values. Blocks of very small or large values are scaled by a power of two, so that the reciprocal and
 // the products stay in range (values that this flushes to zero are nearest to the zero code either way).
+struct Kv4Bin {
+  float mid;       // the midpoint in the bin, or infinity
+  uint32_t base;   // midpoints below the bin
+};
 template <int BOOK>
 struct Kv4Codes {
-  float den, rcp, mul;
-  __device__ __forceinline__ explicit Kv4Codes(float a) {
+  float mul, rcp;
+  __device__ __forceinline__ explicit Kv4Codes(uint32_t absmax) {
+    const float a = __uint_as_float(absmax << 16);
     mul = a < 0x1p-60f ? 0x1p100f : a > 0x1p100f ? 0x1p-100f : 1.f;
-    den = a > 0.f ? a * mul : 1.f;
-    rcp = __builtin_amdgcn_rcpf(den);
+    const float den = a > 0.f ? a * mul : 1.f;
+    rcp = (BOOK == 0 ? 16.f : BOOK == 1 ? 6.f : 7.f) * __builtin_amdgcn_rcpf(den);
   }
-  __device__ __forceinline__ uint32_t code(float x) const {
-    const float n = x * mul;
-    if (BOOK == 0) {
-      const float q = n * rcp;
-      uint32_t idx = 0;
-#pragma unroll
-      for (int i = 0; i < 15; ++i) idx += q > 0.5f * (code_value(i) + code_value(i + 1)) ? 1u : 0u;
-      return idx;
+  // two neighbours, x in the high half, into byte j of `codes`
+  __device__ __forceinline__ void two(uint32_t& codes, int j, float x, float y, const Kv4Bin* bins) const {
+    const float n = x * mul, m = y * mul;
+    if (BOOK == 1) {
+      const float u = n * rcp, v = m * rcp;
+      const float a = __fmaf_rn(fabsf(v), -1e-5f, v), b = __fmaf_rn(fabsf(u), -1e-5f, u);
+      if (j == 0) codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, a, b, 1.f, 0);
+      if (j == 1) codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, a, b, 1.f, 1);
+      if (j == 2) codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, a, b, 1.f, 2);
+      if (j == 3) codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, a, b, 1.f, 3);
+      return;
     }
-    if (BOOK == 2) {
-      float k = fminf(fmaxf(ceilf(__fmaf_rn(7.f * n, rcp, -0.5f)), -7.f), 7.f);
-      const float l = 14.f * n;
-      if (k < 7.f && l > __fmaf_rn(2.f * k, den, den)) k += 1.f;
-      else if (k > -7.f && l <= __fmaf_rn(2.f * k, den, -den)) k -= 1.f;
-      return (uint32_t)(int)(k + 7.f);
-    }
-    // |x| past a midpoint, or on it where x is negative (the lower code is then the larger magnitude)
-    constexpr float mid[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.f};
-    const uint32_t neg = __float_as_uint(x) >> 31, m = __float_as_uint(6.f * fabsf(n)) + neg;
-    uint32_t c = 0;
-#pragma unroll
-    for (int i = 0; i < 7; ++i) c += m > __float_as_uint(mid[i] * den) ? 1u : 0u;
-    return c ? c | neg << 3 : 0u;
+    codes |= (code(n, bins) << 4 | code(m, bins)) << (8 * j);
   }
-  static constexpr uint32_t zero = BOOK == 1 ? 0u : 7u;
+  __device__ __forceinline__ uint32_t code(float n, const Kv4Bin* bins) const {
+    if (BOOK == 2) return (uint32_t)ceilf(__fmaf_rn(n, rcp, 6.49999f));
+    const float y = __fmaf_rn(n, rcp, 16.f);
+    const Kv4Bin b = bins[min((uint32_t)fmaxf(y, 0.f), 32u)];
+    return b.base + (y > b.mid ? 1u : 0u);
+  }
+  static __device__ __forceinline__ uint32_t finish(uint32_t codes) {
+    if (BOOK != 1) return codes;
+    const uint32_t some = (codes & 0x77777777u) + 0x77777777u;   // bit 3 of a nibble: its magnitude is not zero
+    return codes & (0x77777777u | some);
+  }
+  static constexpr uint32_t zero = BOOK == 1 ? 0u : 0x77777777u;
 };
 
-// What a lane works on: values 8 e .. 8 e + 7 of the block, the row's token and head.
+// What a lane works on: 16 values of a row's block.
 struct Kv4Place {
-  bool in, values;    // a block of the sequence; its 8 values are the row's (not filling)
-  int64_t token, at;  // of k and v; of the cache
-  int head, block, e;
+  bool in, first, second;   // the block is the sequence's; its half's first and last 8 values are the row's (not filling)
+  int64_t token, at;        // of k and v; of the cache
+  int head, block, half, column;
 };
-__device__ __forceinline__ Kv4Place kv4_place(const AttnSeqs& sq, int tile, int kv_heads, int nb, int d) {
-  const Found f = find_seq(sq, tile);
-  const int u = (tile - f.first) * 256 + (int)threadIdx.x;   // quads of all blocks of the sequence in turn
-  const int blocks = f.seq.nq * kv_heads * nb;
+template <int B>
+__device__ __forceinline__ Kv4Place kv4_place(const AttnSeqs& sq, const Kv4Args& a) {
+  constexpr int ROWS = 128 / B;
+  const Found f = find_seq(sq, (int)blockIdx.x);
+  const int tokens = 1 << a.log_tokens, heads = ROWS >> a.log_tokens;   // of a workgroup
+  const int across = (a.kv_heads + heads - 1) / heads, tile = (int)blockIdx.x - f.first;
+  const int t = (int)threadIdx.x % (2 * B), row = (int)threadIdx.x / (2 * B);
   Kv4Place p;
-  const int blk = min(u >> 2, blocks - 1);
-  p.in = (u >> 2) < blocks;
-  const int row = blk / nb, t = row % f.seq.nq;
-  p.block = blk % nb;
-  p.head = row / f.seq.nq;
-  p.token = f.seq.q0 + t;
-  p.at = f.seq.k0 + (f.seq.nk - f.seq.nq) + t;
-  p.e = u & 3;
-  p.values = p.in && 32 * p.block + 8 * p.e < d;
+  const int i = tile / across * tokens + (row & (tokens - 1));
+  p.head = tile % across * heads + (row >> a.log_tokens);
+  p.block = t >> 1;
+  p.half = t & 1;
+  p.column = 16 * t;
+  p.in = i < f.seq.nq && p.head < a.kv_heads && p.block < a.nb;
+  p.first = p.in && p.column < a.d;
+  p.second = p.in && p.column + 8 < a.d;
+  p.token = f.seq.q0 + i;
+  p.at = f.seq.k0 + (f.seq.nk - f.seq.nq) + i;
   return p;
 }
 
-template <int BOOK>
+template <int BOOK, int B>
 __global__ __launch_bounds__(256) void kv4_write_kernel(const Kv4Args a, const AttnSeqs sq) {
-  const Kv4Place p = kv4_place(sq, (int)blockIdx.x, a.kv_heads, a.nb, a.d);
-  const AttnTensor& src = blockIdx.y ? a.v : a.k;
-  const Kv4Tensor& dst = blockIdx.y ? a.v4 : a.k4;
-  u32x4 x = u32x4{0u, 0u, 0u, 0u};
-  if (p.values)
-    x = *reinterpret_cast<const u32x4*>(src.p + p.token * src.token + (int64_t)p.head * src.head + 32 * p.block + 8 * p.e);
-  uint32_t m = 0;
+  __shared__ Kv4Bin bins[33];
+  if (BOOK == 0 && threadIdx.x < 33) {
+    Kv4Bin b{__builtin_inff(), 0u};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) m = max(m, max(x[k] & 0x7FFFu, x[k] >> 16 & 0x7FFFu));
-  m = umax4(m);
-  const Kv4Codes<BOOK> c(__uint_as_float(m << 16));
-  uint32_t o = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t lo = c.code(__uint_as_float(x[k] << 16)), hi = c.code(__uint_as_float(x[k] & 0xFFFF0000u));
-    o |= (lo << 4 | hi) << (8 * k);
+    for (int i = 0; i < 15; ++i) {
+      const double m = 8.0 * ((double)code_value(i) + (double)code_value(i + 1)) + 16.0;
+      if (m < (double)threadIdx.x) ++b.base;
+      else if (m < (double)threadIdx.x + 1.0) b.mid = (float)m;
+    }
+    bins[threadIdx.x] = b;
   }
-  if (m >= kBf16Infinity) o = 0x11111111u * Kv4Codes<BOOK>::zero;
-  if (p.in) {
-    const int64_t at = p.at * dst.token + (int64_t)p.head * dst.head + p.block;
-    *reinterpret_cast<uint32_t*>(dst.codes + 16 * at + 4 * p.e) = o;
-    if (p.e == 0) dst.absmax[at] = (uint16_t)m;
+  const Kv4Place p = kv4_place<B>(sq, a);
+  u32x4 x[2][2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const AttnTensor& src = w ? a.v : a.k;
+    const uint16_t* from = src.p + p.token * src.token + (int64_t)p.head * src.head + p.column;
+    x[w][0] = x[w][1] = u32x4{0u, 0u, 0u, 0u};
+    if (p.first) x[w][0] = *reinterpret_cast<const u32x4*>(from);
+    if (p.second) x[w][1] = *reinterpret_cast<const u32x4*>(from + 8);
+  }
+  if (BOOK == 0) __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t m = 0, h = 0;   // largest magnitudes, of the low and high halves
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      m = max(m, x[w][k / 4][k % 4] & 0x7FFFu);
+      h = max(h, x[w][k / 4][k % 4] & 0x7FFF0000u);
+    }
+    m = max(m, h >> 16);
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));   // the block's other lane
+    const Kv4Codes<BOOK> c(m);
+    u32x2 o = u32x2{0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t e = o[k / 4];
+      c.two(e, k % 4, __uint_as_float(x[w][k / 4][k % 4] << 16), __uint_as_float(x[w][k / 4][k % 4] & 0xFFFF0000u), bins);
+      o[k / 4] = e;
+    }
+    o[0] = m >= kBf16Infinity ? c.zero : c.finish(o[0]);
+    o[1] = m >= kBf16Infinity ? c.zero : c.finish(o[1]);
+    if (p.in) {
+      const Kv4Tensor& dst = w ? a.v4 : a.k4;
+      const int64_t at = p.at * dst.token + (int64_t)p.head * dst.head + p.block;
+      *reinterpret_cast<u32x2*>(dst.codes + 16 * at + 8 * p.half) = o;
+      if (p.half == 0) dst.absmax[at] = (uint16_t)m;
+    }
   }
 }
 
+template <class Deq, int B>
 __global__ __launch_bounds__(256) void kv4_read_kernel(const Kv4Args a, const AttnSeqs sq) {
-  const Kv4Place p = kv4_place(sq, (int)blockIdx.x, a.kv_heads, a.nb, a.d);
-  if (!p.values) return;
-  const AttnTensor& dst = blockIdx.y ? a.v : a.k;
-  const Kv4Tensor& src = blockIdx.y ? a.v4 : a.k4;
-  const int64_t at = p.at * src.token + (int64_t)p.head * src.head + p.block;
-  const uint32_t codes = *reinterpret_cast<const uint32_t*>(src.codes + 16 * at + 4 * p.e);
-  const uint32_t m = src.absmax[at];
-  u32x4 o = Kv4Table(a.t, kv4_step(m, a.unit)).in_order(codes);
-  // infinity stands for NaN with every code
-  if (m >= kBf16Infinity) o = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
-  *reinterpret_cast<u32x4*>(dst.p + p.token * dst.token + (int64_t)p.head * dst.head + 32 * p.block + 8 * p.e) = o;
+  const Kv4Place p = kv4_place<B>(sq, a);
+  if (!p.first) return;
+  u32x2 codes[2];
+  uint32_t m[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const Kv4Tensor& src = w ? a.v4 : a.k4;
+    const int64_t at = p.at * src.token + (int64_t)p.head * src.head + p.block;
+    codes[w] = *reinterpret_cast<const u32x2*>(src.codes + 16 * at + 8 * p.half);
+    m[w] = src.absmax[at];
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const AttnTensor& dst = w ? a.v : a.k;
+    uint16_t* to = dst.p + p.token * dst.token + (int64_t)p.head * dst.head + p.column;
+    const Deq q(a.t, kv4_step(m[w] >= kBf16Infinity ? kBf16Nan : m[w], a.unit));   // infinity stands for NaN with every code
+    *reinterpret_cast<u32x4*>(to) = q.in_order(codes[w][0]);
+    if (p.second) *reinterpret_cast<u32x4*>(to + 8) = q.in_order(codes[w][1]);
+  }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -144,19 +187,32 @@ bool kv4_codes(int book, Codes& t, float* unit) {
   return true;
 }
 
-static int kv4_tiles(const AttnSeq& s, const Kv4Args& a) { return (int)ceil64((int64_t)s.nq * a.kv_heads * a.nb, 64); }
+// 1, 2 or 4 blocks a row; as many tokens a workgroup as it has rows, or the power of two that holds the longest sequence's
+template <int B>
+static void kv4_rows(Kv4Args a, int book, bool write, const std::vector<AttnSeq>& v, hipStream_t stream) {
+  constexpr int kRows = 128 / B;
+  int longest = 1;
+  for (const AttnSeq& s : v) longest = std::max(longest, s.nq);
+  a.log_tokens = 0;
+  while ((1 << a.log_tokens) < std::min(longest, kRows)) ++a.log_tokens;
+  const int64_t across = ceil64(a.kv_heads, kRows >> a.log_tokens);
+  for (size_t from = 0; from < v.size();) {
+    const AttnSeqs q = pack_seqs(v, from, 1, [&](const AttnSeq& s) { return ceil64(s.nq, 1 << a.log_tokens) * across; });
+    from += (size_t)q.count;
+    const dim3 grid((unsigned)q.first[q.count]), wg(256);
+    if (!write && book == 1) hipLaunchKernelGGL((kv4_read_kernel<Kv4E2m1, B>), grid, wg, 0, stream, a, q);
+    else if (!write) hipLaunchKernelGGL((kv4_read_kernel<Kv4Table, B>), grid, wg, 0, stream, a, q);
+    else if (book == 0) hipLaunchKernelGGL((kv4_write_kernel<0, B>), grid, wg, 0, stream, a, q);
+    else if (book == 1) hipLaunchKernelGGL((kv4_write_kernel<1, B>), grid, wg, 0, stream, a, q);
+    else hipLaunchKernelGGL((kv4_write_kernel<2, B>), grid, wg, 0, stream, a, q);
+  }
+}
 
 hipError_t launch_kv4(const Kv4Args& a, int book, bool write, const AttnSeq* seqs, int64_t count, hipStream_t stream) {
   const std::vector<AttnSeq> v = by_work(seqs, count, false);
-  for (size_t from = 0; from < v.size();) {
-    const AttnSeqs q = pack_seqs(v, from, 2, [&](const AttnSeq& s) { return kv4_tiles(s, a); });
-    from += (size_t)q.count;
-    const dim3 grid((unsigned)q.first[q.count], 2), wg(256);
-    if (!write) hipLaunchKernelGGL(kv4_read_kernel, grid, wg, 0, stream, a, q);
-    else if (book == 0) hipLaunchKernelGGL(kv4_write_kernel<0>, grid, wg, 0, stream, a, q);
-    else if (book == 1) hipLaunchKernelGGL(kv4_write_kernel<1>, grid, wg, 0, stream, a, q);
-    else hipLaunchKernelGGL(kv4_write_kernel<2>, grid, wg, 0, stream, a, q);
-  }
+  if (a.nb == 1) kv4_rows<1>(a, book, write, v, stream);
+  else if (a.nb == 2) kv4_rows<2>(a, book, write, v, stream);
+  else kv4_rows<4>(a, book, write, v, stream);
   return hipGetLastError();
 }
 

@@ -254,6 +254,7 @@ struct Kv4Args {
   int kv_heads, d, nb;
   float unit;
   Codes t;
+  int log_tokens;                    // tokens of a workgroup; set by launch_kv4
 };
 struct AttnKv4Args {
   AttnFwdArgs f;                     // k and v unused

@@ -235,10 +235,11 @@ struct RopeArgs {
   int heads, kv_heads, d, rot, interleaved;
   float eps, factor;
   uint64_t turn[64];                 // the pairs' frequencies, in 2^-64 turns a position
+  int per, q_groups;                 // heads of an item, workgroups of queries; set by the launchers
 };
 hipError_t launch_rope_fwd(const RopeArgs& a, hipStream_t stream);
 // dqw, dkw: [d] or null; part holds rope_bwd_ws_floats floats where one is asked for
-size_t rope_bwd_ws_floats(const RopeArgs& a);
+size_t rope_bwd_ws_floats(RopeArgs a);
 hipError_t launch_rope_bwd(const RopeArgs& a, float* dqw, float* dkw, int accumulate, float* part, hipStream_t stream);
 
 // ---- Keys and values in 4 bits (kv4.hip, attn_kv4.hip; format in kv4.h). Block b of (token, head) is block

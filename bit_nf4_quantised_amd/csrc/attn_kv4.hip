@@ -23,6 +23,25 @@ struct Kv4Split {
   int64_t row0[kAttnSeqs];        // first record of a sequence in part
   int join_first[kAttnSeqs + 1];  // prefix sums of rows x key heads over the sequences of several ranges
 };
+// A workgroup's sequence with its ranges. Lane i reads all entries of sequence i before the workgroup knows which it needs: a
+// second trip to the kernel arguments would cost its start about 0.4 us (one token of 601 keys 6.4 us, and 6.0 so).
+struct Kv4Found {
+  Found at;
+  int lo, chunk, ranges;
+  int64_t row0;
+};
+__device__ __forceinline__ Kv4Found kv4_find(const AttnSeqs& sq, const Kv4Split& sp, int tile) {
+  const int lane = threadIdx.x & 63;
+  const int lo = sp.lo[lane], chunk = sp.chunk[lane], ranges = sp.ranges[lane];
+  const int64_t row0 = sp.row0[lane];
+  Kv4Found f;
+  f.at = find_seq(sq, tile);
+  f.lo = lane_value(lo, f.at.index);
+  f.chunk = lane_value(chunk, f.at.index);
+  f.ranges = lane_value(ranges, f.at.index);
+  f.row0 = lane_value(row0, f.at.index);
+  return f;
+}
 
 __device__ __forceinline__ bool kv4_lost(uint32_t absmax) { return absmax >= kBf16Infinity; }   // absmax has no sign
 
@@ -173,15 +192,15 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = a.f.heads / a.f.kv_heads;
   const Unit u = unit_of((int)blockIdx.x, a.f.kv_heads, 1);
-  const Found at_seq = find_seq(sq, u.tile);
-  const AttnSeq s = at_seq.seq;
-  const int si = at_seq.index, local = u.tile - at_seq.first;
-  const int ns = sp.ranges[si], split = local % ns, rt = local / ns;
+  const Kv4Found found = kv4_find(sq, sp, u.tile);
+  const AttnSeq s = found.at.seq;
+  const int local = u.tile - found.at.first;
+  const int ns = found.ranges, split = local % ns, rt = local / ns;
   const int shift = s.nk - s.nq, rows = s.nq * G;
   const int t0 = rt * R / G, t1 = min(rows - 1, rt * R + R - 1) / G;   // tokens of the row tile
   const Range first = visible(t0 + shift, s.nk, a.f.causal, a.f.window), last = visible(t1 + shift, s.nk, a.f.causal, a.f.window);
   // tiles are counted from the first key that the sequence's first row sees (none before it is read)
-  const int lo = sp.lo[si], chunk = sp.chunk[si];
+  const int lo = found.lo, chunk = found.chunk;
   const int k_lo = lo + max((first.lo - lo) & ~(BN - 1), split * chunk);
   const int k_hi = min(last.hi, lo + (split + 1) * chunk);
   const int64_t kbase = s.k0 * a.k4.token + (int64_t)u.kvh * a.k4.head, vbase = s.k0 * a.v4.token + (int64_t)u.kvh * a.v4.head;
@@ -299,7 +318,7 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(
       else *o = pack_bf16x2(v[0] * inv, v[1] * inv);
       if (c0 == 0 && a.f.lse) a.f.lse[(int64_t)head * a.f.lse_stride + s.q0 + tok] = lse_of(mxc, l);
     } else {
-      float* part = sp.part + (sp.row0[si] + ((int64_t)grow * a.f.kv_heads + u.kvh) * ns + split) * (int64_t)(a.f.d + 8);
+      float* part = sp.part + (found.row0 + ((int64_t)grow * a.f.kv_heads + u.kvh) * ns + split) * (int64_t)(a.f.d + 8);
       if constexpr (E == 8) {
         *reinterpret_cast<f32x4*>(part + c0) = f32x4{v[0], v[1], v[2], v[3]};
         *reinterpret_cast<f32x4*>(part + c0 + 4) = f32x4{v[4], v[5], v[6], v[7]};
@@ -375,17 +394,17 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = a.f.heads / a.f.kv_heads;
   const Unit u = unit_of((int)blockIdx.x, a.f.kv_heads, 1);
-  const Found at_seq = find_seq(sq, u.tile);
-  const AttnSeq s = at_seq.seq;
-  const int si = at_seq.index, local = at_seq.next - 1 - u.tile;   // from the last rows (the most keys when causal) to the first
-  const int ns = sp.ranges[si], split = local % ns, rt = local / ns;
+  const Kv4Found found = kv4_find(sq, sp, u.tile);
+  const AttnSeq s = found.at.seq;
+  const int local = found.at.next - 1 - u.tile;   // from the last rows (the most keys when causal) to the first
+  const int ns = found.ranges, split = local % ns, rt = local / ns;
   const int shift = s.nk - s.nq, rows = s.nq * G;
   const int row = rt * R + wave * 32 + (lane & 31);
   const int tok = min(row, rows - 1) / G, head = u.kvh * G + min(row, rows - 1) % G;
   auto sees = [&](int r) { return visible(min(r, rows - 1) / G + shift, s.nk, a.f.causal, a.f.window); };
   const Range mine = visible(tok + shift, s.nk, a.f.causal, a.f.window);
   const Range wa = sees(rt * R + wave * 32), wb = sees(rt * R + wave * 32 + 31);   // of the wave's first and last row
-  const int lo = sp.lo[si], chunk = sp.chunk[si];
+  const int lo = found.lo, chunk = found.chunk;
   const int k_lo = lo + max((sees(rt * R).lo - lo) & ~(BN - 1), split * chunk);
   const int k_hi = min(sees(rt * R + R - 1).hi, lo + (split + 1) * chunk);
   const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
@@ -475,7 +494,7 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
     }
     if (in && a.f.lse && lane < 32) a.f.lse[(int64_t)head * a.f.lse_stride + s.q0 + tok] = lse_of(acc.mc, l);
   } else {
-    float* part = sp.part + (sp.row0[si] + ((int64_t)row * a.f.kv_heads + u.kvh) * ns + split) * (int64_t)(a.f.d + 8);
+    float* part = sp.part + (found.row0 + ((int64_t)row * a.f.kv_heads + u.kvh) * ns + split) * (int64_t)(a.f.d + 8);
 #pragma unroll
     for (int i = 0; i < 2 * DT; ++i) {
       const int c = 16 * i + 8 * (lane >> 5);
@@ -501,22 +520,28 @@ __global__ __launch_bounds__(256) void attn_kv4_join_kernel(const AttnFwdArgs a,
   constexpr int ITEMS = 8 / S;
   const int lane = threadIdx.x & 63, grp = (int)threadIdx.x >> 5;
   const int G = a.heads / a.kv_heads;
-  const int item = (int)blockIdx.x * ITEMS + grp / S, slice = grp % S, all = sp.join_first[sq.count];
-  // sequences with one range have no items; the wave's items may be of two sequences
-  const int f = lane < sq.count ? sp.join_first[lane] : 0x7FFFFFFF;
-  const int i0 = __builtin_amdgcn_readfirstlane(min(item, all - 1));
+  const int slice = grp % S;
+  // sequences with one range have no items; as kv4_find, one trip to the arguments
+  const int f = lane < sq.count ? sp.join_first[lane] : 0x7FFFFFFF, next = sp.join_first[lane + 1], ranges = sp.ranges[lane];
+  const int64_t row0 = sp.row0[lane], q0 = sq.seq[lane].q0;
+  const int all = lane_value(next, sq.count - 1);
+  const int want = (int)blockIdx.x * ITEMS + grp / S, item = min(want, all - 1);
+  const int i0 = __builtin_amdgcn_readfirstlane(item);
   int si = (int)__popcll(__ballot(f <= i0)) - 1;
-  if constexpr (ITEMS > 1) {
-    while (__any(min(item, all - 1) >= sp.join_first[si + 1])) {   // whole waves step on until each half has its own
-      if (min(item, all - 1) >= sp.join_first[si + 1]) ++si;
-    }
+  int first = lane_value(f, si), ns = lane_value(ranges, si);
+  int64_t base = lane_value(row0, si), tok0 = lane_value(q0, si);
+  if (ITEMS > 1 && __any(item >= lane_value(next, si))) {   // the wave's second item is of a later sequence
+    while (item >= sp.join_first[si + 1]) ++si;
+    first = sp.join_first[si];
+    ns = sp.ranges[si];
+    base = sp.row0[si];
+    tok0 = sq.seq[si].q0;
   }
-  const AttnSeq s = sq.seq[si];
-  const int local = min(item, all - 1) - sp.join_first[si], ns = sp.ranges[si];
+  const int local = item - first;
   const int grow = local / a.kv_heads, kvh = local % a.kv_heads;
   const int tok = grow / G, head = kvh * G + grow % G;
   const int64_t step = a.d + 8;
-  const float* part = sp.part + (sp.row0[si] + (int64_t)local * ns) * step;
+  const float* part = sp.part + (base + (int64_t)local * ns) * step;
   const int c = 4 * (lane & 31), cc = min(c, a.d - 4);   // d is a multiple of 8
   float mx = -INFINITY, l = 0.f;
   f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -576,12 +601,12 @@ __global__ __launch_bounds__(256) void attn_kv4_join_kernel(const AttnFwdArgs a,
     }
     mx = top;
   }
-  if (item >= all) return;
+  if (want >= all) return;
   const float inv = inverse_sum(l);
   if (c < a.d)
-    *reinterpret_cast<u32x2*>(a.o.p + (s.q0 + tok) * a.o.token + (int64_t)head * a.o.head + c) =
+    *reinterpret_cast<u32x2*>(a.o.p + (tok0 + tok) * a.o.token + (int64_t)head * a.o.head + c) =
         u32x2{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
-  if (a.lse && (lane & 31) == 0) a.lse[(int64_t)head * a.lse_stride + s.q0 + tok] = lse_of(mx, l);
+  if (a.lse && (lane & 31) == 0) a.lse[(int64_t)head * a.lse_stride + tok0 + tok] = lse_of(mx, l);
 }
 
 // ------------------------------------------------------------------------------------------

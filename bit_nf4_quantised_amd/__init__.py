@@ -742,9 +742,9 @@ def qlora_attn_bwd(seqs: AttnSeqs, q, k, v, o, lse, dout, dq, dk, dv, scale: flo
 
 # ------------------------------------------------------------------------- rotary positions
 class Rope:
-    """Rotary positions, marshalled once (for all layers of a model): the first `rot` features of a head in pairs,
-    (2i, 2i+1) if interleaved, else (i, i + rot/2), pair i turned by inv_freq[i] radians a position, by default
-    base ** (-2 i / rot). `factor` multiplies the rotated features.
+    """Rotary positions, marshalled once (for all layers of a model; not changed afterwards): the first `rot`
+    features of a head in pairs, (2i, 2i+1) if interleaved, else (i, i + rot/2), pair i turned by inv_freq[i] radians
+    a position, by default base ** (-2 i / rot). `factor` multiplies the rotated features.
 
     For contexts longer than the model was trained on, `stretch` divides the frequencies: all of them when `trained`
     is 0 (positions are interpolated); else those that make less than `low` turns in `trained` positions, while
@@ -752,7 +752,7 @@ class Rope:
 
     def __init__(self, rot: int, base: float = 10000.0, interleaved: bool = False, stretch: float = 1.0, trained: int = 0,
                  low: float = 1.0, high: float = 4.0, factor: float = 1.0, inv_freq=None):
-        self.rot, self.interleaved, self.factor = int(rot), bool(interleaved), float(factor)
+        self._made = int(rot), bool(interleaved), float(factor)
         if inv_freq is None:
             if not stretch > 0 or not base > 0 or (trained and not high > low):
                 raise ValueError("base and stretch must be above 0, and high above low")
@@ -761,44 +761,81 @@ class Rope:
                 f = float(base) ** (-2.0 * i / self.rot)
                 keep = min(1.0, max(0.0, (trained * f / (2 * math.pi) - low) / (high - low))) if trained else 0.0
                 inv_freq.append(f * (keep + (1.0 - keep) / stretch))
-        self.inv_freq = tuple(float(f) for f in inv_freq)
-        if len(self.inv_freq) * 2 != self.rot:
+        self._inv_freq = tuple(float(f) for f in inv_freq)
+        if len(self._inv_freq) * 2 != self.rot:
             raise ValueError("one frequency for each of the rot / 2 pairs")
-        self._freq = (ctypes.c_double * max(len(self.inv_freq), 1))(*self.inv_freq)
-        self._last = (None, None)   # as AttnSeqs: what the last configuration was made of, and it
+        self._freq = (ctypes.c_double * max(len(self._inv_freq), 1))(*self._inv_freq)
+        self._plans = {}   # configuration and strides of the calls' tensors, by their shapes and strides
 
-    def _config(self, q, k, eps):
+    # what the plans were made with: read only
+    rot = property(lambda self: self._made[0])
+    interleaved = property(lambda self: self._made[1])
+    factor = property(lambda self: self._made[2])
+    inv_freq = property(lambda self: self._inv_freq)
+
+    def _plan(self, key, eps, qs, ks):
+        """Checks the shapes of a call's query-like and key-like tensors and marshals what does not change."""
+        q, k = qs[0], ks[0]
+        for ts, like in ((qs, q), (ks, k)):
+            for t in ts:
+                if t is not None and (like is None or t.dim() != 3 or t.shape != like.shape):
+                    raise ValueError("shape mismatch: heads are [tokens, heads, d], gradients and outputs like their inputs")
+        if any((t is None) != (k is None) for t in ks[:2]) or (k is not None and (k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2])):
+            raise ValueError("shape mismatch: keys go with keys, of the queries' tokens and head size")
+        at = array("q")
+        for t in qs + ks:
+            at.extend(_attn_tensors((t, t.shape))[0] if t is not None else (0, 0, 0))
         tokens, heads, d = q.shape
-        kv_heads = 0 if k is None else k.shape[1]
-        key = (tokens, heads, kv_heads, d, eps)
-        last, cfg = self._last
-        if last != key:
-            cfg = CRopeConfig(heads, kv_heads, d, self.rot, int(self.interleaved), eps, self.factor, tokens)
-            self._last = (key, cfg)
-        return ctypes.byref(cfg)
+        cfg = CRopeConfig(heads, 0 if k is None else k.shape[1], d, self.rot, int(self.interleaved), eps, self.factor, tokens)
+        if len(self._plans) >= 256:   # a program of ever new shapes
+            self._plans.clear()
+        self._plans[key] = plan = (at, cfg, ctypes.byref(cfg), tokens)
+        return plan
+
+    def _tensors(self, eps, qs, ks):
+        """The qlora_attn_tensor structures of the tensors (None: not there), as an array to be kept until the library has
+        read them, their addresses, the configuration, and the tokens."""
+        key = [eps]
+        for t in qs + ks:
+            if t is None:
+                key.append(None)
+            else:
+                key.append(t.shape)
+                key.append(t.stride())
+        key = tuple(key)
+        plan = self._plans.get(key) or self._plan(key, eps, qs, ks)
+        v = plan[0][:]
+        at = v.buffer_info()[0]
+        ptrs = []
+        for i, t in enumerate(qs + ks):
+            if t is None:
+                ptrs.append(None)
+                continue
+            if t.dtype not in _BF16:
+                _dtype(t, *_BF16)
+            if not t.is_cuda:
+                raise ValueError("tensor must live on the GPU")
+            v[3 * i] = t.data_ptr()
+            ptrs.append(at + 24 * i)
+        return v, ptrs, plan[2], plan[3]
 
 
-def _rope_positions(rope, positions, q):
+def _rope_positions(rope, positions, tokens):
     if positions is None:
         if rope.rot:
             raise ValueError("positions are needed to rotate")
         return None
-    if positions.shape != q.shape[:1]:
+    if positions.shape != (tokens,):
         raise ValueError("positions must hold one value a token")
     return _dptr(positions, (torch.int64,))
 
 
 def _rope_weight(w, like):
-    if w is not None and (like is None or w.numel() != like.shape[2]):
+    if w is None:
+        return None
+    if like is None or w.numel() != like.shape[2]:
         raise ValueError("a head weight must hold d values")
     return _dptr(w, _BF16)
-
-
-def _rope_pair(q, k, name):
-    """Shapes of the query and key rows of a call; k may be None."""
-    if q.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2])):
-        raise ValueError(f"shape mismatch: {name} are [tokens, heads, d] of the same tokens and head size")
-    return q.shape, None if k is None else k.shape
 
 
 def qlora_rope_fwd(rope: Rope, positions, q, k, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -806,17 +843,9 @@ def qlora_rope_fwd(rope: Rope, positions, q, k, q_out, k_out, q_weight=None, k_w
     """Query and key heads [tokens, heads, d] (bf16, tokens and heads may be strided), normed over d where a weight
     [d] is given, then rotated by their tokens' positions (int64 [tokens]). k and k_out may be None; an output may
     be its input."""
-    sq, sk = _rope_pair(q, k, "q and k")
-    if (k is None) != (k_out is None):
-        raise ValueError("k and k_out go together")
-    pq, pw = _rope_positions(rope, positions, q), (_rope_weight(q_weight, q), _rope_weight(k_weight, k))
-    if k is None:
-        keep, tq, to = _attn_tensors((q, sq), (q_out, sq))
-        tk = tko = None
-    else:
-        keep, tq, to, tk, tko = _attn_tensors((q, sq), (q_out, sq), (k, sk), (k_out, sk))
-    _check(lib.qlora_rope_fwd(rope._config(q, k, eps), rope._freq, pq, tq, tk, *pw, to, tko, _stream(stream)),
-           "qlora_rope_fwd")
+    keep, (tq, to, tk, tko), cfg, tokens = rope._tensors(eps, (q, q_out), (k, k_out))
+    _check(lib.qlora_rope_fwd(cfg, rope._freq, _rope_positions(rope, positions, tokens), tq, tk, _rope_weight(q_weight, q),
+                              _rope_weight(k_weight, k), to, tko, _stream(stream)), "qlora_rope_fwd")
 
 
 def qlora_rope_bwd(rope: Rope, positions, dq_out, dk_out, dq, dk, q=None, k=None, q_weight=None, k_weight=None,
@@ -824,40 +853,23 @@ def qlora_rope_bwd(rope: Rope, positions, dq_out, dk_out, dq, dk, q=None, k=None
                    stream=None) -> None:
     """Backward of qlora_rope_fwd: dq, dk from the gradients dq_out, dk_out of its outputs, and, where asked for, the
     weights' (float32 [d], added to with accumulate). Normed heads need the forward's inputs q and k."""
-    sq, sk = _rope_pair(dq_out, dk_out, "dq_out and dk_out")
-    if (dk_out is None) != (dk is None):
-        raise ValueError("dk_out and dk go together")
     if (q_weight is not None and q is None) or (k_weight is not None and k is None):
         raise ValueError("the backward of normed heads needs their inputs")
-    pp = _rope_positions(rope, positions, dq_out)
-    pw = _rope_weight(q_weight, dq_out), _rope_weight(k_weight, dk_out)
-    for dw, w in ((dq_weight, q_weight), (dk_weight, k_weight)):
-        if dw is not None and (w is None or dw.numel() != sq[2]):
-            raise ValueError("a head weight's gradient goes with the weight and holds d values")
-    pdw = _dptr(dq_weight, _F32), _dptr(dk_weight, _F32)
-    pairs = [(dq_out, sq), (dq, sq)]
-    if q_weight is not None:
-        pairs.append((q, sq))
-    if dk is not None:
-        pairs += [(dk_out, sk), (dk, sk)]
-        if k_weight is not None:
-            pairs.append((k, sk))
-    keep, *ts = _attn_tensors(*pairs)
-    ts = iter(ts)
-    tgo, tdq = next(ts), next(ts)
-    tq = next(ts) if q_weight is not None else None
-    tgk = tdk = tk = None
-    if dk is not None:
-        tgk, tdk = next(ts), next(ts)
-        tk = next(ts) if k_weight is not None else None
-    cfg = rope._config(dq_out, dk_out, eps)
+    keep, (tgo, tdq, tq, tgk, tdk, tk), cfg, tokens = rope._tensors(
+        eps, (dq_out, dq, q if q_weight is not None else None), (dk_out, dk, k if k_weight is not None else None))
+    pdw = None, None
     nbytes = 0
-    if pdw[0] is not None or pdw[1] is not None:
+    if dq_weight is not None or dk_weight is not None:
+        for dw, w in ((dq_weight, q_weight), (dk_weight, k_weight)):
+            if dw is not None and (w is None or dw.numel() != w.numel()):
+                raise ValueError("a head weight's gradient goes with the weight and holds d values")
+        pdw = _dptr(dq_weight, _F32), _dptr(dk_weight, _F32)
         if ws is None:
             ws = _scratch(max(int(lib.qlora_rope_workspace_bytes(cfg)), 256), dq.device, stream)
         nbytes = ws.numel() * ws.element_size()
-    _check(lib.qlora_rope_bwd(cfg, rope._freq, pp, tq, tk, *pw, tgo, tgk, tdq, tdk, *pdw, int(bool(accumulate)),
-                              _ptr(ws), nbytes, _stream(stream)), "qlora_rope_bwd")
+    _check(lib.qlora_rope_bwd(cfg, rope._freq, _rope_positions(rope, positions, tokens), tq, tk, _rope_weight(q_weight, dq_out),
+                              _rope_weight(k_weight, dk_out), tgo, tgk, tdq, tdk, *pdw, int(bool(accumulate)),
+                              None if ws is None else _ptr(ws), nbytes, _stream(stream)), "qlora_rope_bwd")
 
 
 # ------------------------------------------------------------------------- a key/value cache in 4 bits

@@ -706,12 +706,19 @@ int check_rope_pair(const qlora_rope_config* c, const qlora_attn_tensor* q, cons
   return check_attn_tensor(k, c->tokens, c->kv_heads, c->d, output);
 }
 
-// turns a position, modulo one, in units of 2^-64. Without a library call for frequencies below one turn, as nearly all
-// are: 64 of them take 1 us of every call, and 11 us with ldexpl and floorl.
+// turns a position, modulo one, in units of 2^-64. For frequencies in (0, 2), as nearly all are, the double's 53 bits times
+// 2^64 / (2 pi), shifted to their place: 64 of them take 0.1 us of a call, and 11 us by long division and ldexpl.
 uint64_t turn_of(double radians) {
+  uint64_t bits;
+  memcpy(&bits, &radians, 8);
+  const int e = (int)(bits >> 52);   // sign and exponent
+  if (e > 0 && e < 1024) {
+    const unsigned __int128 t = (unsigned __int128)((bits & ((uint64_t(1) << 52) - 1)) | uint64_t(1) << 52) * 0x28BE60DB9391054BULL;
+    const int shift = 1075 - e;   // the value is the 53 bits times 2^(e - 1075)
+    return shift < 128 ? (uint64_t)(t >> shift) : 0;
+  }
   long double t = (long double)radians * 0.15915494309189533576888376337251436L;   // 1 / (2 pi)
-  if (!(t >= 0.0L && t < 1.0L)) t -= floorl(t);
-  t *= 18446744073709551616.0L;
+  t = (t - floorl(t)) * 18446744073709551616.0L;
   return t >= 18446744073709551616.0L ? 0 : (uint64_t)t;
 }
 

@@ -8,7 +8,8 @@
 // in the same order, and the output's columns back into theirs.
 //
 // A value block that stands for NaN enters as zeros, and the same block of its key as NaN: a query that sees the
-// key gets NaN through the score, and one that does not gets nothing of it (0 times NaN would be NaN).
+// key gets NaN through the score, and one that does not gets nothing of it (0 times NaN would be NaN). A key's block
+// of infinite maximum is NaN with every code: a score of minus infinity would pass for a hidden key.
 //
 // Keys of a range that end within a tile: the lanes past it take the last key again, which the mask hides.
 #include "attn.h"
@@ -70,7 +71,7 @@ struct Kv4Few<128> {
       va[i] = a.v4.absmax[vt + vo];
     }
   }
-  __device__ __forceinline__ float step(int i, float unit) const { return kv4_step(kv4_lost(va[i]) ? kBf16Nan : ka[i], unit); }
+  __device__ __forceinline__ float step(int i, float unit) const { return kv4_step(kv4_lost(max(ka[i], va[i])) ? kBf16Nan : ka[i], unit); }
   template <class Deq>
   __device__ __forceinline__ void values(uint16_t* tile, const AttnKv4Args& a, int lane) const {
 #pragma unroll
@@ -103,7 +104,7 @@ struct Kv4Few<64> {
     v = *reinterpret_cast<const u32x4*>(a.v4.codes + 16 * vt + 16u * vo);
     va = a.v4.absmax[vt + vo];
   }
-  __device__ __forceinline__ float step(int i, float unit) const { return kv4_step(kv4_lost(kva[i]) ? kBf16Nan : ka[i], unit); }
+  __device__ __forceinline__ float step(int i, float unit) const { return kv4_step(kv4_lost(max(ka[i], kva[i])) ? kBf16Nan : ka[i], unit); }
   template <class Deq>
   __device__ __forceinline__ void values(uint16_t* tile, const AttnKv4Args& a, int lane) const {
     const Deq q(a.t, kv4_step(kv4_lost(va) ? 0u : va, a.unit));
@@ -365,7 +366,7 @@ struct Kv4Many {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const bool val = value(tid, i);
-      const Deq q(a.t, kv4_step(kv4_lost(vm[i]) ? (val ? 0u : kBf16Nan) : m[i], a.unit));
+      const Deq q(a.t, kv4_step(kv4_lost(max(m[i], vm[i])) ? (val ? 0u : kBf16Nan) : m[i], a.unit));
       uint16_t* tile = val ? vt : kt;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -668,16 +669,20 @@ static void kv4_choose(Kv4Class& c, int from, int to, bool e2m1, int G, int kv_h
     const Kv4Kernel& k = kKv4Kernels[x];
     for (double chunk = k.step;; chunk = up(chunk * 1.19 / k.step) * k.step) {
       const bool whole = chunk >= longest;
-      double large = 0, records = 0, load = 0, top = 0, most = 0;
+      double large = 0, records = 0, joined = 0, load = 0, top = 0, most = 0;
       for (size_t i = 0; i < n; ++i) {
         const double r = whole ? 1 : up(keys[i] / chunk), w = up(rows[i] / k.rows) * kv_heads;
         if (keys[i] > 0.5 * r * std::min(chunk, longest)) large += w * r;
         most = std::max(most, w * r);
         load += w * keys[i];
         top = std::max(top, up(keys[i] / (r * k.step)) * k.step);
-        if (r > 1) records += rows[i] * kv_heads * r;
+        if (r > 1) {
+          joined += rows[i] * kv_heads;
+          records += rows[i] * kv_heads * r;
+        }
       }
-      if (whole || most <= (double)kAttnGroups) {   // a sequence has to fit a launch
+      // a sequence has to fit a launch, and so have the rows to join
+      if (whole || (most <= (double)kAttnGroups && joined <= (double)(1 << 22))) {
         // workgroups on each of 256 units: those of more than half a range's length, or by the work
         const double full = std::max({1.0, up(large / 256), up(load / top / 256 - 0.25)});
         const int on = (int)std::min<double>(k.most, full);
@@ -742,7 +747,7 @@ hipError_t launch_attn_kv4(const AttnKv4Args& a, int book, const AttnSeq* seqs, 
                            bool* fits, hipStream_t stream) {
   const Kv4Plan plan = kv4_plan(seqs, count, book, a.f.heads, a.f.kv_heads, a.f.d, a.f.window);
   *fits = !plan.part_floats || (ws && ws_floats >= (size_t)plan.part_floats);
-  if (!*fits) return hipSuccess;
+  if (!*fits || (plan.few.seqs.empty() && plan.many.seqs.empty())) return hipSuccess;
   const int G = a.f.heads / a.f.kv_heads;
   for (const Kv4Class* c : {&plan.few, &plan.many}) {
     for (size_t from = 0; from < c->seqs.size();) {

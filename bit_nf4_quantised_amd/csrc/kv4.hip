@@ -210,6 +210,7 @@ static void kv4_rows(Kv4Args a, int book, bool write, const std::vector<AttnSeq>
 
 hipError_t launch_kv4(const Kv4Args& a, int book, bool write, const AttnSeq* seqs, int64_t count, hipStream_t stream) {
   const std::vector<AttnSeq> v = by_work(seqs, count, false);
+  if (v.empty()) return hipSuccess;
   if (a.nb == 1) kv4_rows<1>(a, book, write, v, stream);
   else if (a.nb == 2) kv4_rows<2>(a, book, write, v, stream);
   else kv4_rows<4>(a, book, write, v, stream);

@@ -71,12 +71,12 @@ struct Kv4Few<128> {
       va[i] = a.v4.absmax[vt + vo];
     }
   }
-  __device__ __forceinline__ float step(int i, float unit) const { return kv4_step(kv4_lost(max(ka[i], va[i])) ? kBf16Nan : ka[i], unit); }
+  __device__ __forceinline__ uint32_t absmax(int i) const { return kv4_lost(max(ka[i], va[i])) ? kBf16Nan : ka[i]; }
   template <class Deq>
-  __device__ __forceinline__ void values(uint16_t* tile, const AttnKv4Args& a, int lane) const {
+  __device__ __forceinline__ void values(uint16_t* tile, const typename Deq::Shared& tables, const AttnKv4Args& a, int lane) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const Deq q(a.t, kv4_step(kv4_lost(va[i]) ? 0u : va[i], a.unit));
+      const Deq q(tables, a.t, a.unit, kv4_lost(va[i]) ? 0u : va[i]);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         *reinterpret_cast<u32x4*>(tile + Tile<128>::elem(16 * i + (lane & 15), 4 * (lane >> 4) + t)) = q.eight(v[i][t]);
@@ -104,10 +104,10 @@ struct Kv4Few<64> {
     v = *reinterpret_cast<const u32x4*>(a.v4.codes + 16 * vt + 16u * vo);
     va = a.v4.absmax[vt + vo];
   }
-  __device__ __forceinline__ float step(int i, float unit) const { return kv4_step(kv4_lost(max(ka[i], kva[i])) ? kBf16Nan : ka[i], unit); }
+  __device__ __forceinline__ uint32_t absmax(int i) const { return kv4_lost(max(ka[i], kva[i])) ? kBf16Nan : ka[i]; }
   template <class Deq>
-  __device__ __forceinline__ void values(uint16_t* tile, const AttnKv4Args& a, int lane) const {
-    const Deq q(a.t, kv4_step(kv4_lost(va) ? 0u : va, a.unit));
+  __device__ __forceinline__ void values(uint16_t* tile, const typename Deq::Shared& tables, const AttnKv4Args& a, int lane) const {
+    const Deq q(tables, a.t, a.unit, kv4_lost(va) ? 0u : va);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
       *reinterpret_cast<u32x4*>(tile + Tile<64>::elem(lane & 31, 4 * (lane >> 5) + t)) = q.eight(v[t]);
@@ -188,6 +188,7 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(
   // a wave's tile of values, later its outputs as [row][d + 4]
   __shared__ __attribute__((aligned(16))) float lds[NW][R * P];
   __shared__ float Ms[NW][R], Ls[NW][R];
+  __shared__ typename Deq::Shared tables;
   static_assert(BN * DP * 2 <= R * P * 4, "the tile fits");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -209,6 +210,7 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(
   Blocks now, next;
   if (j_w < k_hi) now.load(a, kbase + (int64_t)j_w * a.k4.token, vbase + (int64_t)j_w * a.v4.token, k_hi - 1 - j_w, lane);
 
+  Deq::share(tables, tid, a.t, a.unit);
   bf16x8 qf[NR][KS];
   Range mine[NR];   // keys that the lane's rows see
   Online16<DT> acc[NR];
@@ -229,6 +231,7 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(
   }
   const float slack = slack_of(a.f.c);
   uint16_t* const vt = reinterpret_cast<uint16_t*>(lds[wave]);
+  lds_barrier();   // the tables are there
 
   // the tile of keys from j, in `now`; the wave's next goes to `next`
   auto tile = [&](Blocks& now, Blocks& next, int j) __attribute__((always_inline)) {
@@ -237,7 +240,7 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(
     f32x4 sc[NR][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const Deq kq(a.t, now.step(i, a.unit));
+      const Deq kq(tables, a.t, a.unit, now.absmax(i));
 #pragma unroll
       for (int t = 0; t < KS; ++t) {
         const bf16x8 kf = __builtin_bit_cast(bf16x8, kq.eight(now.k[i][t]));
@@ -245,7 +248,7 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(
         for (int r = 0; r < NR; ++r) sc[r][i] = mfma16(kf, qf[r][t], t ? sc[r][i] : f32x4{0.f, 0.f, 0.f, 0.f});
       }
     }
-    now.template values<Deq>(vt, a, lane);
+    now.template values<Deq>(vt, tables, a, lane);
     // some row does not see some key
     if (j + BN > first.hi || j < last.lo) {
 #pragma unroll
@@ -362,11 +365,11 @@ struct Kv4Many {
   }
   // the loaded blocks into a tile
   template <class Deq>
-  __device__ __forceinline__ void store(uint16_t* kt, uint16_t* vt, const AttnKv4Args& a, int tid) const {
+  __device__ __forceinline__ void store(uint16_t* kt, uint16_t* vt, const typename Deq::Shared& tables, const AttnKv4Args& a, int tid) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const bool val = value(tid, i);
-      const Deq q(a.t, kv4_step(kv4_lost(max(m[i], vm[i])) ? (val ? 0u : kBf16Nan) : m[i], a.unit));
+      const Deq q(tables, a.t, a.unit, kv4_lost(max(m[i], vm[i])) ? (val ? 0u : kBf16Nan) : m[i]);
       uint16_t* tile = val ? vt : kt;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -391,6 +394,7 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
   constexpr int BN = 64, KS = DP / 16, DT = DP / 32, R = 32 * WV;
   typedef Tile<DP> T;
   __shared__ __attribute__((aligned(16))) uint16_t K0[BN * DP], V0[BN * DP], K1[BN * DP], V1[BN * DP];
+  __shared__ typename Deq::Shared tables;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = a.f.heads / a.f.kv_heads;
@@ -417,6 +421,7 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
     codes.load(a, kbase + (int64_t)at * a.k4.token, vbase + (int64_t)at * a.v4.token, k_hi - 1 - (k_lo + at), tid);
   };
   if (nt > 0) load(0);
+  Deq::share(tables, tid, a.t, a.unit);
   bf16x8 qf[KS];
   {
     const uint16_t* q = a.f.q.p + (s.q0 + tok) * a.f.q.token + (int64_t)head * a.f.q.head;
@@ -432,14 +437,15 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
   acc.init();
   const float slack = slack_of(a.f.c);
   if (nt > 0) {
-    codes.template store<Deq>(K0, V0, a, tid);
+    lds_barrier();   // the tables are there
+    codes.template store<Deq>(K0, V0, tables, a, tid);
     load(1);
   }
   // tile t is in (Kt, Vt); tile t + 1 is made in (kn, vn). No branches around the products: a wave whose rows see nothing of a
   // tile hides all of it (branches made the compiler move the outputs between registers, 81 us against 76)
   auto tile = [&](int t, const uint16_t* Kt, const uint16_t* Vt, uint16_t* kn, uint16_t* vn) __attribute__((always_inline)) {
     lds_barrier();   // tile t is in, and every wave is done with tile t - 1
-    codes.template store<Deq>(kn, vn, a, tid);
+    codes.template store<Deq>(kn, vn, tables, a, tid);
     load(t + 2);
     const int j0 = k_lo + t * BN;
     f32x16 sc[2];
@@ -615,17 +621,17 @@ __global__ __launch_bounds__(256) void attn_kv4_join_kernel(const AttnFwdArgs a,
 static int64_t kv4_keys(const AttnSeq& s, int window) { return std::max<int64_t>(1, s.nk - first_key(s, window)); }
 
 // The kernels: rows of a workgroup, keys of a step (a range is a multiple of it), workgroups that a compute unit holds, and
-// the time of a step in us with 1, 2 .. of them on it, for tables and for E2M1 (d = 128; d <= 64 takes 0.6 of it). Measured
-// with one, two and three workgroups a unit, on caches of 2000 to 30000 keys.
+// the time of a step in us with 1, 2 .. of them on it, d = 128 and d <= 64, for tables and for E2M1 each. Measured as the
+// difference of 16 steps and 8 of workgroups that are all alike.
 struct Kv4Kernel {
   int rows, waves, step, most;
-  double us[2][3];
+  double us[2][2][3];
 };
 constexpr Kv4Kernel kKv4Kernels[] = {
-    {16, 4, 128, 3, {{1.65, 2.65, 4.4}, {1.2, 1.8, 2.55}}},
-    {32, 4, 128, 2, {{2.0, 3.85, 0}, {1.6, 3.05, 0}}},
-    {128, 4, 64, 2, {{1.82, 2.95, 0}, {1.52, 2.6, 0}}},
-    {256, 8, 64, 1, {{2.07, 0, 0}, {1.9, 0, 0}}},
+    {16, 4, 128, 3, {{{1.65, 2.4, 3.4}, {1.05, 1.6, 2.2}}, {{1.25, 1.55, 2.0}, {0.95, 1.1, 1.5}}}},
+    {32, 4, 128, 2, {{{1.9, 2.6, 0}, {1.25, 1.95, 0}}, {{1.4, 1.8, 0}, {1.05, 1.25, 0}}}},
+    {128, 4, 64, 2, {{{1.6, 2.5, 0}, {1.4, 2.25, 0}}, {{1.1, 1.6, 0}, {1.0, 1.4, 0}}}},
+    {256, 8, 64, 1, {{{2.05, 0, 0}, {1.95, 0, 0}}, {{1.55, 0, 0}, {1.45, 0, 0}}}},
 };
 
 // The sequences of one launch form: their rows in tiles of the kernel's, their keys in ranges of about `chunk`.
@@ -648,9 +654,7 @@ static AttnSeqs kv4_seqs(const Kv4Class& c, size_t from, int G, int kv_heads, in
 
 // Chooses the kernel among [from, to) and the length of a range by the smallest estimate: 5 us around the steps (launch, first
 // loads, joining the waves), the longest range's steps at the rate of a unit that holds its share of workgroups, times the
-// rounds of workgroups, and, where there are ranges to join, 3.5 us and their sums at 7 TB/s. Estimated and measured, us: 5 tokens
-// each over 8 caches of 2000 keys, 32 heads over 8, 17.7 and 17.7; one token of 30000 keys 21 and 20; 65 tokens over
-// 30000 keys 80 and 77; 65 tokens over 300 keys each of 4 (one range) 14 and 15, where ranges of 128 keys took 26.
+// rounds of workgroups, and, where there are ranges to join, 3.5 us and their sums, written and read, at 3.5 TB/s.
 static inline double up(double x) {   // to a whole number; x is not large
   const int64_t i = (int64_t)x;
   return (double)(i + ((double)i < x));
@@ -686,8 +690,8 @@ static void kv4_choose(Kv4Class& c, int from, int to, bool e2m1, int G, int kv_h
         // workgroups on each of 256 units: those of more than half a range's length, or by the work
         const double full = std::max({1.0, up(large / 256), up(load / top / 256 - 0.25)});
         const int on = (int)std::min<double>(k.most, full);
-        const double us = 5 + top / k.step * k.us[e2m1][on - 1] * (d <= 64 ? 0.6 : 1.0) * up(full / on) +
-                          (records > 0 ? 3.5 + records * (d + 8) * 8 / 7e6 : 0);
+        const double us = 5 + top / k.step * k.us[d <= 64][e2m1][on - 1] * up(full / on) +
+                          (records > 0 ? 3.5 + records * (d + 8) * 8 / 3.5e6 : 0);
         if (best < 0 || us < best) {
           best = us;
           c.kernel = x;

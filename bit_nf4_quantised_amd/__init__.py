@@ -789,12 +789,14 @@ class Rope:
         cfg = CRopeConfig(heads, 0 if k is None else k.shape[1], d, self.rot, int(self.interleaved), eps, self.factor, tokens)
         if len(self._plans) >= 256:   # a program of ever new shapes
             self._plans.clear()
-        self._plans[key] = plan = (at, cfg, ctypes.byref(cfg), tokens)
+        need = int(lib.qlora_rope_workspace_bytes(ctypes.byref(cfg)))
+        self._plans[key] = plan = (at, ctypes.byref(cfg), tokens, need)
         return plan
 
     def _tensors(self, eps, qs, ks):
         """The qlora_attn_tensor structures of the tensors (None: not there), as an array to be kept until the library has
-        read them, their addresses, the configuration, and the tokens."""
+        read them, their addresses, and the plan: those structures' strides, the configuration, the tokens and the bytes of
+        the backward's workspace."""
         key = [eps]
         for t in qs + ks:
             if t is None:
@@ -817,7 +819,7 @@ class Rope:
                 raise ValueError("tensor must live on the GPU")
             v[3 * i] = t.data_ptr()
             ptrs.append(at + 24 * i)
-        return v, ptrs, plan[2], plan[3]
+        return v, ptrs, plan
 
 
 def _rope_positions(rope, positions, tokens):
@@ -843,7 +845,7 @@ def qlora_rope_fwd(rope: Rope, positions, q, k, q_out, k_out, q_weight=None, k_w
     """Query and key heads [tokens, heads, d] (bf16, tokens and heads may be strided), normed over d where a weight
     [d] is given, then rotated by their tokens' positions (int64 [tokens]). k and k_out may be None; an output may
     be its input."""
-    keep, (tq, to, tk, tko), cfg, tokens = rope._tensors(eps, (q, q_out), (k, k_out))
+    keep, (tq, to, tk, tko), (_, cfg, tokens, _) = rope._tensors(eps, (q, q_out), (k, k_out))
     _check(lib.qlora_rope_fwd(cfg, rope._freq, _rope_positions(rope, positions, tokens), tq, tk, _rope_weight(q_weight, q),
                               _rope_weight(k_weight, k), to, tko, _stream(stream)), "qlora_rope_fwd")
 
@@ -855,7 +857,7 @@ def qlora_rope_bwd(rope: Rope, positions, dq_out, dk_out, dq, dk, q=None, k=None
     weights' (float32 [d], added to with accumulate). Normed heads need the forward's inputs q and k."""
     if (q_weight is not None and q is None) or (k_weight is not None and k is None):
         raise ValueError("the backward of normed heads needs their inputs")
-    keep, (tgo, tdq, tq, tgk, tdk, tk), cfg, tokens = rope._tensors(
+    keep, (tgo, tdq, tq, tgk, tdk, tk), (_, cfg, tokens, need) = rope._tensors(
         eps, (dq_out, dq, q if q_weight is not None else None), (dk_out, dk, k if k_weight is not None else None))
     pdw = None, None
     nbytes = 0
@@ -865,7 +867,7 @@ def qlora_rope_bwd(rope: Rope, positions, dq_out, dk_out, dq, dk, q=None, k=None
                 raise ValueError("a head weight's gradient goes with the weight and holds d values")
         pdw = _dptr(dq_weight, _F32), _dptr(dk_weight, _F32)
         if ws is None:
-            ws = _scratch(max(int(lib.qlora_rope_workspace_bytes(cfg)), 256), dq.device, stream)
+            ws = _scratch(max(need, 256), dq.device, stream)
         nbytes = ws.numel() * ws.element_size()
     _check(lib.qlora_rope_bwd(cfg, rope._freq, _rope_positions(rope, positions, tokens), tq, tk, _rope_weight(q_weight, dq_out),
                               _rope_weight(k_weight, dk_out), tgo, tgk, tdq, tdk, *pdw, int(bool(accumulate)),

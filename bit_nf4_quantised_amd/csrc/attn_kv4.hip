@@ -47,7 +47,7 @@ __device__ __forceinline__ Kv4Found kv4_find(const AttnSeqs& sq, const Kv4Split&
 __device__ __forceinline__ bool kv4_lost(uint32_t absmax) { return absmax >= kBf16Infinity; }   // absmax has no sign
 
 // ------------------------------------------------------------------------------------------
-// Few rows: 16 NR rows a workgroup, its keys one range of the sequence's, of which its NW waves take 32-key tiles in
+// Few rows: 16 NR rows a workgroup, its keys one range of the sequence's, of which its four waves take 32-key tiles in
 // turn; there are no barriers until the waves are joined. Products are v_mfma_f32_16x16x32_bf16: lane (n, q) = (lane
 // % 16, lane / 16) holds of a result column n and rows 4 q .. 4 q + 3, of an operand row (or column) n and 8 values.
 // The contraction of the first product may run over d in any order, so lane (n, q) takes the block q (d <= 64: half
@@ -181,9 +181,9 @@ struct Online16 {
   }
 };
 
-template <int DP, class Deq, int NW, int NR>
-__global__ __launch_bounds__(NW * 64, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(const AttnKv4Args a, const AttnSeqs sq, const Kv4Split sp) {
-  constexpr int BN = 32, KS = DP / 32, DT = DP / 16, R = 16 * NR, P = DP + 4;
+template <int DP, class Deq, int NR>
+__global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(const AttnKv4Args a, const AttnSeqs sq, const Kv4Split sp) {
+  constexpr int NW = 4, BN = 32, KS = DP / 32, DT = DP / 16, R = 16 * NR, P = DP + 4;
   typedef Kv4Few<DP> Blocks;
   // a wave's tile of values, later its outputs as [row][d + 4]
   __shared__ __attribute__((aligned(16))) float lds[NW][R * P];
@@ -293,42 +293,35 @@ __global__ __launch_bounds__(NW * 64, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(
     for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<f32x4*>(&lds[wave][at * P + 16 * dt + 4 * (lane >> 4)]) = acc[r].o[dt];
   }
   __syncthreads();
-  constexpr int E = NW == 4 ? 8 : 2;   // columns a thread
-  for (int x = tid; x < R * (DP / E); x += NW * 64) {
-    const int row = x / (DP / E), c0 = x % (DP / E) * E, grow = rt * R + row;
+  for (int x = tid; x < R * (DP / 8); x += 256) {   // 8 columns a thread
+    const int row = x / (DP / 8), c0 = x % (DP / 8) * 8, grow = rt * R + row;
     if (grow >= rows) break;
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) mx = fmaxf(mx, Ms[w][row]);
     const float mxc = mx == -INFINITY ? 0.f : mx * a.f.c;
-    float l = 0.f, v[E];
+    float l = 0.f, v[8];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float f = Ms[w][row] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(Ms[w][row] * a.f.c - mxc);
       l += Ls[w][row] * f;   // 0 times NaN stays NaN
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(lds[w][row * P + (c0 & ~7) + kv4_place_of((c0 & 7) + e)], f, v[e]);
+      for (int e = 0; e < 8; ++e) v[e] = __fmaf_rn(lds[w][row * P + c0 + kv4_place_of(e)], f, v[e]);
     }
     if (c0 >= a.f.d) continue;
     const int tok = grow / G, head = u.kvh * G + grow % G;
     if (ns == 1) {
       const float inv = inverse_sum(l);
-      uint32_t* o = reinterpret_cast<uint32_t*>(a.f.o.p + (s.q0 + tok) * a.f.o.token + (int64_t)head * a.f.o.head + c0);
-      if constexpr (E == 8)
-        *reinterpret_cast<u32x4*>(o) = u32x4{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv),
-                                             pack_bf16x2(v[4] * inv, v[5] * inv), pack_bf16x2(v[6] * inv, v[7] * inv)};
-      else *o = pack_bf16x2(v[0] * inv, v[1] * inv);
+      *reinterpret_cast<u32x4*>(a.f.o.p + (s.q0 + tok) * a.f.o.token + (int64_t)head * a.f.o.head + c0) =
+          u32x4{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv),
+                pack_bf16x2(v[4] * inv, v[5] * inv), pack_bf16x2(v[6] * inv, v[7] * inv)};
       if (c0 == 0 && a.f.lse) a.f.lse[(int64_t)head * a.f.lse_stride + s.q0 + tok] = lse_of(mxc, l);
     } else {
       float* part = sp.part + (found.row0 + ((int64_t)grow * a.f.kv_heads + u.kvh) * ns + split) * (int64_t)(a.f.d + 8);
-      if constexpr (E == 8) {
-        *reinterpret_cast<f32x4*>(part + c0) = f32x4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f32x4*>(part + c0 + 4) = f32x4{v[4], v[5], v[6], v[7]};
-      } else {
-        *reinterpret_cast<float2*>(part + c0) = make_float2(v[0], v[1]);
-      }
+      *reinterpret_cast<f32x4*>(part + c0) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(part + c0 + 4) = f32x4{v[4], v[5], v[6], v[7]};
       if (c0 == 0) {
         part[a.f.d] = l == 0.f ? -INFINITY : mxc;   // finite (0 at least) where the sum is NaN: the join reads it
         part[a.f.d + 1] = l;
@@ -740,8 +733,8 @@ template <int DP, class Deq>
 static void kv4_launch(int kernel, const AttnKv4Args& a, const AttnSeqs& q, const Kv4Split& sp, hipStream_t stream) {
   const dim3 grid((unsigned)(q.first[q.count] * a.f.kv_heads)), wg((unsigned)kKv4Kernels[kernel].waves * 64);
   switch (kernel) {
-    case 0: hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 4, 1>), grid, wg, 0, stream, a, q, sp); break;
-    case 1: hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 4, 2>), grid, wg, 0, stream, a, q, sp); break;
+    case 0: hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 1>), grid, wg, 0, stream, a, q, sp); break;
+    case 1: hipLaunchKernelGGL((attn_kv4_few_kernel<DP, Deq, 2>), grid, wg, 0, stream, a, q, sp); break;
     case 2: hipLaunchKernelGGL((attn_kv4_many_kernel<DP, Deq, 4>), grid, wg, 0, stream, a, q, sp); break;
     default: hipLaunchKernelGGL((attn_kv4_many_kernel<DP, Deq, 8>), grid, wg, 0, stream, a, q, sp); break;
   }

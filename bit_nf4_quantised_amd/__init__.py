@@ -179,6 +179,18 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _stream_on(stream, *tensors):
+    """_stream, for a call with these tensors (None: not there): all must live on the current device, on whose streams
+    the kernels run. A kernel that is given another GPU's memory faults where the two are not peers."""
+    current = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"tensor lives on {t.device} and the current device is cuda:{current}")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(current)
+    return _stream(stream)
+
+
 def _pool_of(stream, device):
     """The context in which torch allocates from the memory pool of the stream that a call is given. A block of
     another pool may be handed out again, or still be read, by that other stream's work while the call's kernels
@@ -809,14 +821,17 @@ class Rope:
         v = plan[0][:]
         at = v.buffer_info()[0]
         ptrs = []
+        gpu = qs[0].get_device()
+        if gpu < 0:
+            raise ValueError("tensor must live on the GPU")
         for i, t in enumerate(qs + ks):
             if t is None:
                 ptrs.append(None)
                 continue
             if t.dtype not in _BF16:
                 _dtype(t, *_BF16)
-            if not t.is_cuda:
-                raise ValueError("tensor must live on the GPU")
+            if t.get_device() != gpu:
+                raise ValueError("the tensors must live on one GPU")
             v[3 * i] = t.data_ptr()
             ptrs.append(at + 24 * i)
         return v, ptrs, plan
@@ -847,7 +862,8 @@ def qlora_rope_fwd(rope: Rope, positions, q, k, q_out, k_out, q_weight=None, k_w
     be its input."""
     keep, (tq, to, tk, tko), (_, cfg, tokens, _) = rope._tensors(eps, (q, q_out), (k, k_out))
     _check(lib.qlora_rope_fwd(cfg, rope._freq, _rope_positions(rope, positions, tokens), tq, tk, _rope_weight(q_weight, q),
-                              _rope_weight(k_weight, k), to, tko, _stream(stream)), "qlora_rope_fwd")
+                              _rope_weight(k_weight, k), to, tko,
+                              _stream_on(stream, q, positions, q_weight, k_weight)), "qlora_rope_fwd")
 
 
 def qlora_rope_bwd(rope: Rope, positions, dq_out, dk_out, dq, dk, q=None, k=None, q_weight=None, k_weight=None,
@@ -871,7 +887,9 @@ def qlora_rope_bwd(rope: Rope, positions, dq_out, dk_out, dq, dk, q=None, k=None
         nbytes = ws.numel() * ws.element_size()
     _check(lib.qlora_rope_bwd(cfg, rope._freq, _rope_positions(rope, positions, tokens), tq, tk, _rope_weight(q_weight, dq_out),
                               _rope_weight(k_weight, dk_out), tgo, tgk, tdq, tdk, *pdw, int(bool(accumulate)),
-                              None if ws is None else _ptr(ws), nbytes, _stream(stream)), "qlora_rope_bwd")
+                              None if ws is None else _ptr(ws), nbytes,
+                              _stream_on(stream, dq, positions, q_weight, k_weight, dq_weight, dk_weight, ws)),
+           "qlora_rope_bwd")
 
 
 # ------------------------------------------------------------------------- a key/value cache in 4 bits
@@ -933,13 +951,15 @@ def qlora_kv4_write(seqs: AttnSeqs, k, v, k4: Kv4, v4: Kv4, stream=None) -> None
     """New keys and values k, v [tokens, kv heads, d] (bf16, strided) into a 4-bit cache: the nq tokens of every
     sequence (q0, nq, k0, nk) become its last nq keys, so the list that the attention then takes says where."""
     cfg, (tk, tv), (pk, pv), keep = _kv4_copy(seqs, k, v, k4, v4)
-    _check(lib.qlora_kv4_write(cfg, seqs.count, seqs._seqs, tk, tv, pk, pv, _stream(stream)), "qlora_kv4_write")
+    _check(lib.qlora_kv4_write(cfg, seqs.count, seqs._seqs, tk, tv, pk, pv, _stream_on(stream, k, v, k4.codes, v4.codes)),
+           "qlora_kv4_write")
 
 
 def qlora_kv4_read(seqs: AttnSeqs, k4: Kv4, v4: Kv4, k, v, stream=None) -> None:
     """The last nq keys and values of every sequence out of a 4-bit cache, in bf16: into tokens q0 .. of k and v."""
     cfg, (tk, tv), (pk, pv), keep = _kv4_copy(seqs, k, v, k4, v4)
-    _check(lib.qlora_kv4_read(cfg, seqs.count, seqs._seqs, pk, pv, tk, tv, _stream(stream)), "qlora_kv4_read")
+    _check(lib.qlora_kv4_read(cfg, seqs.count, seqs._seqs, pk, pv, tk, tv, _stream_on(stream, k, v, k4.codes, v4.codes)),
+           "qlora_kv4_read")
 
 
 def qlora_attn_kv4_fwd(seqs: AttnSeqs, q, k4: Kv4, v4: Kv4, o, lse=None, scale: float | None = None, ws=None,
@@ -960,8 +980,8 @@ def qlora_attn_kv4_fwd(seqs: AttnSeqs, q, k4: Kv4, v4: Kv4, o, lse=None, scale: 
         ws = _scratch(need, q.device, stream) if need else None
     if ws is not None:
         pws, nbytes = _ptr(ws), ws.numel() * ws.element_size()
-    _check(lib.qlora_attn_kv4_fwd(cfg, seqs.count, seqs._seqs, tq, pk, pv, to, plse, pws, nbytes, _stream(stream)),
-           "qlora_attn_kv4_fwd")
+    _check(lib.qlora_attn_kv4_fwd(cfg, seqs.count, seqs._seqs, tq, pk, pv, to, plse, pws, nbytes,
+                                  _stream_on(stream, q, o, k4.codes, v4.codes, lse, ws)), "qlora_attn_kv4_fwd")
 
 
 # ------------------------------------------------------------------------- format variants

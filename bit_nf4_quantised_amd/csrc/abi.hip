@@ -744,6 +744,18 @@ nf4::RopeArgs rope_args(const qlora_rope_config* c, const double* inv_freq, cons
   return a;
 }
 
+// Outputs yq, yk in memory apart, and each in its inputs' only with their strides: a row that another lane has yet to read
+// would be written over.
+bool rope_apart(const qlora_rope_config* c, const qlora_attn_tensor* q, const qlora_attn_tensor* k, const qlora_attn_tensor* yq,
+                const qlora_attn_tensor* yk) {
+  auto meets = [&](const qlora_attn_tensor* x, const qlora_attn_tensor* y, int heads, bool same) {
+    if (!x || x->data != y->data) return false;
+    return !same || (c->tokens > 1 && x->token_stride != y->token_stride) || (heads > 1 && x->head_stride != y->head_stride);
+  };
+  if (meets(q, yq, c->heads, true)) return false;
+  return !c->kv_heads || !(meets(yq, yk, 0, false) || meets(k, yq, 0, false) || meets(q, yk, 0, false) || meets(k, yk, c->kv_heads, true));
+}
+
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 }  // namespace
@@ -757,6 +769,7 @@ int qlora_rope_fwd(const qlora_rope_config* cfg, const double* inv_freq, const i
   if (cfg->tokens == 0) return NF4_OK;
   if (cfg->rot && !positions) return NF4_ERR_NULL;
   if (!aligned8(positions) || !aligned16(q_weight) || !aligned16(k_weight)) return NF4_ERR_ALIGN;
+  if (!rope_apart(cfg, q, k, q_out, k_out)) return NF4_ERR_SHAPE;
   nf4::RopeArgs a = rope_args(cfg, inv_freq, positions, q, k, q_weight, k_weight);
   a.qo = rope_tensor(q_out);
   a.ko = rope_tensor(k_out);
@@ -788,6 +801,9 @@ int qlora_rope_bwd(const qlora_rope_config* cfg, const double* inv_freq, const i
       !aligned16(ws))
     return NF4_ERR_ALIGN;
   if ((dq_weight || dk_weight) && (!ws || ws_bytes < qlora_rope_workspace_bytes(cfg))) return NF4_ERR_WORKSPACE;
+  if (!rope_apart(cfg, dq_out, dk_out, dq, dk) || !rope_apart(cfg, q_weight ? q : nullptr, k_weight ? k : nullptr, dq, dk) ||
+      (dq_weight && dq_weight == dk_weight))
+    return NF4_ERR_SHAPE;
   nf4::RopeArgs a = rope_args(cfg, inv_freq, positions, q, k, q_weight, k_weight);
   a.qo = rope_tensor(dq_out);
   a.ko = rope_tensor(dk_out);
@@ -839,6 +855,7 @@ int kv4_copy(bool write, const qlora_attn_config* cfg, int64_t count, const qlor
   for (int64_t i = 0; i < count; ++i) {
     if (seqs[i].nq > seqs[i].nk) return NF4_ERR_SHAPE;
     if ((seqs[i].nq * cfg->kv_heads * nb + 63) / 64 > nf4::kMaxThreads / 512) return NF4_ERR_SHAPE;
+    if (!write && seqs[i].nq && k->data == v->data) return NF4_ERR_SHAPE;
   }
   try {
     if (write && count > 1) {   // two sequences that write the same token would leave either's blocks

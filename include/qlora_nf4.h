@@ -486,7 +486,7 @@ typedef struct {
  *                key heads. q_out and k_out may be their inputs' memory with the same strides; apart from that
  *                outputs overlap neither inputs nor each other.
  *   q_weight, k_weight   [d] bf16 or NULL: those heads are not normed.
- * Errors: NF4_ERR_SHAPE, NF4_ERR_NULL, NF4_ERR_ALIGN, NF4_ERR_HIP. */
+ * Errors: NF4_ERR_SHAPE (sizes, strides, and outputs that start where they may not), NF4_ERR_NULL, NF4_ERR_ALIGN, NF4_ERR_HIP. */
 int qlora_rope_fwd(const qlora_rope_config *cfg, const double *inv_freq, const int64_t *positions,
                    const qlora_attn_tensor *q, const qlora_attn_tensor *k, const uint16_t *q_weight,
                    const uint16_t *k_weight, const qlora_attn_tensor *q_out, const qlora_attn_tensor *k_out,
@@ -499,7 +499,8 @@ int qlora_rope_fwd(const qlora_rope_config *cfg, const double *inv_freq, const i
  *   q, k: the forward's inputs; read, and needed, only where the heads are normed (else they may be NULL).
  *   dq and dk may be the memory of dq_out and dk_out, or of q and k, with the same strides.
  *   ws: with dq_weight or dk_weight, at least qlora_rope_workspace_bytes(cfg) bytes.
- * The sums run in a fixed order. Errors: as the forward; NF4_ERR_NULL also for a weight's gradient without the
+ * The sums run in a fixed order. Errors: as the forward; NF4_ERR_SHAPE also for one memory for both weights'
+ * gradients (a weight that queries and keys share: add the two); NF4_ERR_NULL also for a weight's gradient without the
  * weight; NF4_ERR_WORKSPACE. */
 int qlora_rope_bwd(const qlora_rope_config *cfg, const double *inv_freq, const int64_t *positions,
                    const qlora_attn_tensor *q, const qlora_attn_tensor *k, const uint16_t *q_weight,
@@ -538,7 +539,7 @@ typedef struct {
  * used; the rest is checked as for qlora_attn_fwd. k4 and v4 have the same codebook.
  * Of one sequence ceil(nq * kv_heads * nb / 64) is below 2^23.
  * Errors: as qlora_attn_fwd; NF4_ERR_SHAPE also for nq > nk and, when writing, for two sequences that would write
- * the same cache token, a cache whose rows overlap, and k4 and v4 in the same memory. */
+ * the same cache token, a cache whose rows overlap, and k4 and v4 in the same memory; when reading, k and v in it. */
 int qlora_kv4_write(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs, const qlora_attn_tensor *k,
                     const qlora_attn_tensor *v, const qlora_kv4 *k4, const qlora_kv4 *v4, hipStream_t stream);
 int qlora_kv4_read(const qlora_attn_config *cfg, int64_t count, const qlora_attn_seq *seqs, const qlora_kv4 *k4,

@@ -70,6 +70,23 @@ def test_rope_backward_refusals():
     assert _rope_bwd(dqw=FAKE) == WS and _rope_bwd(dqw=FAKE, ws=FAKE, ws_bytes=need - 1) == WS
 
 
+def test_rope_outputs_that_meet_are_refused():
+    """One memory for two outputs, an output in the other's input, and one in its own input with other strides."""
+    a, b, c, e = (_t(FAKE * i) for i in (1, 2, 3, 4))
+    for bad in (dict(tq=a, tk=b, qo=c, ko=c), dict(tq=a, tk=b, qo=b, ko=c), dict(tq=a, tk=b, qo=c, ko=a), dict(tq=a, tk=b, qo=_t(token=8192), ko=b),
+                dict(tq=a, tk=b, qo=a, ko=_t(2 * FAKE, head=256))):
+        assert _rope(**bad) == SHAPE, bad
+    for bad in (dict(go=a, gk=b, dq=c, dk=c), dict(go=a, gk=b, dq=b, dk=c), dict(go=a, gk=b, dq=_t(token=8192), dk=b),
+                dict(go=a, gk=b, tq=c, tk=e, dq=e, dk=b), dict(go=a, gk=b, tq=c, tk=e, dq=a, dk=_t(4 * FAKE, head=256)),
+                dict(go=a, gk=b, tq=c, tk=e, dq=a, dk=b, dqw=FAKE, dkw=FAKE, ws=FAKE, ws_bytes=1 << 20)):
+        assert _rope_bwd(**bad) == SHAPE, bad
+
+
+def test_values_read_over_keys_are_refused():
+    assert _write(read=True) == SHAPE and _write(read=True, k=_t(), v=_t(token=8192)) == SHAPE
+    assert _write(read=True, seqs=((0, 0, 0, 10),)) == OK
+
+
 def _c4(codes=FAKE, absmax=FAKE + 2, token=4, head=4096, book=0):
     return q.CKv4(codes, absmax, token, head, book)
 

@@ -353,3 +353,21 @@ def test_example_decodes_over_both_caches():
             nf4.qlora_attn_fwd = real
     four, like = host(torch.cat(four)), host(torch.cat(like))
     assert _rel(four, like) < 5e-3 * 2 ** 0.5      # the probabilities' and the output's roundings differ
+
+
+def test_tensors_of_another_device_than_the_current_one_are_refused(monkeypatch):
+    """Before anything is launched; the current device is made to look like another one."""
+    import bit_nf4_quantised_amd as nf4
+    q, k = (torch.zeros(4, h, 64, dtype=torch.bfloat16, device="cuda:0") for h in (4, 2))
+    k4, v4 = (nf4.empty_kv4(8, 2, 64, device="cuda:0") for _ in range(2))
+    pos, rope, seqs = torch.zeros(4, dtype=torch.int64, device="cuda:0"), nf4.Rope(64), nf4.AttnSeqs([(0, 4, 0, 4)])
+    calls = [lambda: nf4.qlora_rope_fwd(rope, pos, q, k, q, k), lambda: nf4.qlora_rope_bwd(rope, pos, q, k, q, k),
+             lambda: nf4.qlora_kv4_write(seqs, k, k, k4, v4), lambda: nf4.qlora_kv4_read(seqs, k4, v4, k, torch.empty_like(k)),
+             lambda: nf4.qlora_attn_kv4_fwd(seqs, q, k4, v4, torch.empty_like(q), torch.empty(4, 4, device="cuda:0"))]
+    for f in calls:
+        f()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for f in calls:
+        with pytest.raises(ValueError, match="current device"):
+            f()

@@ -25,8 +25,10 @@
 namespace nf4 {
 
 constexpr int kRopeHeads = 4;      // heads of a token that a group of lanes takes at a time
-constexpr int kRopeGrid = 2048;    // workgroups at most, of queries and of keys together: they go on to further tokens
-constexpr int kRopeSums = 1024;    // the same where each leaves partial sums of dw
+// Workgroups at most, of queries and of keys together; past them they go on to further tokens. That is slower than more
+// workgroups (4096 tokens of 64 and 8 heads, d 128, normed, 2304 and 4608 of them: 25.4 us, and 27.3 with 2048; 32768 tokens
+// 199 and 229), but where each leaves partial sums of dw these have to be added (32768 tokens 386 and 354 with 4096).
+constexpr int kRopeGrid = 65536, kRopeSums = 4096;
 
 struct CosSin {
   float c, s;
@@ -289,13 +291,15 @@ __global__ __launch_bounds__(256) void rope_dw_kernel(const float* part, int q_g
 }
 
 // ------------------------------------------------------------------------------------------
-// Host side. A group takes 8 heads of a token, two rounds of four, where there are enough groups for every lane of the GPU
-// (8192 of 16 lanes; a token's sines and cosines are then formed half as often), else 4.
-static int rope_plan(RopeArgs& a, int most) {
+// Host side. A group takes 4 heads of a token; where sums of dw are left and there are enough groups for every lane of the
+// GPU (8192 of 16 lanes), 8, two rounds of four: half as many sums to join (2048 tokens of 32 and 8 heads, d 128, 17.2 us, and
+// 20.3 by fours; 256 tokens 9.5, and 8.5 by fours).
+static int rope_plan(RopeArgs& a, bool sums) {
   const int64_t lanes = a.d <= 64 ? 32 : 16;   // groups of a workgroup
+  const int most = sums ? kRopeSums : kRopeGrid;
   auto items = [&](int heads) { return a.tokens * ((heads + a.per - 1) / a.per); };
   a.per = 2 * kRopeHeads;
-  if (items(a.heads) + items(a.kv_heads) < 8192) a.per = kRopeHeads;
+  if (!sums || items(a.heads) + items(a.kv_heads) < 8192) a.per = kRopeHeads;
   int64_t q = (items(a.heads) + lanes - 1) / lanes, k = (items(a.kv_heads) + lanes - 1) / lanes;
   if (q + k > most) {   // shares by the work
     q = std::max<int64_t>(1, most * a.heads / (a.heads + a.kv_heads));
@@ -305,11 +309,11 @@ static int rope_plan(RopeArgs& a, int most) {
   return (int)(q + k);
 }
 
-size_t rope_bwd_ws_floats(RopeArgs a) { return (size_t)rope_plan(a, kRopeSums) * 128; }
+size_t rope_bwd_ws_floats(RopeArgs a) { return (size_t)rope_plan(a, true) * 128; }
 
 template <bool INTER, bool NORM>
 static void rope_fwd(RopeArgs a, hipStream_t stream) {
-  const dim3 grid((unsigned)rope_plan(a, kRopeGrid));
+  const dim3 grid((unsigned)rope_plan(a, false));
   if (a.d <= 64) hipLaunchKernelGGL((rope_fwd_kernel<8, INTER, NORM>), grid, dim3(256), 0, stream, a);
   else hipLaunchKernelGGL((rope_fwd_kernel<16, INTER, NORM>), grid, dim3(256), 0, stream, a);
 }
@@ -323,7 +327,7 @@ hipError_t launch_rope_fwd(const RopeArgs& a, hipStream_t stream) {
 
 template <bool INTER, bool NORM, bool DW>
 static void rope_bwd(RopeArgs a, float* part, hipStream_t stream) {
-  const dim3 grid((unsigned)rope_plan(a, DW ? kRopeSums : kRopeGrid));
+  const dim3 grid((unsigned)rope_plan(a, DW));
   if (a.d <= 64) hipLaunchKernelGGL((rope_bwd_kernel<8, INTER, NORM, DW>), grid, dim3(256), 0, stream, a, part);
   else hipLaunchKernelGGL((rope_bwd_kernel<16, INTER, NORM, DW>), grid, dim3(256), 0, stream, a, part);
 }
@@ -343,7 +347,7 @@ hipError_t launch_rope_bwd(const RopeArgs& args, float* dqw, float* dkw, int acc
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dw) return e;
   RopeArgs p = a;
-  const int groups = rope_plan(p, kRopeSums);
+  const int groups = rope_plan(p, true);
   hipLaunchKernelGGL(rope_dw_kernel, dim3((unsigned)(a.d / 8), 2), dim3(256), 0, stream, part, p.q_groups, groups, a.d, dqw, dkw, accumulate);
   return hipGetLastError();
 }

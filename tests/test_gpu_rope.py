@@ -152,6 +152,37 @@ def test_more_tokens_than_workgroups_start_with():
     assert torch.equal(dw, again)
 
 
+def test_more_groups_than_the_largest_grid():
+    """65536 workgroups of 32 groups take 2097152 items at a time (4 heads of a token, d <= 64), with sums of dw 4096 workgroups.
+    dw: 64 values a lane, then 32 groups, 128 workgroups a slice and 32 slices, 256 * 2^-24 = 1.6e-5 of the terms, and the
+    terms' own 2e-6."""
+    import bit_nf4_quantised_amd as nf4
+    t, h = 133000, 64
+    g = torch.Generator(device="cuda:0").manual_seed(6)
+    x, k = (torch.randn(t, n, 8, generator=g, device="cuda:0").to(torch.bfloat16) for n in (h, 1))
+    w = torch.randn(8, generator=g, device="cuda:0").to(torch.bfloat16)
+    pos, rope = torch.arange(t, device="cuda:0"), nf4.Rope(8)
+    y, yk, dx, dk, dx2, dk2 = (torch.full_like(a, 3.0) for a in (x, k, x, k, x, k))
+    dw, dwk = torch.zeros(8, device="cuda:0"), torch.zeros(8, device="cuda:0")
+    nf4.qlora_rope_fwd(rope, pos, x, k, y, yk, q_weight=w, k_weight=w)
+    nf4.qlora_rope_bwd(rope, pos, y, yk, dx, dk, q=x, k=k, q_weight=w, k_weight=w)
+    nf4.qlora_rope_bwd(rope, pos, y, yk, dx2, dk2, q=x, k=k, q_weight=w, k_weight=w, dq_weight=dw, dk_weight=dwk)
+    assert torch.equal(dx, dx2) and torch.equal(dk, dk2)
+    for a in (0, 65500, 131060, t - 50):
+        s = slice(a, a + 50)
+        one, onek = torch.empty_like(x[s]), torch.empty_like(k[s])
+        nf4.qlora_rope_fwd(rope, pos[s], x[s], k[s], one, onek, q_weight=w, k_weight=w)
+        assert torch.equal(one, y[s]) and torch.equal(onek, yk[s])
+        nf4.qlora_rope_bwd(rope, pos[s], y[s], yk[s], one, onek, q=x[s], k=k[s], q_weight=w, k_weight=w)
+        assert torch.equal(one, dx[s]) and torch.equal(onek, dk[s])
+    # without a rotation the weight's gradient is a plain sum
+    nf4.qlora_rope_bwd(nf4.Rope(0), None, y, yk, dx, dk, q=x, k=k, q_weight=w, k_weight=w, dq_weight=dw, dk_weight=dwk)
+    for d, i, got in ((y, x, dw), (yk, k, dwk)):
+        i = i.double()
+        terms = d.double() * i * torch.rsqrt(i.square().mean(-1, keepdim=True) + 1e-6)
+        assert torch.all((got.double() - terms.sum((0, 1))).abs() <= 1.8e-5 * terms.abs().sum((0, 1)))
+
+
 def test_gradient_against_differences():
     """Central differences of the framework's own forward in the direction of a perturbation: fp32-like accuracy is out of
     reach in bf16, so the loss is taken over many values: its rounding error is U times the root of the sum of squares."""

@@ -270,23 +270,34 @@ __global__ __launch_bounds__(256) void rope_bwd_kernel(const RopeArgs a, float* 
 }
 
 // dw from the workgroups' sums: workgroup (x, y) takes columns 8 x .. 8 x + 7 of the queries' (y = 0) or the keys' weight;
-// thread (slice, column) adds every 32nd workgroup's sums, and the slices are added in order.
-__global__ __launch_bounds__(256) void rope_dw_kernel(const float* part, int q_groups, int groups, int d, float* dqw, float* dkw,
+// thread (slice, column) adds every 128th workgroup's sums, and the slices are added in order, by sixteens.
+__global__ __launch_bounds__(1024) void rope_dw_kernel(const float* part, int q_groups, int groups, int d, float* dqw, float* dkw,
                                                       int accumulate) {
-  __shared__ float s[32][9];
+  __shared__ float s[128][9];
   const int x = (int)threadIdx.x & 7, slice = (int)threadIdx.x >> 3, c = (int)blockIdx.x * 8 + x;
   float* out = blockIdx.y ? dkw : dqw;
   if (!out) return;   // the whole workgroup
   const int from = blockIdx.y ? q_groups : 0, to = blockIdx.y ? groups : q_groups;
   float v = 0.f;
-#pragma unroll 8
-  for (int w = from + slice; w < to; w += 32) v += part[(int64_t)w * 128 + c];
+  for (int w = from + slice; w < to; w += 128 * 16) {   // sixteen on their way; past the end the last again, not added
+    float p[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) p[k] = part[(int64_t)min(w + 128 * k, to - 1) * 128 + c];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v += w + 128 * k < to ? p[k] : 0.f;
+  }
   s[slice][x] = v;
   __syncthreads();
+  if (slice >= 8) return;
+  v = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v += s[16 * slice + k][x];
+  s[16 * slice][x] = v;
+  __builtin_amdgcn_wave_barrier();   // the first wave alone is left: its writes come before its reads
   if (slice) return;
   v = 0.f;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) v += s[k][x];
+  for (int k = 0; k < 8; ++k) v += s[16 * k][x];
   out[c] = accumulate ? out[c] + v : v;
 }
 
@@ -348,7 +359,7 @@ hipError_t launch_rope_bwd(const RopeArgs& args, float* dqw, float* dkw, int acc
   if (e != hipSuccess || !dw) return e;
   RopeArgs p = a;
   const int groups = rope_plan(p, true);
-  hipLaunchKernelGGL(rope_dw_kernel, dim3((unsigned)(a.d / 8), 2), dim3(256), 0, stream, part, p.q_groups, groups, a.d, dqw, dkw, accumulate);
+  hipLaunchKernelGGL(rope_dw_kernel, dim3((unsigned)(a.d / 8), 2), dim3(1024), 0, stream, part, p.q_groups, groups, a.d, dqw, dkw, accumulate);
   return hipGetLastError();
 }
 

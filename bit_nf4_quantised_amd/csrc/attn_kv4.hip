@@ -53,6 +53,11 @@ __device__ __forceinline__ bool kv4_lost(uint32_t absmax) { return absmax >= kBf
 // The contraction of the first product may run over d in any order, so lane (n, q) takes the block q (d <= 64: half
 // the block q / 2) of keys n and 16 + n as it lies in the cache, 16 bytes, and its dequantised dwords are the
 // operand. Values go through an LDS tile of the wave's own, from which transpose loads read them across.
+// Bound by the vector instructions of the tables' codes (3 a value, shared by the 8 or 16 rows that a token or two leave), then
+// by memory: one token each over 16 caches of 1 to 8191 keys, 64 heads over 8, d 128, takes 25 us (63 MB, 2.5 TB/s) in NF4;
+// 131071 and 60001 keys in E2M1, whose codes cost 2 instructions a value, 47 (220 MB, 4.7 TB/s). Three waves a SIMD: the
+// registers of four spill (32 us for the first of these). One range with 8 or 16 waves a workgroup instead of several
+// ranges and a join takes 10.3 to 13 us for 601 keys that take 8.2 so: the codes of a key head are then one unit's work.
 template <int DP>
 struct Kv4Few;
 // d > 64: lane (n, q) holds block q of keys n and 16 + n, key and value
@@ -334,6 +339,11 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(cons
 // Many rows: WV waves of 32 rows each share tiles of 64 keys in LDS, which they dequantise together, two tiles deep: while
 // a tile is multiplied, the next one's codes become values and the one after it is on its way from memory. Products are
 // v_mfma_f32_32x32x16_bf16 as in attn.hip. A workgroup's keys are one range of the sequence's.
+// Bound by the codes, the softmax and the products together, which two waves a SIMD, in step at the barriers, overlap little: 512
+// tokens each on 4096 and 1911 keys, 32 heads over 8, d 128, NF4, take 77 to 79 us (590 TFLOP/s; the vector unit and the matrix
+// unit are busy 54 and 37 % of the cycles of the units at work). With 4 waves, of which two workgroups fit a unit, 95:
+// twice the codes. Waves that form codes before and after their products in turn 86; products of both key halves in
+// turn, and priority for them: no gain.
 template <int DP, int WV>
 struct Kv4Many {
   static constexpr int UNITS = 64 * (DP / 32) * 2, N = (UNITS + WV * 64 - 1) / (WV * 64);   // blocks of a tile, and of a thread
@@ -514,7 +524,10 @@ __global__ __launch_bounds__(WV * 64, 2) void attn_kv4_many_kernel(const AttnKv4
 
 // ------------------------------------------------------------------------------------------
 // Joins the ranges: an item is a row and key head of a sequence of several ranges. 32 lanes hold its columns, 4 each; S groups
-// of them take its ranges in turn, four at a time on their way, and are joined in order.
+// of them take its ranges in turn, four at a time on their way, and are joined in order. Bound by memory where rows are many
+// (2048 workgroups of 8 items of 2 ranges, 6 us) and by latency where ranges are (3.6 us for 32 items, 6.5 for 128 of over 90).
+// S = 8 for more than 4 ranges, else 1: the whole attention of 8 rows over 130000 keys takes 52 us with 8 and 68 with 1, that of
+// two times 2048 rows over 4000 keys (2 ranges) 110 with 8 and 86 with 1.
 template <int S>
 __global__ __launch_bounds__(256) void attn_kv4_join_kernel(const AttnFwdArgs a, const AttnSeqs sq, const Kv4Split sp) {
   constexpr int ITEMS = 8 / S;
@@ -615,7 +628,11 @@ static int64_t kv4_keys(const AttnSeq& s, int window) { return std::max<int64_t>
 
 // The kernels: rows of a workgroup, keys of a step (a range is a multiple of it), workgroups that a compute unit holds, and
 // the time of a step in us with 1, 2 .. of them on it, d = 128 and d <= 64, for tables and for E2M1 each. Measured as the
-// difference of 16 steps and 8 of workgroups that are all alike.
+// difference of 16 steps and 8 of workgroups that are all alike. Calls (us) with each of the four, NF4, d 128:
+//   24 rows, 16 times 4000 keys, 8 key heads   51   36   53   67         100 rows, 4 times 8000   83   57   45   49
+//   64 rows, 16 times 1000 keys                26   21   28   30         400 rows, 8000 keys      72   56   45   38
+//   1200 rows, twice 4000 keys                174  135   75   64         100 rows, 1000 keys      11.5 11.8 14.2 13.6
+// The estimate below chose the fastest of each, or one within 0.3 us of it.
 struct Kv4Kernel {
   int rows, waves, step, most;
   double us[2][2][3];

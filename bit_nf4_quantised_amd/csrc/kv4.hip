@@ -5,7 +5,7 @@
 // its value, 16 values a lane. A workgroup takes 256 / (2 B) rows (B blocks a row, 1, 2 or 4, the last of them perhaps
 // empty): neighbouring tokens of one head, so that stores to a cache whose heads come first run on, or, where the
 // sequences are shorter than that, tokens of several heads. Where a lane stands takes shifts alone: with divisions that
-// took three times the instructions of the codes, and 8191 tokens of 8 heads, d 128, FP4, 20 us to write and 14 to read.
+// took three times the instructions of the codes, and 8191 tokens of 8 heads, d 128, FP4, 20 us to write and 14.6 to read.
 //
 // The nearest code to x is decided exactly, ties to the lower code, by an approximate quotient (2^-22, relative): x and
 // absmax have 8 significant bits, and a quotient of two such numbers is a tie or well away from one.
@@ -15,7 +15,9 @@
 //   INT4  ceil(7 x / absmax - 1/2 - 1e-5), which a tie passes downwards: other quotients are 1e-4 away from one.
 //   FP4   the hardware's conversion of 6 x / absmax, of which 1e-5 of its magnitude is taken away first, so that a
 //         tie falls to the lower code; other quotients are 1e-4 away, relative. -0 becomes 0.
-// Bound by memory: 2 bytes a value on one side, 0.5625 on the other.
+// Bound by memory: 2 bytes a value on one side, 0.5625 on the other. Those 8191 tokens are written in 10 us and read in 10.4
+// (43 MB, 4.3 and 4.1 TB/s); 6007 of them in NF4 are read in 8.8 us (3.6 TB/s), 1024 written in 4.4, 16 written in 3.7 and
+// read in 2.9 (the latency of arguments and loads, and of the bins).
 #include "kv4.h"
 
 #include <string.h>

@@ -17,6 +17,9 @@
 // leaves its lane. A workgroup works on queries or on keys alone, so that strides and weights are the same for
 // all its lanes; a group of L lanes takes heads of one token, four at a time, whose loads are all on their way
 // together and which share the lane's four sines and cosines. All sums are fp32; outputs are rounded once.
+// 4096 tokens of 64 and 8 heads, d 128, normed: forward 25 us (151 MB, 6.0 TB/s), backward 42 (226 MB, 5.4 TB/s) and
+// 4.4 for the weights' sums; 32 and 56 with queries and keys in one workgroup and sines by polynomials. 2048 tokens of 32 and 8
+// heads, not normed: 9.4 either way (42 MB, 4.5 TB/s). One token: 3.3, the latency of its arguments and loads.
 #include "common.h"
 #include "launch.h"
 

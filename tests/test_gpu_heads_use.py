@@ -355,6 +355,125 @@ def test_example_decodes_over_both_caches():
     assert _rel(four, like) < 5e-3 * 2 ** 0.5      # the probabilities' and the output's roundings differ
 
 
+def test_calls_with_nothing_to_do():
+    """No tokens, no sequences, sequences without new tokens, an empty cache: nothing is written and nothing fails."""
+    import bit_nf4_quantised_amd as nf4
+    e, ek, some = (torch.empty(*s, dtype=torch.bfloat16, device="cuda:0") for s in ((0, 4, 64), (0, 2, 64), (3, 4, 64)))
+    some.fill_(3.0)
+    pos, rope = torch.empty(0, dtype=torch.int64, device="cuda:0"), nf4.Rope(64)
+    w, dw = torch.ones(64, dtype=torch.bfloat16, device="cuda:0"), torch.full((64,), 2.0, device="cuda:0")
+    nf4.qlora_rope_fwd(rope, pos, e, ek, e, ek)
+    nf4.qlora_rope_bwd(rope, pos, e, ek, e, ek, q=e, q_weight=w, dq_weight=dw, accumulate=True)
+    none, full = [nf4.empty_kv4(0, 2, 64) for _ in range(2)], [nf4.empty_kv4(9, 2, 64) for _ in range(2)]
+    for t in full:
+        t.codes.fill_(7)
+        t.absmax.fill_(1.0)
+    nf4.qlora_kv4_write(nf4.AttnSeqs([]), ek, ek, *none)
+    nf4.qlora_kv4_write(nf4.AttnSeqs([(0, 0, 0, 9), (0, 0, 4, 0)]), ek, ek, *full)
+    nf4.qlora_kv4_read(nf4.AttnSeqs([(0, 0, 0, 9)]), *full, ek, ek)
+    o, lse = torch.full_like(some, 5.0), torch.full((4, 3), 5.0, device="cuda:0")
+    nf4.qlora_attn_kv4_fwd(nf4.AttnSeqs([]), some, *full, o, lse)
+    nf4.qlora_attn_kv4_fwd(nf4.AttnSeqs([(0, 0, 0, 9)]), some, *full, o, lse)
+    nf4.qlora_attn_kv4_fwd(nf4.AttnSeqs([]), e, *none, torch.empty_like(e))
+    torch.cuda.synchronize()
+    assert torch.all(o == 5) and torch.all(lse == 5) and torch.all(full[0].codes == 7) and torch.all(full[1].absmax == 1) and torch.all(dw == 2)
+    nf4.qlora_attn_kv4_fwd(nf4.AttnSeqs([(1, 2, 0, 0)]), some, *none, o, lse)      # rows, but no keys
+    assert torch.all(o[0] == 5) and torch.all(o[1:] == 0) and torch.all(torch.isneginf(lse[:, 1:])) and torch.all(lse[:, 0] == 5)
+
+
+def test_heads_that_are_one_in_memory():
+    """Inputs whose heads are broadcast (head stride 0), and a query that is every head's: as their copies."""
+    import bit_nf4_quantised_amd as nf4
+    gen = torch.Generator(device="cuda:0").manual_seed(3)
+    one = torch.randn(40, 1, 96, generator=gen, device="cuda:0").to(torch.bfloat16)
+    q, k = one.expand(-1, 8, -1), one.expand(-1, 4, -1)
+    qc, kc = q.contiguous(), k.contiguous()
+    pos, rope = torch.arange(40, device="cuda:0") * 3, nf4.Rope(96)
+    w = torch.randn(96, generator=gen, device="cuda:0").to(torch.bfloat16)
+    got, want = [[torch.empty_like(t) for t in (qc, kc, qc, kc)] + [torch.empty(96, device="cuda:0") for _ in range(2)] for _ in range(2)]
+    for (a, b), o in (((q, k), got), ((qc, kc), want)):
+        nf4.qlora_rope_fwd(rope, pos, a, b, o[0], o[1], q_weight=w)
+        nf4.qlora_rope_bwd(rope, pos, a, b, o[2], o[3], q=a, k=b, q_weight=w, k_weight=w, dq_weight=o[4], dk_weight=o[5])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    seqs, caches = nf4.AttnSeqs([(0, 40, 0, 40)]), [[nf4.empty_kv4(40, 4, 96) for _ in range(2)] for _ in range(2)]
+    outs = [torch.empty_like(qc) for _ in range(2)]
+    for (a, b), c, o in (((q, k), caches[0], outs[0]), ((qc, kc), caches[1], outs[1])):
+        nf4.qlora_kv4_write(seqs, b, b, *c)
+        nf4.qlora_attn_kv4_fwd(seqs, a, *c, o)
+    assert torch.equal(outs[0], outs[1])
+    assert all(torch.equal(x.codes, y.codes) and torch.equal(x.absmax, y.absmax) for x, y in zip(*caches))
+
+
+def test_sequences_that_share_keys():
+    """Several continuations of one prompt: ranges that start together, lie in one another, and are the same twice. Against each
+    alone, whose ranges may be others: both round probabilities (the terms) and outputs once, so they differ by twice that."""
+    import bit_nf4_quantised_amd as nf4
+    gen = torch.Generator(device="cuda:0").manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda:0").to(torch.bfloat16)  # noqa: E731
+    k4, v4 = nf4.empty_kv4(3000, 2, 128), nf4.empty_kv4(3000, 2, 128)
+    nf4.qlora_kv4_write(nf4.AttnSeqs([(0, 3000, 0, 3000)]), r(3000, 2, 128), r(3000, 2, 128), k4, v4)
+    keys = [(0, 3000), (0, 3000), (0, 2000), (500, 1700), (2999, 1)]
+    q = r(5, 16, 128)
+    q[1] = q[0]
+    o, terms, alone = torch.empty_like(q), torch.empty_like(q), torch.empty(1, 16, 128, dtype=q.dtype, device=q.device)
+    seqs = nf4.AttnSeqs([(i, 1, k0, n) for i, (k0, n) in enumerate(keys)])
+    nf4.qlora_attn_kv4_fwd(seqs, q, k4, v4, o)
+    kb, vb = r(3000, 2, 128), r(3000, 2, 128)
+    nf4.qlora_kv4_read(nf4.AttnSeqs([(0, 3000, 0, 3000)]), k4, v4, kb, vb)
+    nf4.qlora_attn_fwd(seqs, q, kb, vb.abs(), terms)
+    assert torch.equal(o[0], o[1])
+    for i, (k0, n) in enumerate(keys):
+        nf4.qlora_attn_kv4_fwd(nf4.AttnSeqs([(0, 1, k0, n)]), q[i:i + 1], k4, v4, alone)
+        a, b, t = alone[0].float(), o[i].float(), terms[i].float()
+        assert torch.all((a - b).abs() <= 2 * (U * b.abs() + (U + 1e-4) * t) * (1 + U))
+
+
+def test_a_training_step_replays_from_a_graph():
+    """Forward and backward of normed and rotated heads with attention between them, the weights' gradients added to: three
+    replays against three eager steps, bit for bit."""
+    import bit_nf4_quantised_amd as nf4
+    gen = torch.Generator(device="cuda:0").manual_seed(8)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda:0").to(torch.bfloat16)  # noqa: E731
+    lens, heads, kv, d = [300, 1, 99], 8, 2, 80
+    M = sum(lens)
+    q, k, v, do, wq, wk = r(M, heads, d), r(M, kv, d), r(M, kv, d), r(M, heads, d), r(d), r(d)
+    pos, rope, seqs = torch.cat([torch.arange(n) for n in lens]).to("cuda:0"), nf4.Rope(32, interleaved=True), nf4.AttnSeqs.packed(lens)
+    acc = torch.zeros(2, d, device="cuda:0")
+    outs = [torch.empty_like(t) for t in (q, k, q, q, k, k, q, k)] + [acc]
+
+    def step():
+        y, yk, o, dy, dyk, dv, dx, dxk, _ = outs
+        lse = torch.empty(heads, M, device="cuda:0")
+        nf4.qlora_rope_fwd(rope, pos, q, k, y, yk, q_weight=wq, k_weight=wk)
+        nf4.qlora_attn_fwd(seqs, y, yk, v, o, lse)
+        nf4.qlora_attn_bwd(seqs, y, yk, v, o, lse, do, dy, dyk, dv)
+        nf4.qlora_rope_bwd(rope, pos, dy, dyk, dx, dxk, q=q, k=k, q_weight=wq, k_weight=wk, dq_weight=acc[0], dk_weight=acc[1], accumulate=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2, 3):
+        gen.manual_seed(seed)
+        for t in (q, k, v, do):
+            t.copy_(torch.randn(t.shape, generator=gen, device="cuda:0"))
+        start = acc.clone()
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in outs]
+        for t in outs[:8]:
+            t.zero_()
+        acc.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(outs, want)):
+            assert torch.equal(a, b), (seed, i)
+
+
 def test_tensors_of_another_device_than_the_current_one_are_refused(monkeypatch):
     """Before anything is launched; the current device is made to look like another one."""
     import bit_nf4_quantised_amd as nf4

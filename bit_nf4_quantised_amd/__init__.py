@@ -179,13 +179,15 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _stream_on(stream, *tensors):
-    """_stream, for a call with these tensors (None: not there): all must live on the current device, on whose streams
-    the kernels run. A kernel that is given another GPU's memory faults where the two are not peers."""
+def _stream_on(stream, gpu, *tensors):
+    """_stream, for a call with tensors of device `gpu` and these (None: not there): all must live on the current device, on
+    whose streams the kernels run. A kernel that is given another GPU's memory faults where the two are not peers."""
     current = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != current:
-            raise ValueError(f"tensor lives on {t.device} and the current device is cuda:{current}")
+            gpu = t.get_device()
+    if gpu != current:
+        raise ValueError(f"a tensor lives on GPU {gpu} and the current device is GPU {current}")
     if stream is None and _raw_stream is not None:
         return _raw_stream(current)
     return _stream(stream)
@@ -652,7 +654,7 @@ class AttnSeqs:
         self.causal, self.window = bool(causal), int(window)
         self._seqs = (ctypes.c_int64 * max(len(flat), 4))(*flat)
         self._last = (None, None)   # what the last configuration was made of, and it
-        self._need4 = (None, None, 0)   # a configuration, a codebook, and the workspace of qlora_attn_kv4_fwd for them
+        self._plans = {}            # of the calls over 4-bit caches (_planned)
 
     @staticmethod
     def packed(lengths, causal: bool = True, window: int = 0) -> "AttnSeqs":
@@ -680,6 +682,9 @@ class AttnSeqs:
         return ctypes.byref(cfg)
 
     def workspace_bytes(self, q, k, backward: bool = False, scale: float | None = None) -> int:
+        """Of a call with these queries and keys; of qlora_attn_kv4_fwd if k is a Kv4."""
+        if isinstance(k, Kv4):
+            return int(lib.qlora_attn_kv4_workspace_bytes(self._config(q, k, scale), self.count, self._seqs, k.codebook))
         return int(lib.qlora_attn_workspace_bytes(self._config(q, k, scale), self.count, self._seqs,
                                                   int(bool(backward))))
 
@@ -708,6 +713,33 @@ def _attn_tensors(*pairs):
         v.extend((t.data_ptr(), token, head))
     at = v.buffer_info()[0]
     return [v, *range(at, at + 24 * len(pairs), 24)]
+
+
+def _planned(plans, head, tensors, make):
+    """What make() marshals for tensors [tokens, heads, d] (None: not there), kept in `plans` by `head` and all of the tensors
+    that it may depend on, which their memory is not; their qlora_attn_tensor structures as an array, to be kept until
+    the library has read them, and the array's address, 24 bytes for each."""
+    key = [*head]
+    for t in tensors:
+        key += (t.shape, t.stride(), t.dtype, t.get_device()) if t is not None else (None,)
+    key = tuple(key)
+    plan = plans.get(key)
+    if plan is None:
+        made, v = make(), array("q")
+        for t in tensors:
+            v.extend(_attn_tensors((t, t.shape))[0] if t is not None else (0, 0, 0))
+            v[-3] = 0
+            if t is not None and t.get_device() != tensors[0].get_device():
+                raise ValueError("the tensors must live on one GPU")
+        if len(plans) >= 256:   # a program of ever new shapes
+            plans.clear()
+        plans[key] = plan = v, made
+    v, i = plan[0][:], 0
+    for t in tensors:
+        if t is not None:
+            v[i] = t.data_ptr()
+        i += 3
+    return plan[1], v, v.buffer_info()[0]
 
 
 def _lse_ptr(lse, q):
@@ -777,7 +809,7 @@ class Rope:
         if len(self._inv_freq) * 2 != self.rot:
             raise ValueError("one frequency for each of the rot / 2 pairs")
         self._freq = (ctypes.c_double * max(len(self._inv_freq), 1))(*self._inv_freq)
-        self._plans = {}   # configuration and strides of the calls' tensors, by their shapes and strides
+        self._plans = {}
 
     # what the plans were made with: read only
     rot = property(lambda self: self._made[0])
@@ -785,56 +817,27 @@ class Rope:
     factor = property(lambda self: self._made[2])
     inv_freq = property(lambda self: self._inv_freq)
 
-    def _plan(self, key, eps, qs, ks):
-        """Checks the shapes of a call's query-like and key-like tensors and marshals what does not change."""
-        q, k = qs[0], ks[0]
-        for ts, like in ((qs, q), (ks, k)):
-            for t in ts:
-                if t is not None and (like is None or t.dim() != 3 or t.shape != like.shape):
-                    raise ValueError("shape mismatch: heads are [tokens, heads, d], gradients and outputs like their inputs")
-        if any((t is None) != (k is None) for t in ks[:2]) or (k is not None and (k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2])):
-            raise ValueError("shape mismatch: keys go with keys, of the queries' tokens and head size")
-        at = array("q")
-        for t in qs + ks:
-            at.extend(_attn_tensors((t, t.shape))[0] if t is not None else (0, 0, 0))
-        tokens, heads, d = q.shape
-        cfg = CRopeConfig(heads, 0 if k is None else k.shape[1], d, self.rot, int(self.interleaved), eps, self.factor, tokens)
-        if len(self._plans) >= 256:   # a program of ever new shapes
-            self._plans.clear()
-        need = int(lib.qlora_rope_workspace_bytes(ctypes.byref(cfg)))
-        self._plans[key] = plan = (at, ctypes.byref(cfg), tokens, need)
-        return plan
+    def _planned(self, eps, qs, ks):
+        """_planned for a call's query-like and key-like tensors, which must be alike: with the configuration, the tokens and the
+        bytes of the backward's workspace."""
+        def make():
+            q, k = qs[0], ks[0]
+            for ts, like in ((qs, q), (ks, k)):
+                for t in ts:
+                    if t is not None and (like is None or t.dim() != 3 or t.shape != like.shape):
+                        raise ValueError("shape mismatch: heads are [tokens, heads, d], gradients and outputs like their inputs")
+            if any((t is None) != (k is None) for t in ks[:2]) or (k is not None and (k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2])):
+                raise ValueError("shape mismatch: keys go with keys, of the queries' tokens and head size")
+            tokens, heads, d = q.shape
+            cfg = CRopeConfig(heads, 0 if k is None else k.shape[1], d, self.rot, int(self.interleaved), eps, self.factor, tokens)
+            return ctypes.byref(cfg), tokens, self.workspace_bytes(q, k)
+        return _planned(self._plans, (eps,), qs + ks, make)
 
-    def _tensors(self, eps, qs, ks):
-        """The qlora_attn_tensor structures of the tensors (None: not there), as an array to be kept until the library has
-        read them, their addresses, and the plan: those structures' strides, the configuration, the tokens and the bytes of
-        the backward's workspace."""
-        key = [eps]
-        for t in qs + ks:
-            if t is None:
-                key.append(None)
-            else:
-                key.append(t.shape)
-                key.append(t.stride())
-        key = tuple(key)
-        plan = self._plans.get(key) or self._plan(key, eps, qs, ks)
-        v = plan[0][:]
-        at = v.buffer_info()[0]
-        ptrs = []
-        gpu = qs[0].get_device()
-        if gpu < 0:
-            raise ValueError("tensor must live on the GPU")
-        for i, t in enumerate(qs + ks):
-            if t is None:
-                ptrs.append(None)
-                continue
-            if t.dtype not in _BF16:
-                _dtype(t, *_BF16)
-            if t.get_device() != gpu:
-                raise ValueError("the tensors must live on one GPU")
-            v[3 * i] = t.data_ptr()
-            ptrs.append(at + 24 * i)
-        return v, ptrs, plan
+    def workspace_bytes(self, q, k=None) -> int:
+        """Of qlora_rope_bwd for weights' gradients."""
+        tokens, heads, d = q.shape
+        cfg = CRopeConfig(heads, 0 if k is None else k.shape[1], d, self.rot, int(self.interleaved), 0.0, self.factor, tokens)
+        return int(lib.qlora_rope_workspace_bytes(ctypes.byref(cfg)))
 
 
 def _rope_positions(rope, positions, tokens):
@@ -860,10 +863,11 @@ def qlora_rope_fwd(rope: Rope, positions, q, k, q_out, k_out, q_weight=None, k_w
     """Query and key heads [tokens, heads, d] (bf16, tokens and heads may be strided), normed over d where a weight
     [d] is given, then rotated by their tokens' positions (int64 [tokens]). k and k_out may be None; an output may
     be its input."""
-    keep, (tq, to, tk, tko), (_, cfg, tokens, _) = rope._tensors(eps, (q, q_out), (k, k_out))
-    _check(lib.qlora_rope_fwd(cfg, rope._freq, _rope_positions(rope, positions, tokens), tq, tk, _rope_weight(q_weight, q),
-                              _rope_weight(k_weight, k), to, tko,
-                              _stream_on(stream, q, positions, q_weight, k_weight)), "qlora_rope_fwd")
+    (cfg, tokens, _), keep, at = rope._planned(eps, (q, q_out), (k, k_out))
+    tk, tko = (None, None) if k is None else (at + 48, at + 72)
+    _check(lib.qlora_rope_fwd(cfg, rope._freq, _rope_positions(rope, positions, tokens), at, tk, _rope_weight(q_weight, q),
+                              _rope_weight(k_weight, k), at + 24, tko,
+                              _stream_on(stream, q.get_device(), positions, q_weight, k_weight)), "qlora_rope_fwd")
 
 
 def qlora_rope_bwd(rope: Rope, positions, dq_out, dk_out, dq, dk, q=None, k=None, q_weight=None, k_weight=None,
@@ -873,8 +877,10 @@ def qlora_rope_bwd(rope: Rope, positions, dq_out, dk_out, dq, dk, q=None, k=None
     weights' (float32 [d], added to with accumulate). Normed heads need the forward's inputs q and k."""
     if (q_weight is not None and q is None) or (k_weight is not None and k is None):
         raise ValueError("the backward of normed heads needs their inputs")
-    keep, (tgo, tdq, tq, tgk, tdk, tk), (_, cfg, tokens, need) = rope._tensors(
+    (cfg, tokens, need), keep, at = rope._planned(
         eps, (dq_out, dq, q if q_weight is not None else None), (dk_out, dk, k if k_weight is not None else None))
+    tgk, tdk = (None, None) if dk_out is None else (at + 72, at + 96)
+    tq, tk = None if q_weight is None else at + 48, None if k_weight is None else at + 120
     pdw = None, None
     nbytes = 0
     if dq_weight is not None or dk_weight is not None:
@@ -886,9 +892,9 @@ def qlora_rope_bwd(rope: Rope, positions, dq_out, dk_out, dq, dk, q=None, k=None
             ws = _scratch(max(need, 256), dq.device, stream)
         nbytes = ws.numel() * ws.element_size()
     _check(lib.qlora_rope_bwd(cfg, rope._freq, _rope_positions(rope, positions, tokens), tq, tk, _rope_weight(q_weight, dq_out),
-                              _rope_weight(k_weight, dk_out), tgo, tgk, tdq, tdk, *pdw, int(bool(accumulate)),
+                              _rope_weight(k_weight, dk_out), at, tgk, at + 24, tdk, *pdw, int(bool(accumulate)),
                               None if ws is None else _ptr(ws), nbytes,
-                              _stream_on(stream, dq, positions, q_weight, k_weight, dq_weight, dk_weight, ws)),
+                              _stream_on(stream, dq.get_device(), positions, q_weight, k_weight, dq_weight, dk_weight, ws)),
            "qlora_rope_bwd")
 
 
@@ -922,6 +928,7 @@ class Kv4:
         self.codes, self.absmax, self.d, self.codebook = codes, absmax, int(d), _book(codebook)
         self.shape = (tokens, heads, self.d)
         self._c = CKv4(codes.data_ptr(), absmax.data_ptr(), at, ah, self.codebook)
+        self._ptr = ctypes.byref(self._c)
 
 
 def empty_kv4(tokens: int, kv_heads: int, d: int, device="cuda", codebook="nf4") -> Kv4:
@@ -931,57 +938,49 @@ def empty_kv4(tokens: int, kv_heads: int, d: int, device="cuda", codebook="nf4")
                torch.empty(kv_heads, tokens, nb, dtype=torch.bfloat16, device=device).permute(1, 0, 2), d, codebook)
 
 
-def _kv4_pair(k4, v4, heads, d):
-    if k4.shape != v4.shape or k4.codebook != v4.codebook:
-        raise ValueError("k4 and v4 must be alike")
-    if k4.d != d or (heads is not None and k4.shape[1] != heads):
-        raise ValueError("shape mismatch between the cache and the tensors")
-    return ctypes.byref(k4._c), ctypes.byref(v4._c)
-
-
-def _kv4_copy(seqs, k, v, k4, v4):
-    if k.dim() != 3:
-        raise ValueError("k and v are [tokens, kv heads, d]")
-    pk, pv = _kv4_pair(k4, v4, k.shape[1], k.shape[2])
-    keep, tk, tv = _attn_tensors((k, k.shape), (v, k.shape))
-    return seqs._config(k, k4, None), (tk, tv), (pk, pv), keep
+def _kv4_planned(seqs, tensors, heads, k4, v4, scale, need):
+    """_planned for a call over a cache, whose k4 and v4 must be alike and go with the tensors: with the configuration and,
+    if need, the bytes of the attention's workspace."""
+    def make():
+        t = tensors[0]
+        if t.dim() != 3 or any(x.shape != t.shape for x in tensors):
+            raise ValueError("shape mismatch: the tensors are [tokens, heads, d] and alike")
+        if k4.shape != v4.shape or k4.codebook != v4.codebook:
+            raise ValueError("k4 and v4 must be alike")
+        if k4.d != t.shape[2] or (heads and k4.shape[1] != t.shape[1]):
+            raise ValueError("shape mismatch between the cache and the tensors")
+        cfg = seqs._config(t, k4, scale)
+        return cfg, int(lib.qlora_attn_kv4_workspace_bytes(cfg, seqs.count, seqs._seqs, k4.codebook)) if need else 0
+    return _planned(seqs._plans, (need, scale, seqs.causal, seqs.window, k4.shape, v4.shape, k4.codebook, v4.codebook), tensors, make)
 
 
 def qlora_kv4_write(seqs: AttnSeqs, k, v, k4: Kv4, v4: Kv4, stream=None) -> None:
     """New keys and values k, v [tokens, kv heads, d] (bf16, strided) into a 4-bit cache: the nq tokens of every
     sequence (q0, nq, k0, nk) become its last nq keys, so the list that the attention then takes says where."""
-    cfg, (tk, tv), (pk, pv), keep = _kv4_copy(seqs, k, v, k4, v4)
-    _check(lib.qlora_kv4_write(cfg, seqs.count, seqs._seqs, tk, tv, pk, pv, _stream_on(stream, k, v, k4.codes, v4.codes)),
-           "qlora_kv4_write")
+    (cfg, _), keep, at = _kv4_planned(seqs, (k, v), True, k4, v4, None, False)
+    _check(lib.qlora_kv4_write(cfg, seqs.count, seqs._seqs, at, at + 24, k4._ptr, v4._ptr,
+                               _stream_on(stream, k.get_device(), k4.codes, v4.codes)), "qlora_kv4_write")
 
 
 def qlora_kv4_read(seqs: AttnSeqs, k4: Kv4, v4: Kv4, k, v, stream=None) -> None:
     """The last nq keys and values of every sequence out of a 4-bit cache, in bf16: into tokens q0 .. of k and v."""
-    cfg, (tk, tv), (pk, pv), keep = _kv4_copy(seqs, k, v, k4, v4)
-    _check(lib.qlora_kv4_read(cfg, seqs.count, seqs._seqs, pk, pv, tk, tv, _stream_on(stream, k, v, k4.codes, v4.codes)),
-           "qlora_kv4_read")
+    (cfg, _), keep, at = _kv4_planned(seqs, (k, v), True, k4, v4, None, False)
+    _check(lib.qlora_kv4_read(cfg, seqs.count, seqs._seqs, k4._ptr, v4._ptr, at, at + 24,
+                              _stream_on(stream, k.get_device(), k4.codes, v4.codes)), "qlora_kv4_read")
 
 
 def qlora_attn_kv4_fwd(seqs: AttnSeqs, q, k4: Kv4, v4: Kv4, o, lse=None, scale: float | None = None, ws=None,
                        stream=None) -> None:
     """qlora_attn_fwd over a 4-bit cache: q, o [query tokens, heads, d] (bf16, strided)."""
-    if q.dim() != 3:
-        raise ValueError("q is [query tokens, heads, d]")
-    pk, pv = _kv4_pair(k4, v4, None, q.shape[2])
-    keep, tq, to = _attn_tensors((q, q.shape), (o, q.shape))
-    cfg = seqs._config(q, k4, scale)
-    plse = _lse_ptr(lse, q)
+    (cfg, need), keep, at = _kv4_planned(seqs, (q, o), False, k4, v4, scale, True)
+    plse = None if lse is None else _lse_ptr(lse, q)
     pws, nbytes = None, 0
-    if ws is None:
-        last, book, need = seqs._need4      # a configuration is never written to, so the same one has the same need
-        if last is not cfg._obj or book != k4.codebook:
-            need = int(lib.qlora_attn_kv4_workspace_bytes(cfg, seqs.count, seqs._seqs, k4.codebook))
-            seqs._need4 = (cfg._obj, k4.codebook, need)
-        ws = _scratch(need, q.device, stream) if need else None
+    if ws is None and need:
+        ws = _scratch(need, q.device, stream)
     if ws is not None:
         pws, nbytes = _ptr(ws), ws.numel() * ws.element_size()
-    _check(lib.qlora_attn_kv4_fwd(cfg, seqs.count, seqs._seqs, tq, pk, pv, to, plse, pws, nbytes,
-                                  _stream_on(stream, q, o, k4.codes, v4.codes, lse, ws)), "qlora_attn_kv4_fwd")
+    _check(lib.qlora_attn_kv4_fwd(cfg, seqs.count, seqs._seqs, at, k4._ptr, v4._ptr, at + 24, plse, pws, nbytes,
+                                  _stream_on(stream, q.get_device(), k4.codes, v4.codes, lse, ws)), "qlora_attn_kv4_fwd")
 
 
 # ------------------------------------------------------------------------- format variants

@@ -185,6 +185,12 @@ def test_rope_frequencies():
             setattr(r, name, 1)
 
 
+def test_binding_sizes_workspaces():
+    x, y = torch.empty(3, 4, 64), torch.empty(3, 2, 64)
+    assert q.Rope(64).workspace_bytes(x, y) >= q.Rope(64).workspace_bytes(x) >= 512
+    assert q.Rope(72).workspace_bytes(x, y) == 0      # refused: more features than the head has
+
+
 def test_binding_refuses_before_the_library():
     x, y = torch.empty(3, 4, 64, dtype=torch.bfloat16), torch.empty(3, 2, 64, dtype=torch.bfloat16)
     r, pos = q.Rope(64), torch.zeros(3, dtype=torch.int64)

@@ -161,7 +161,7 @@ def test_two_graphs_share_a_workspace():
         q, seqs = r(nq, 4, d), nf4.AttnSeqs([(0, nq, 0, nk)])
         o, want = torch.zeros_like(q), torch.zeros_like(q)
         nf4.qlora_attn_kv4_fwd(seqs, q, k4, v4, want)
-        assert seqs._need4[2] > 0
+        assert seqs.workspace_bytes(q, k4) > 0
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             nf4.qlora_attn_kv4_fwd(seqs, q, k4, v4, o, ws=ws)

@@ -682,6 +682,8 @@ int qlora_attn_bwd(const qlora_attn_config* cfg, int64_t count, const qlora_attn
   }
 }
 
+}  // extern "C"
+
 // ---- rotary positions and head norms
 namespace {
 
@@ -760,6 +762,8 @@ bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0
 
 }  // namespace
 
+extern "C" {
+
 int qlora_rope_fwd(const qlora_rope_config* cfg, const double* inv_freq, const int64_t* positions,
                    const qlora_attn_tensor* q, const qlora_attn_tensor* k, const uint16_t* q_weight,
                    const uint16_t* k_weight, const qlora_attn_tensor* q_out, const qlora_attn_tensor* k_out,
@@ -811,6 +815,8 @@ int qlora_rope_bwd(const qlora_rope_config* cfg, const double* inv_freq, const i
   a.dk = rope_tensor(dk);
   return from_hip(nf4::launch_rope_bwd(a, dq_weight, dk_weight, accumulate, static_cast<float*>(ws), stream));
 }
+
+}  // extern "C"
 
 // ---- keys and values in 4 bits
 namespace {
@@ -885,6 +891,8 @@ int check_kv4_rows(const qlora_attn_config* c, int64_t count, const qlora_attn_s
 }
 
 }  // namespace
+
+extern "C" {
 
 int qlora_kv4_write(const qlora_attn_config* cfg, int64_t count, const qlora_attn_seq* seqs, const qlora_attn_tensor* k,
                     const qlora_attn_tensor* v, const qlora_kv4* k4, const qlora_kv4* v4, hipStream_t stream) {

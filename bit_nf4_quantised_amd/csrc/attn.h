@@ -319,14 +319,15 @@ inline std::vector<AttnSeq> by_work(const AttnSeq* seqs, int64_t count, bool key
 }
 
 // The sequences of one launch from v[from] on, `tiles_of(seq)` workgroup tiles each and `per_tile` workgroups a
-// tile: up to kAttnSeqs, and no more workgroups than a launch holds. One sequence alone always fits (the entry
-// points refuse those that do not).
+// tile: up to kAttnSeqs, and no more workgroups than a launch holds (`most`; by default those of 256 threads). One
+// sequence alone always fits (the entry points refuse those that do not).
 template <typename F>
-inline AttnSeqs pack_seqs(const std::vector<AttnSeq>& v, size_t from, int64_t per_tile, F tiles_of) {
+inline AttnSeqs pack_seqs(const std::vector<AttnSeq>& v, size_t from, int64_t per_tile, F tiles_of,
+                          int64_t most = kAttnGroups) {
   AttnSeqs q{};
   for (size_t i = from; i < v.size() && q.count < kAttnSeqs; ++i) {
     const int64_t end = q.first[q.count] + (int64_t)tiles_of(v[i]);
-    if (q.count && end * per_tile > kAttnGroups) break;
+    if (q.count && end * per_tile > most) break;
     q.seq[q.count] = v[i];
     q.first[q.count + 1] = (int)end;
     ++q.count;

@@ -799,7 +799,12 @@ int qlora_rope_bwd(const qlora_rope_config* cfg, const double* inv_freq, const i
       (st = check_rope_pair(cfg, dq_out, dk_out, false)) || (st = check_rope_pair(cfg, dq, dk, true)))
     return st;
   if ((dq_weight && !q_weight) || (dk_weight && (!k_weight || !keys))) return NF4_ERR_NULL;
-  if (cfg->tokens == 0) return NF4_OK;
+  if (cfg->tokens == 0) {   // the weights' gradients are sums of nothing
+    if (accumulate || !(dq_weight || dk_weight)) return NF4_OK;
+    if (!aligned16(dq_weight) || !aligned16(dk_weight)) return NF4_ERR_ALIGN;
+    if (dq_weight == dk_weight) return NF4_ERR_SHAPE;
+    return from_hip(nf4::launch_rope_no_dw(cfg->d, dq_weight, dk_weight, stream));
+  }
   if (cfg->rot && !positions) return NF4_ERR_NULL;
   if (!aligned8(positions) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(dq_weight) || !aligned16(dk_weight) ||
       !aligned16(ws))

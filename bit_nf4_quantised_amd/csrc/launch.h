@@ -241,6 +241,8 @@ hipError_t launch_rope_fwd(const RopeArgs& a, hipStream_t stream);
 // dqw, dkw: [d] or null; part holds rope_bwd_ws_floats floats where one is asked for
 size_t rope_bwd_ws_floats(RopeArgs a);
 hipError_t launch_rope_bwd(const RopeArgs& a, float* dqw, float* dkw, int accumulate, float* part, hipStream_t stream);
+// zeros: dqw, dkw of no tokens
+hipError_t launch_rope_no_dw(int d, float* dqw, float* dkw, hipStream_t stream);
 
 // ---- Keys and values in 4 bits (kv4.hip, attn_kv4.hip; format in kv4.h). Block b of (token, head) is block
 // token * token + head * head + b of the arrays.

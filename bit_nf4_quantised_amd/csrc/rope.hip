@@ -321,6 +321,13 @@ static void rope_bwd(RopeArgs a, float* part, hipStream_t stream) {
   else hipLaunchKernelGGL((rope_bwd_kernel<16, INTER, NORM, DW>), grid, dim3(256), 0, stream, a, part);
 }
 
+static hipError_t rope_dw(const float* part, int q_groups, int groups, int d, float* dqw, float* dkw, int accumulate, hipStream_t stream) {
+  hipLaunchKernelGGL(rope_dw_kernel, dim3((unsigned)(d / 8), 2), dim3(1024), 0, stream, part, q_groups, groups, d, dqw, dkw, accumulate);
+  return hipGetLastError();
+}
+
+hipError_t launch_rope_no_dw(int d, float* dqw, float* dkw, hipStream_t stream) { return rope_dw(nullptr, 0, 0, d, dqw, dkw, 0, stream); }
+
 hipError_t launch_rope_bwd(const RopeArgs& args, float* dqw, float* dkw, int accumulate, float* part, hipStream_t stream) {
   const RopeArgs& a = args;
   const bool norm = a.qw || a.kw, dw = dqw || dkw;
@@ -337,8 +344,7 @@ hipError_t launch_rope_bwd(const RopeArgs& args, float* dqw, float* dkw, int acc
   if (e != hipSuccess || !dw) return e;
   RopeArgs p = a;
   const int groups = rope_plan(p, true);
-  hipLaunchKernelGGL(rope_dw_kernel, dim3((unsigned)(a.d / 8), 2), dim3(1024), 0, stream, part, p.q_groups, groups, a.d, dqw, dkw, accumulate);
-  return hipGetLastError();
+  return rope_dw(part, p.q_groups, groups, a.d, dqw, dkw, accumulate, stream);
 }
 
 }  // namespace nf4

@@ -477,7 +477,7 @@ typedef struct {
   int32_t interleaved;
   float eps;                 /* >= 0 */
   float factor;              /* on the rotated features, finite; 1 for most models */
-  int64_t tokens;            /* 0: a no-op */
+  int64_t tokens;            /* 0: nothing to do but the backward's weights' gradients, which are zero */
 } qlora_rope_config;
 /* Forward.
  *   inv_freq     HOST array of rot / 2 angles a position, in radians, finite (may be NULL with rot 0).
@@ -495,7 +495,7 @@ int qlora_rope_fwd(const qlora_rope_config *cfg, const double *inv_freq, const i
  * n = x rsqrt(mean(x^2) + eps),
  *   dq, dk = rsqrt(mean(x^2) + eps) (weight g - n mean(weight g n)), or g without a weight;
  *   dq_weight, dk_weight [d] float = sum over tokens and heads of g n, or NULL (a frozen weight);
- *     accumulate adds into them.
+ *     accumulate adds into them (without it they are written in every call, with zeros for no tokens).
  *   q, k: the forward's inputs; read, and needed, only where the heads are normed (else they may be NULL).
  *   dq and dk may be the memory of dq_out and dk_out, or of q and k, with the same strides.
  *   ws: with dq_weight or dk_weight, at least qlora_rope_workspace_bytes(cfg) bytes.

@@ -172,6 +172,14 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
 
+// What a wave's lanes wrote to LDS before is read by its other lanes after. The hardware keeps a wave's LDS accesses in order, so
+// this is no instruction: it keeps the compiler, which sees one lane, from passing a read of another address over the write.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // Workgroup barrier after the wave's LDS accesses complete. Written as inline asm so that the
 // compiler does not add a wait for every LDS-DMA load in flight (it cannot tell that those target
 // stages nobody reads before the next barrier); code that needs a DMA landed waits for it with

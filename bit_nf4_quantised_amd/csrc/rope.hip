@@ -288,7 +288,7 @@ __global__ __launch_bounds__(1024) void rope_dw_kernel(const float* part, int q_
 #pragma unroll
   for (int k = 0; k < 16; ++k) v += s[16 * slice + k][x];
   s[16 * slice][x] = v;
-  __builtin_amdgcn_wave_barrier();   // the first wave alone is left: its writes come before its reads
+  wave_lds_order();   // the first wave alone is left
   if (slice) return;
   v = 0.f;
 #pragma unroll

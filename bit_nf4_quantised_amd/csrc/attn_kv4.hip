@@ -253,7 +253,9 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(cons
         for (int r = 0; r < NR; ++r) sc[r][i] = mfma16(kf, qf[r][t], t ? sc[r][i] : f32x4{0.f, 0.f, 0.f, 0.f});
       }
     }
+    wave_lds_order();   // the last tile's values have been read
     now.template values<Deq>(vt, tables, a, lane);
+    wave_lds_order();
     // some row does not see some key
     if (j + BN > first.hi || j < last.lo) {
 #pragma unroll
@@ -286,6 +288,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(cons
   }
 
   // join the waves: each leaves its statistics and sums, which are scaled to the common maximum and added in wave order
+  wave_lds_order();   // its tile has been read
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     const float l = quarter_sum(acc[r].l);

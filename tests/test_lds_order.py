@@ -23,7 +23,7 @@ def _functions(source, folder):
 
 
 @pytest.mark.slow
-@pytest.mark.parametrize("source,kernel,exchanges", [("rope.hip", "rope_dw_kernel", 1)])
+@pytest.mark.parametrize("source,kernel,exchanges", [("rope.hip", "rope_dw_kernel", 1), ("attn_kv4.hip", "attn_kv4_few_kernel", 3)])
 def test_exchanges_between_lanes_are_fenced(source, kernel, exchanges, tmp_path):
     found = {n: body for n, body in _functions(source, tmp_path).items() if kernel in n}
     assert found

@@ -1,6 +1,7 @@
 """Plans of attention over a 4-bit cache: every launch fits, whatever the kernel's workgroups are. No kernel runs here."""
 import pytest
 
+from kv4_cases import CASES, name_of, sequences
 from plan_helpers import Kv4Plans
 
 THREADS = (1 << 32) - 1     # of a launch
@@ -29,3 +30,15 @@ def test_every_launch_fits(plan, heads, kv, nq, nk):
         return
     for p in plan([(nq * i, nq, 0, nk) for i in range(130)], heads, kv, 128):
         assert p["threads"] <= THREADS and p["groups"] < 1 << 31
+
+
+@pytest.mark.parametrize("case", CASES, ids=name_of)
+def test_cases_take_the_kernels_that_they_are_for(plan, case):
+    few, many = plan(sequences(case), case.heads, case.kv, case.d, case.book, case.window)
+    taken = few if case.nq * case.heads // case.kv <= 32 else many
+    assert (taken["kernel"], taken["several"] > 0) == (case.kernel, case.several)
+
+
+def test_cases_cover_every_kernel():
+    have = {(c.kernel, c.d <= 64, c.book == "fp4", c.several) for c in CASES}
+    assert len(have) == 4 * 2 * 2 * 2

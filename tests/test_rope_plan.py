@@ -54,3 +54,11 @@ def test_every_number_of_heads_fills_the_grid(plan, tokens, heads, kv, d, sums):
         assert n <= most and (n >= most - 1 or n - q == want_k)
         # shares by the heads; the keys take what is left
         assert abs(q - most * heads / (heads + kv)) <= 1
+
+
+def test_where_groups_go_on_to_further_tokens(plan):
+    """The sizes of the GPU test of it."""
+    q, k = 54613, 10923
+    assert plan(450000, 5, 1, 128, False) == (q + k, q, 4) and q * 16 < 2 * 450000 and k * 16 < 450000
+    q, k = 3413, 683
+    assert plan(450000, 5, 1, 128, True) == (q + k, q, 8) and q * 16 < 450000 and k * 16 < 450000

@@ -9,9 +9,10 @@
 //
 // The nearest code to x is decided exactly, ties to the lower code, by an approximate quotient (2^-22, relative): x and
 // absmax have 8 significant bits, and a quotient of two such numbers is a tie or well away from one.
-//   NF4   no quotient is within 2.1e-7 of a midpoint (checked over all of them; the test suite repeats it), and the
-//         comparison is good to 1.3e-7: y = 16 x / absmax + 16, whose whole part is a bin of width 1/16 that
-//         holds one midpoint at most; a table in LDS gives the number of midpoints below the bin and the one in it.
+//   NF4   no quotient is within 2.1e-7 of a midpoint, and the comparison is good to 1.3e-7 there (the midpoint 0.0398);
+//         none is within 2.9e-7 of another, where it is good to 2.3e-7 (the test suite checks all of them):
+//         y = 16 x / absmax + 16, whose whole part is a bin of width 1/16 that holds one midpoint at most; a table in LDS
+//         gives the number of midpoints below the bin and the one in it.
 //   INT4  ceil(7 x / absmax - 1/2 - 1e-5), which a tie passes downwards: other quotients are 1e-4 away from one.
 //   FP4   the hardware's conversion of 6 x / absmax, of which 1e-5 of its magnitude is taken away first, so that a
 //         tie falls to the lower code; other quotients are 1e-4 away, relative. -0 becomes 0.

@@ -346,7 +346,8 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void attn_kv4_few_kernel(cons
 // tokens each on 4096 and 1911 keys, 32 heads over 8, d 128, NF4, take 77 to 79 us (590 TFLOP/s; the vector unit and the matrix
 // unit are busy 54 and 37 % of the cycles of the units at work). With 4 waves, of which two workgroups fit a unit, 95:
 // twice the codes. Waves that form codes before and after their products in turn 86; products of both key halves in
-// turn, and priority for them: no gain.
+// turn, and priority for them: no gain. Every row tile dequantises its keys again: 8191 tokens on as many keys take 570 us, and 517
+// if the cache is read back once (11) and attended to in bf16; 512 tokens on 8191 keys 89, and 109 so.
 template <int DP, int WV>
 struct Kv4Many {
   static constexpr int UNITS = 64 * (DP / 32) * 2, N = (UNITS + WV * 64 - 1) / (WV * 64);   // blocks of a tile, and of a thread
